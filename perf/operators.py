@@ -1,0 +1,526 @@
+"""The serving operators around the expert layer: what is measured, and their plain forms.
+
+A decoder layer's step has an attention half before the expert half.  This
+file lists cases of its operators over a paged key-value cache and of the
+4-bit products around them:
+
+  decode   attention of one new token per sequence over the paged cache
+  prompt   causal attention of the new tokens of several prompts over the
+           cache, with a sliding window and a few first tokens kept visible
+  append   new keys and values into the pages (rounded to e4m3 where the
+           cache holds 8 bits)
+  pages    forking, freeing and compacting the pages themselves
+  w4       y = x W^T with 4-bit codes, group scales and zero points
+
+``own`` false: the plain forms, in elementary torch operations in 32 bits;
+true: the calls of the package.  ``exact`` computes the results in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "e4m3": torch.float8_e4m3fn}
+E4M3_MAX = 448.0
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+
+def attention_case(kind, name=None, *, batch, q_heads, kv_heads, head_dim, page, longest, new=1,
+                   window=0, sinks=0, dtype="bf16", cache=None):
+    """`longest`: tokens of the longest sequence, the new ones among them; the
+    others are spread between a sixteenth of it and all of it.  `new`: new
+    tokens of the longest prompt (1: decode).  window 0: none."""
+    c = {"kind": kind, "batch": batch, "q_heads": q_heads, "kv_heads": kv_heads,
+         "head_dim": head_dim, "page": page, "longest": longest, "new": new, "window": window,
+         "sinks": sinks, "dtype": dtype, "cache": cache or dtype}
+    return {"name": name, **c} if name else c
+
+
+def append_case(name=None, *, batch, kv_heads, head_dim, page, longest, new=1, dtype="bf16",
+                cache=None):
+    c = {"kind": "append", "batch": batch, "kv_heads": kv_heads, "head_dim": head_dim,
+         "page": page, "longest": longest, "new": new, "dtype": dtype, "cache": cache or dtype}
+    return {"name": name, **c} if name else c
+
+
+def pages_case(op, name=None, *, layers, seqs, kv_heads, head_dim, page, longest, dtype="bf16"):
+    """fork: half of the sequences are forked into the other half, whose
+    former contents are freed first.  compact: the pool has as many free
+    pages, spread over it, as live ones, and the live ones move together."""
+    c = {"kind": "pages", "op": op, "layers": layers, "seqs": seqs, "kv_heads": kv_heads,
+         "head_dim": head_dim, "page": page, "longest": longest, "dtype": dtype}
+    return {"name": name, **c} if name else c
+
+
+def w4_case(name=None, *, tokens, k, n, group, zeros, dtype="bf16"):
+    c = {"kind": "w4", "tokens": tokens, "k": k, "n": n, "group": group, "zeros": zeros,
+         "dtype": dtype}
+    return {"name": name, **c} if name else c
+
+
+def listed():
+    return [
+        # one token of one request on one tensor-parallel rank of eight: latency
+        attention_case("decode", "decode_b1_share", batch=1, q_heads=7, kv_heads=1, head_dim=128,
+                       page=16, longest=1500),
+        # a full decode batch of unequal conversations on an 8-bit cache
+        attention_case("decode", "decode_b64_e4m3", batch=64, q_heads=56, kv_heads=8,
+                       head_dim=128, page=64, longest=8192, cache="e4m3"),
+        # two very long contexts: few rows, the work is along the cache
+        attention_case("decode", "decode_b2_long", batch=2, q_heads=56, kv_heads=8, head_dim=128,
+                       page=64, longest=131072),
+        # a few mid-sized prompts, one with an odd tail, in a windowed layer
+        attention_case("prompt", "prompt_b3_window", batch=3, q_heads=14, kv_heads=2,
+                       head_dim=128, page=16, longest=2031, new=2031, window=512, sinks=4),
+        # the last chunk of a long prompt on one rank
+        attention_case("prompt", "prompt_8k_window", batch=1, q_heads=14, kv_heads=2,
+                       head_dim=128, page=64, longest=8192, new=8192, window=4096, sinks=16),
+        # one decode step's keys and values into an 8-bit cache: latency
+        append_case("append_b64_e4m3", batch=64, kv_heads=8, head_dim=128, page=64, longest=1024,
+                    cache="e4m3"),
+        # whole prompts into the cache
+        append_case("append_prompts", batch=4, kv_heads=8, head_dim=128, page=64, longest=8000,
+                    new=8000),
+        # sampling several continuations of each of a few prompts: latency
+        pages_case("fork", "fork_32", layers=2, seqs=64, kv_heads=2, head_dim=128, page=16,
+                   longest=500),
+        # a fragmented pool pulled together
+        pages_case("compact", "compact_pool", layers=4, seqs=64, kv_heads=8, head_dim=128,
+                   page=64, longest=1000),
+        # fused query, key and value rows of one rank of eight, one token
+        w4_case("w4_share_b1", tokens=1, k=7168, n=1152, group=128, zeros=False),
+        # the whole layer's query, key and value rows, a small batch
+        w4_case("w4_qkv_b8", tokens=8, k=7168, n=9216, group=64, zeros=True),
+        # output rows, the largest decode batch
+        w4_case("w4_out_b64", tokens=64, k=7168, n=7168, group=128, zeros=True, dtype="fp16"),
+    ]
+
+
+def draw(rng):
+    def logint(lo, hi):
+        return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+    def heads():
+        kv = rng.choice((1, 2, 4, 8))
+        return kv, kv * rng.choice((1, 2, 3, 5, 7, 8, 16) if kv <= 2 else (1, 4, 7, 8))
+
+    kind = rng.choice(("decode", "decode", "prompt", "append", "pages", "w4", "w4"))
+    dtype = rng.choice(("bf16", "bf16", "fp16"))
+    page = rng.choice((16, 32, 64, 128))
+    d = rng.choice((64, 96, 128, 128, 192, 256))
+    if kind == "decode":
+        kv, q = heads()
+        batch = logint(1, 64)
+        longest = logint(64, min(131072, (1 << 29) // (batch * kv * d)))
+        window = rng.choice((0, 0, logint(16, 8192)))
+        return attention_case(kind, batch=batch, q_heads=q, kv_heads=kv, head_dim=d, page=page,
+                              longest=longest, window=window,
+                              sinks=rng.randint(1, 32) if window else 0, dtype=dtype,
+                              cache=rng.choice((dtype, dtype, "e4m3")))
+    if kind == "prompt":
+        kv = rng.choice((1, 2))
+        q = kv * rng.choice((1, 2, 4, 7))
+        new = logint(100, 8192)
+        batch = rng.randint(1, max(1, min(4, (1 << 24) // (new * new))))
+        longest = min(8192, new + rng.choice((0, 0, logint(16, 4096))))
+        window = rng.choice((0, logint(16, 4096), logint(16, 4096)))
+        if new > 4096:
+            q, batch, d = min(q, 4) // kv * kv, 1, min(d, 128)
+        return attention_case(kind, batch=batch, q_heads=q, kv_heads=kv, head_dim=d, page=page,
+                              longest=longest, new=new, window=window,
+                              sinks=rng.randint(1, 32) if window else 0, dtype=dtype,
+                              cache=rng.choice((dtype, dtype, "e4m3")))
+    if kind == "append":
+        batch = logint(1, 64)
+        kv = rng.choice((1, 2, 4, 8))
+        new = rng.choice((1, logint(2, max(2, min(8000, (1 << 24) // (batch * kv * d))))))
+        return append_case(batch=batch, kv_heads=kv, head_dim=d, page=page,
+                           longest=new + rng.randint(0, 500), new=new, dtype=dtype,
+                           cache=rng.choice((dtype, "e4m3")))
+    if kind == "pages":
+        return pages_case(rng.choice(("fork", "compact")), layers=rng.randint(1, 4),
+                          seqs=2 * logint(1, 32), kv_heads=rng.choice((1, 2, 4)), head_dim=d,
+                          page=page, longest=logint(50, 1000), dtype=dtype)
+    return w4_case(tokens=logint(1, 64), k=128 * logint(4, 56), n=logint(300, 9216),
+                   group=rng.choice((32, 64, 128)), zeros=rng.choice((False, True)), dtype=dtype)
+
+
+# ---------------------------------------------------------------------------
+# Inputs
+# ---------------------------------------------------------------------------
+
+def _spread(longest, n, least=1):
+    """n lengths, evenly spread from the longest down to a sixteenth of it:
+    the same ones for every seed, which only orders them."""
+    return [max(least, round(longest * (1 - 15 / 16 * i / n))) for i in range(n)]
+
+
+def _sizes(case):
+    """(lengths, new tokens) of the case's sequences, unordered."""
+    kind = case["kind"]
+    n = case["seqs"] if kind == "pages" else case["batch"]
+    lengths = _spread(case["longest"], n)
+    if kind in ("prompt", "append"):
+        new, past = _spread(case["new"], n), _spread(case["longest"] - case["new"], n, 0)
+        return [a + b for a, b in zip(new, past)], new
+    if kind == "decode" and n > 4:
+        lengths[-1] = 0  # a slot of the batch that no request holds
+    return lengths, [1] * n
+
+
+def _cache(case, gen, seed, lengths, layers=1, spare=0):
+    """A pool of random pages, and tables that hold them in random order."""
+    page, kv, d = case["page"], case["kv_heads"], case["head_dim"]
+    need = (lengths + page - 1) // page
+    used = int(need.sum())
+    pages = used + max(1, spare)
+    order = torch.randperm(pages, generator=gen)[:used].to(torch.int32)
+    tables = torch.full((len(lengths), int(need.max()) + 1), -1, dtype=torch.int32)
+    col = torch.arange(tables.shape[1])
+    tables[col[None, :] < need[:, None]] = order
+    refs = torch.zeros(pages, dtype=torch.int32)
+    refs[order.long()] = 1
+    cuda = torch.Generator("cuda").manual_seed(seed)
+    kind = DTYPES[case.get("cache", case["dtype"])]
+    base = DTYPES[case["dtype"]]
+    data = torch.empty((layers, 2, pages, kv, page, d), dtype=kind, device="cuda")
+    shape = (pages, kv, page, d)
+    for i in range(layers):
+        for j in range(2):
+            data[i, j] = torch.randn(shape, generator=cuda, device="cuda", dtype=base).to(kind)
+    scales = None
+    if kind == torch.float8_e4m3fn:
+        scales = [(0.5 + torch.rand(kv, generator=gen)).cuda() for _ in range(2)]
+    return {"data": data, "tables": tables.cuda(), "lengths": lengths.to(torch.int32).cuda(),
+            "refs": refs.cuda(), "k_scale": scales and scales[0], "v_scale": scales and scales[1],
+            "cuda": cuda}
+
+
+def _inputs(case, seed):
+    gen = torch.Generator().manual_seed(seed)
+    dtype = DTYPES[case["dtype"]]
+    kind = case["kind"]
+    if kind == "w4":
+        cuda = torch.Generator("cuda").manual_seed(seed)
+        t, k, n, g = case["tokens"], case["k"], case["n"], case["group"]
+        s = {"x": torch.randn((t, k), generator=cuda, device="cuda", dtype=dtype),
+             "codes": torch.randint(0, 256, (n, k // 2), generator=cuda, device="cuda",
+                                    dtype=torch.uint8),
+             "scales": (0.001 + 0.01 * torch.rand((n, k // g), generator=cuda,
+                                                  device="cuda")).to(dtype),
+             "zeros": None}
+        if case["zeros"]:
+            s["zeros"] = torch.randint(4, 12, (n, k // g), generator=cuda, device="cuda",
+                                       dtype=torch.uint8)
+        return s
+    lengths, new = (torch.tensor(v) for v in _sizes(case))
+    order = torch.randperm(len(lengths), generator=gen)
+    lengths, new = lengths[order], new[order]
+    if kind == "pages":
+        half = case["seqs"] // 2
+        page = case["page"]
+        s = _cache(case, gen, seed, lengths, case["layers"],
+                   spare=case["seqs"] if case["op"] == "fork"
+                   else int(((lengths + page - 1) // page).sum()))
+        s["parents"] = torch.randint(0, half, (half,), generator=gen).to(torch.int32).cuda()
+        s["children"] = torch.arange(half, 2 * half, dtype=torch.int32).cuda()
+        return s
+    s = _cache(case, gen, seed, lengths)
+    tokens = int(new.sum())
+    s["cu"] = torch.cat([torch.zeros(1, dtype=torch.long), new.cumsum(0)]).to(torch.int32).cuda()
+    s["max_new"] = int(new.max())
+    if kind == "append":
+        for name in ("k", "v"):
+            s[name] = 2 * torch.randn((tokens, case["kv_heads"], case["head_dim"]),
+                                      generator=s["cuda"], device="cuda", dtype=dtype)
+    else:
+        s["q"] = 2 * torch.randn((tokens, case["q_heads"], case["head_dim"]),
+                                 generator=s["cuda"], device="cuda", dtype=dtype)
+    return s
+
+
+def prepare(case, seed):
+    s = {"case": case, **_inputs(case, seed)}
+    if case["kind"] == "pages" and case["op"] == "compact":
+        s["new_tables"], s["new_refs"] = torch.empty_like(s["tables"]), torch.empty_like(s["refs"])
+    if own:
+        from sparse_moe_decode_router_amd import attention, w4
+        if case["kind"] == "w4":
+            s["linear"] = w4.W4Linear(s["codes"], s["scales"], s["zeros"])
+        else:
+            s["kv"] = attention.PagedKV(s["data"], s["tables"], s["lengths"], s["refs"],
+                                        k_scale=s["k_scale"], v_scale=s["v_scale"])
+        if case["kind"] in ("decode", "prompt"):
+            s["attn"] = attention.PagedAttention(s["kv"], case["q_heads"], case["batch"],
+                                                 case["longest"], window=case["window"],
+                                                 sinks=case["sinks"])
+    return s
+
+
+# ---------------------------------------------------------------------------
+# Plain forms
+# ---------------------------------------------------------------------------
+
+def _gathered(s, which):
+    """[B][kv_heads][N][D] f32: each sequence's keys or values in order."""
+    c = s["case"]
+    t = s["tables"].clamp(min=0).long()
+    x = s["data"][0, which][t].float()                   # [B][P][kv][page][D]
+    x = x.transpose(1, 2).flatten(2, 3)                  # [B][kv][P * page][D]
+    scale = s["k_scale"] if which == 0 else s["v_scale"]
+    return x if scale is None else x * scale[None, :, None, None]
+
+
+def plain_attention(s):
+    """out = softmax(scale q K^T over the visible positions) V, per query row;
+    a row that sees nothing gives zeros, and -inf as its log-sum."""
+    c = s["case"]
+    q, cu, lengths = s["q"], s["cu"].long(), s["lengths"].long()
+    n_new = cu[1:] - cu[:-1]
+    most = s["max_new"]
+    at = torch.arange(most, device="cuda")[None, :]
+    row = (cu[:-1, None] + at).clamp(max=q.shape[0] - 1)             # [B][Q]
+    kv, d = c["kv_heads"], c["head_dim"]
+    qs = q[row].float().unflatten(2, (kv, -1)).permute(0, 2, 3, 1, 4)  # [B][kv][G][Q][D]
+    group = qs.shape[2]
+    k = _gathered(s, 0)
+    score = torch.matmul(qs.flatten(2, 3) * d ** -0.5, k.transpose(2, 3)).unflatten(2, (group, most))
+    pos = (lengths - n_new)[:, None] + at                             # [B][Q]
+    t = torch.arange(k.shape[2], device="cuda")
+    sees = (t <= pos[..., None]) & (t < lengths[:, None, None])
+    if c["window"]:
+        sees &= (t > pos[..., None] - c["window"]) | (t < c["sinks"])
+    score = score.masked_fill_(~sees[:, None, None], -math.inf)
+    top = score.amax(-1, keepdim=True)
+    p = torch.exp(score.sub_(top.clamp(min=-3e38)))
+    total = p.sum(-1, keepdim=True)
+    v = _gathered(s, 1).masked_fill_(~(t < lengths[:, None])[:, None, :, None], 0.0)
+    out = torch.matmul(p.flatten(2, 3), v).unflatten(2, (group, most))
+    out = torch.where(total > 0, out / total, 0.0)
+    lse = torch.where(total > 0, top + torch.log(total), -math.inf)[..., 0]
+    real = at < n_new[:, None]                                        # rows that exist
+    out = out.permute(0, 3, 1, 2, 4).flatten(2, 3)[real].to(q.dtype)
+    return out, lse.permute(0, 3, 1, 2).flatten(2, 3)[real]
+
+
+def plain_append(s):
+    c = s["case"]
+    cu = s["cu"].long()
+    tokens = torch.arange(s["k"].shape[0], device="cuda")
+    seq = torch.bucketize(tokens, cu[1:], right=True)
+    pos = s["lengths"].long()[seq] - cu[seq + 1] + tokens
+    page = s["tables"].long()[seq, pos // c["page"]]
+    data = s["data"]
+    k, v = s["k"].float(), s["v"].float()
+    if s["k_scale"] is not None:
+        k = (k / s["k_scale"][None, :, None]).clamp(-E4M3_MAX, E4M3_MAX)
+        v = (v / s["v_scale"][None, :, None]).clamp(-E4M3_MAX, E4M3_MAX)
+    raw = data.view(torch.uint8) if s["k_scale"] is not None else data
+    raw[0, 0, page, :, pos % c["page"]] = k.to(data.dtype).view(raw.dtype)
+    raw[0, 1, page, :, pos % c["page"]] = v.to(data.dtype).view(raw.dtype)
+    return data
+
+
+def plain_free(s, seqs):
+    rows = s["tables"][seqs]
+    s["refs"].index_add_(0, rows.clamp(min=0).flatten().long(), -(rows >= 0).int().flatten())
+    s["tables"][seqs] = -1
+    s["lengths"][seqs] = 0
+
+
+def plain_fork(s, parents, children):
+    page, refs, tables = s["case"]["page"], s["refs"], s["tables"]
+    length = s["lengths"][parents]
+    full, part = length // page, length % page > 0
+    free = torch.argsort((refs != 0).int(), stable=True)  # the lowest free page first
+    new = free[(part.int().cumsum(0) - 1).clamp(min=0)].int()
+    col = torch.arange(tables.shape[1], device="cuda")[None, :]
+    rows = tables[parents]
+    shared, tail = col < full[:, None], (col == full[:, None]) & part[:, None]
+    refs.index_add_(0, rows.clamp(min=0).flatten().long(), shared.int().flatten())
+    refs.index_add_(0, new.long(), part.int())
+    tables[children] = torch.where(shared, rows, torch.where(tail, new[:, None], -1))
+    s["lengths"][children] = length
+    src = rows.gather(1, full[:, None].long())[:, 0]
+    s["data"][:, :, new[part].long()] = s["data"][:, :, src[part].long()]
+
+
+def plain_compact(s):
+    refs, tables = s["refs"], s["tables"]
+    pages = torch.arange(len(refs), device="cuda")
+    live = refs > 0
+    n_live = live.sum()
+    holes, moved = pages[~live & (pages < n_live)], pages[live & (pages >= n_live)]
+    to = pages.clone()
+    to[moved] = holes
+    s["data"][:, :, holes] = s["data"][:, :, moved]
+    s["new_tables"].copy_(torch.where(tables >= 0, to[tables.clamp(min=0).long()].int(), tables))
+    s["new_refs"].copy_(torch.where(pages < n_live, 0, refs))
+    s["new_refs"][to[live]] = refs[live]
+    return s["new_tables"], s["new_refs"]
+
+
+def plain_w4(s):
+    codes, group = s["codes"], s["case"]["group"]
+    q = torch.stack([codes & 15, codes >> 4], -1).flatten(1).float()   # low half: even columns
+    q = q.unflatten(1, (-1, group))
+    q = q - (8.0 if s["zeros"] is None else s["zeros"].float()[..., None])
+    w = (q * s["scales"].float()[..., None]).flatten(1)
+    return (s["x"].float() @ w.t()).to(s["x"].dtype)
+
+
+def run(state):
+    s = state
+    kind = s["case"]["kind"]
+    if kind == "decode":
+        return s["attn"].decode(0, s["q"]) if own else plain_attention(s)
+    if kind == "prompt":
+        if own:
+            return s["attn"].prompt(0, s["q"], s["cu"], s["max_new"])
+        return plain_attention(s)
+    if kind == "append":
+        if not own:
+            return plain_append(s)
+        s["kv"].append(0, s["k"], s["v"], cu=s["cu"] if s["case"]["new"] > 1 else None)
+        return s["data"]
+    if kind == "w4":
+        return s["linear"](s["x"]) if own else plain_w4(s)
+    if s["case"]["op"] == "fork":
+        if own:
+            s["kv"].free(s["children"])
+            s["kv"].fork(s["parents"], s["children"])
+        else:
+            plain_free(s, s["children"])
+            plain_fork(s, s["parents"], s["children"])
+        return s["data"], s["tables"], s["lengths"], s["refs"]
+    if own:
+        s["kv"].compact(out=(s["new_tables"], s["new_refs"]))
+    else:
+        plain_compact(s)
+    return s["data"], s["new_tables"], s["new_refs"]
+
+
+# ---------------------------------------------------------------------------
+# What a pass cannot do without
+# ---------------------------------------------------------------------------
+
+def work(case):
+    kind = case["kind"]
+    size = lambda name: 1 if name == "e4m3" else 2  # noqa: E731
+    if kind == "w4":
+        t, k, n, g = case["tokens"], case["k"], case["n"], case["group"]
+        return {"bytes": n * k / 2 + n * (k // g) * (3 if case["zeros"] else 2) + 2 * t * (k + n),
+                "flops": 2.0 * t * k * n}
+    lengths, new = _sizes(case)
+    n, tokens, page = len(lengths), sum(new), case.get("page")
+    row = case["kv_heads"] * case["head_dim"]
+    if kind == "append":
+        return {"bytes": 2 * tokens * row * (2 + size(case["cache"])), "flops": 0.0}
+    if kind == "pages":
+        one = 2 * case["layers"] * 2 * row * page * 2     # a page's read and write
+        used = sum(-(-t // page) for t in lengths)
+        tables = 4 * used
+        if case["op"] == "fork":  # the last page of each child, where it is not full
+            return {"bytes": n / 2 * (page - 1) / page * one + 2 * tables, "flops": 0.0}
+        return {"bytes": used / 2 * one + 2 * tables + 16 * used, "flops": 0.0}
+    w, sinks = case["window"], case["sinks"]
+    limit = w + sinks if w else 1 << 40
+
+    def upto(last):
+        """Keys that the queries at positions 0 <= p < last see, min(p + 1, limit) each."""
+        m = min(last, limit)
+        return m * (m + 1) / 2 + (last - m) * limit
+    seen = sum(upto(t) - upto(t - m) for t, m in zip(lengths, new) if t)
+    keys = sum(min(t, limit + m - 1) for t, m in zip(lengths, new))
+    out = tokens * case["q_heads"]
+    return {"bytes": keys * row * 2 * size(case["cache"]) + out * (case["head_dim"] * 4 + 4),
+            "flops": 4.0 * seen * case["q_heads"] * case["head_dim"]}
+
+
+# ---------------------------------------------------------------------------
+# The definitions in 64 bits
+# ---------------------------------------------------------------------------
+
+def _exact_attention(s):
+    c = s["case"]
+    page, kv, d = c["page"], c["kv_heads"], c["head_dim"]
+    group = c["q_heads"] // kv
+    f64 = torch.float64
+    outs, sums = [], []
+    cu, lengths = s["cu"].tolist(), s["lengths"].tolist()
+    for b, n in enumerate(lengths):
+        first, last = cu[b], cu[b + 1]
+        q = s["q"][first:last].to(f64)
+        if n == 0:
+            outs.append(torch.zeros_like(q))
+            sums.append(torch.full(q.shape[:2], -math.inf, dtype=f64, device="cuda"))
+            continue
+        ids = s["tables"][b, :-(-n // page)].long()
+        o, z = torch.empty_like(q), torch.empty(q.shape[:2], dtype=f64, device="cuda")
+        for h in range(kv):
+            keys = s["data"][0, 0, ids, h].reshape(-1, d)[:n].to(f64)
+            vals = s["data"][0, 1, ids, h].reshape(-1, d)[:n].to(f64)
+            if s["k_scale"] is not None:
+                keys, vals = keys * s["k_scale"][h].to(f64), vals * s["v_scale"][h].to(f64)
+            for r0 in range(0, last - first, 1024):
+                r1 = min(r0 + 1024, last - first)
+                rows = torch.arange(n - (last - first) + r0, n - (last - first) + r1, device="cuda")
+                t = torch.arange(n, device="cuda")
+                hidden = t[None, :] > rows[:, None]
+                if c["window"]:
+                    hidden |= (t[None, :] <= rows[:, None] - c["window"]) & (t[None, :] >= c["sinks"])
+                for g in range(h * group, (h + 1) * group):
+                    a = q[r0:r1, g] @ keys.t() / math.sqrt(d)
+                    a[hidden] = -math.inf
+                    z[r0:r1, g] = torch.logsumexp(a, 1)
+                    o[r0:r1, g] = torch.softmax(a, 1) @ vals
+        outs.append(o)
+        sums.append(z)
+    return torch.cat(outs), torch.cat(sums)
+
+
+def _exact_append(s):
+    c = s["case"]
+    data = s["data"].double()
+    cu, lengths, tables = s["cu"].tolist(), s["lengths"].tolist(), s["tables"].tolist()
+    for which, new, scale in ((0, s["k"], s["k_scale"]), (1, s["v"], s["v_scale"])):
+        new = new.double()
+        if scale is not None:
+            new = torch.clamp(new / scale.double()[None, :, None], -E4M3_MAX, E4M3_MAX)
+        for b, n in enumerate(lengths):
+            at, pos = cu[b], n - (cu[b + 1] - cu[b])
+            while pos < n:
+                slot = pos % c["page"]
+                take = min(c["page"] - slot, n - pos)
+                data[0, which, tables[b][pos // c["page"]], :, slot:slot + take] = \
+                    new[at:at + take].transpose(0, 1)
+                at, pos = at + take, pos + take
+    return data
+
+
+def _exact_w4(s):
+    codes = s["codes"].to(torch.int16)
+    n, half = codes.shape
+    w = torch.empty((n, 2 * half), dtype=torch.float64, device="cuda")
+    w[:, 0::2], w[:, 1::2] = (codes % 16).double(), (codes // 16).double()
+    g = s["case"]["group"]
+    zero = torch.full_like(s["scales"], 8, dtype=torch.float64) if s["zeros"] is None else \
+        s["zeros"].double()
+    w -= zero.repeat_interleave(g, 1)
+    w *= s["scales"].double().repeat_interleave(g, 1)
+    return s["x"].double() @ w.t()
+
+
+def exact(case, seed):
+    s = {"case": case, **_inputs(case, seed)}
+    if case["kind"] in ("decode", "prompt"):
+        return _exact_attention(s)
+    if case["kind"] == "append":
+        return _exact_append(s)
+    if case["kind"] == "w4":
+        return _exact_w4(s)
+    return None  # pages are copied, not computed
