@@ -359,7 +359,7 @@ def plain_compact(s):
     to[moved] = holes
     s["data"][:, :, holes] = s["data"][:, :, moved]
     s["new_tables"].copy_(torch.where(tables >= 0, to[tables.clamp(min=0).long()].int(), tables))
-    s["new_refs"].copy_(torch.where(pages < n_live, 0, refs))
+    s["new_refs"].zero_()
     s["new_refs"][to[live]] = refs[live]
     return s["new_tables"], s["new_refs"]
 
