@@ -1,0 +1,237 @@
+"""A paged key-value cache and the attention that reads it.
+
+``PagedKV`` binds the tensors of a cache (the pages of every layer, the
+sequences' page tables and lengths, the pages' reference counts) to the
+library's operators on them:
+
+  append   new keys and values into their pages (converted to e4m3 where the
+           cache holds 8 bits)
+  extend   longer sequences, and pages for them
+  fork     copies of sequences that share their full pages
+  free     sequences given up
+  compact  the pages in use moved together
+
+``PagedAttention`` plans attention over such a cache: ``decode`` for one new
+token per sequence, ``prompt`` for many.  All of it runs on the current stream,
+reads lengths and tables on the device and never waits for it, so calls can be
+captured into a HIP graph.  include/moe_serve.h states layouts and formulas.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from .serving import (DTYPES, AttnConfig, Cache, StreamSpace, check, lib, raw_stream, require,
+                      tensor)
+
+E4M3_MAX = 448.0
+
+
+def _rows(t, name, heads, dim, dtypes, device) -> Tuple[int, int]:
+    """Checks a [tokens][heads][dim] tensor whose rows are contiguous; returns
+    its token and head strides."""
+    require(isinstance(t, torch.Tensor), f"{name}: a tensor is needed, got {type(t).__name__}")
+    require(t.dtype in dtypes, f"{name}: {t.dtype} given, {' or '.join(map(str, dtypes))} needed")
+    require(t.device == device, f"{name}: on {t.device}, not on {device}")
+    shape, stride = t.shape, t.stride()
+    require(len(shape) == 3 and shape[1] == heads and shape[2] == dim,
+            f"{name}: shape {tuple(shape)} given, (tokens, {heads}, {dim}) needed")
+    require(stride[2] == 1 and stride[0] % 8 == 0 and stride[1] % 8 == 0 and
+            (heads == 1 or stride[1] >= dim) and t.data_ptr() % 16 == 0,
+            f"{name}: strides {tuple(stride)}: rows of {dim} contiguous elements, 16-byte aligned, "
+            "are needed")
+    return stride[0], stride[1]
+
+
+class PagedKV:
+    """data [layers, 2, pages, kv_heads, page, head_dim] (bf16, fp16 or e4m3; keys
+    at 0, values at 1), tables [seqs, cols] i32 (-1: no page), lengths [seqs]
+    i32, refs [pages] i32; k_scale, v_scale [kv_heads] f32 for e4m3: a code c
+    stands for c * scale.  The tensors stay the caller's and are changed in
+    place; operations on them are ordered by the stream they run on."""
+
+    def __init__(self, data, tables, lengths, refs, k_scale=None, v_scale=None):
+        tensor(data, "data", tuple(DTYPES))
+        require(data.dim() == 6 and data.shape[1] == 2,
+                f"data: shape {tuple(data.shape)} given, (layers, 2, pages, kv_heads, page, "
+                "head_dim) needed")
+        dev = data.device
+        layers, _, pages, heads, page, dim = data.shape
+        tensor(tables, "tables", torch.int32, device=dev)
+        require(tables.dim() == 2, f"tables: shape {tuple(tables.shape)} given, (seqs, cols) needed")
+        seqs, cols = tables.shape
+        tensor(lengths, "lengths", torch.int32, (seqs,), dev)
+        tensor(refs, "refs", torch.int32, (pages,), dev)
+        f8 = data.dtype == torch.float8_e4m3fn
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                require(f8, f"{name}: only an e4m3 cache has scales")
+                tensor(t, name, torch.float32, (heads,), dev)
+        self.data, self.tables, self.lengths, self.refs = data, tables, lengths, refs
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.device, self.dtype = dev, data.dtype
+        self.layers, self.pages, self.kv_heads, self.page, self.head_dim = \
+            layers, pages, heads, page, dim
+        self.seqs, self.cols = seqs, cols
+        self.compute_dtypes = (torch.bfloat16, torch.float16) if f8 else (data.dtype,)
+        self.flags = torch.zeros(1, dtype=torch.int32, device=dev)
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.struct = Cache(data.data_ptr(), tables.data_ptr(), lengths.data_ptr(),
+                            refs.data_ptr(), ptr(k_scale), ptr(v_scale), self.flags.data_ptr(),
+                            DTYPES[data.dtype], layers, pages, heads, page, dim, seqs, cols)
+        self._ref = ctypes.addressof(self.struct)
+        self._lib = lib()
+        check(self._lib.moe_kv_validate(self._ref), "PagedKV")
+        size = self._lib.moe_kv_scratch_size(self._ref, seqs)
+        self._scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+        self._scratch_ptr = self._scratch.data_ptr()
+
+    @classmethod
+    def empty(cls, layers, pages, kv_heads, page, head_dim, seqs, cols, dtype=torch.bfloat16,
+              device="cuda", k_scale=None, v_scale=None) -> "PagedKV":
+        """A new cache without sequences."""
+        i32 = dict(dtype=torch.int32, device=device)
+        data = torch.zeros((layers, 2, pages, kv_heads, page, head_dim), dtype=torch.uint8 if
+                           dtype == torch.float8_e4m3fn else dtype, device=device).view(dtype)
+        return cls(data, torch.full((seqs, cols), -1, **i32), torch.zeros(seqs, **i32),
+                   torch.zeros(pages, **i32), k_scale, v_scale)
+
+    def _list(self, t, name, n=None) -> int:
+        tensor(t, name, torch.int32, None if n is None else (n,), self.device)
+        require(t.dim() == 1, f"{name}: one dimension is needed")
+        require(t.shape[0] <= self.seqs, f"{name}: {t.shape[0]} entries for {self.seqs} sequences")
+        return t.shape[0]
+
+    def append(self, layer: int, k, v, cu=None) -> None:
+        """Writes keys and values [tokens, kv_heads, head_dim] of new tokens,
+        which the lengths count already.  cu None: token i is sequence i's last
+        position (where it has none, nothing is written); else cu [batch + 1]
+        i32: tokens cu[b] .. cu[b + 1] - 1 are sequence b's last positions."""
+        ts, hs = _rows(k, "k", self.kv_heads, self.head_dim, self.compute_dtypes, self.device)
+        require(_rows(v, "v", self.kv_heads, self.head_dim, (k.dtype,), self.device) == (ts, hs) and
+                v.shape == k.shape, "v: the shape and strides of k are needed")
+        tokens = k.shape[0]
+        if cu is None:
+            batch = tokens
+            require(batch <= self.seqs, f"k: {batch} tokens for {self.seqs} sequences")
+        else:
+            tensor(cu, "cu", torch.int32, device=self.device)
+            batch = cu.numel() - 1
+            require(cu.dim() == 1 and 0 <= batch <= self.seqs,
+                    f"cu: 1 to {self.seqs + 1} entries are needed, got shape {tuple(cu.shape)}")
+        require(0 <= layer < self.layers, f"layer {layer} of {self.layers}")
+        check(self._lib.moe_kv_append(self._ref, layer, k.data_ptr(), v.data_ptr(),
+                                      DTYPES[k.dtype], ts, hs, tokens,
+                                      None if cu is None else cu.data_ptr(), batch,
+                                      raw_stream(self.device)), "append")
+
+    def free(self, seqs) -> None:
+        """Gives up the (distinct) sequences of an i32 list."""
+        n = self._list(seqs, "seqs")
+        check(self._lib.moe_kv_free(self._ref, seqs.data_ptr(), n, raw_stream(self.device)), "free")
+
+    def fork(self, parents, children) -> None:
+        """Sequence children[i], which holds nothing, becomes a copy of
+        parents[i]: full pages are shared, a part-filled last page is copied."""
+        n = self._list(parents, "parents")
+        self._list(children, "children", n)
+        check(self._lib.moe_kv_fork(self._ref, parents.data_ptr(), children.data_ptr(), n,
+                                    self._scratch_ptr, raw_stream(self.device)), "fork")
+
+    def extend(self, counts, seqs=None) -> None:
+        """Lengthens sequences (the first ones, or the distinct ones of the list
+        seqs) by counts[i] positions, with pages for them."""
+        n = self._list(counts, "counts")
+        if seqs is not None:
+            self._list(seqs, "seqs", n)
+        check(self._lib.moe_kv_extend(self._ref, None if seqs is None else seqs.data_ptr(),
+                                      counts.data_ptr(), n, self._scratch_ptr,
+                                      raw_stream(self.device)), "extend")
+
+    def compact(self, out=None) -> None:
+        """Moves the used pages to the front of the pool.  out (tables, refs):
+        where the new tables and references go; None: into the cache's own."""
+        tables, refs = out if out is not None else (self.tables, self.refs)
+        if out is not None:
+            tensor(tables, "out tables", torch.int32, (self.seqs, self.cols), self.device)
+            tensor(refs, "out refs", torch.int32, (self.pages,), self.device)
+        check(self._lib.moe_kv_compact(self._ref, tables.data_ptr(), refs.data_ptr(),
+                                       self._scratch_ptr, raw_stream(self.device)), "compact")
+
+    def read_flags(self) -> int:
+        """Sticky flags (waits for the device): 1 fork or extend found too few
+        free pages, 2 a sequence would have outgrown its table row."""
+        return int(self.flags.item())
+
+
+class PagedAttention:
+    """Attention of q_heads query heads over a PagedKV, for calls of up to
+    `batch` sequences.  longest: positions of the longest sequence to plan for;
+    window and sinks: a row sees the last `window` positions up to its own and
+    the first `sinks` (window 0: all up to its own); scale: of the scores,
+    head_dim^-1/2 unless given."""
+
+    def __init__(self, kv: PagedKV, q_heads: int, batch: int, longest: int, window: int = 0,
+                 sinks: int = 0, scale: Optional[float] = None):
+        self.kv, self.q_heads, self.batch = kv, q_heads, batch
+        self.config = AttnConfig(q_heads, batch, longest, window, sinks,
+                                 kv.head_dim ** -0.5 if scale is None else scale)
+        self._cfg, self._lib = ctypes.addressof(self.config), lib()
+        check(self._lib.moe_attn_validate(kv._ref, self._cfg), "PagedAttention")
+        self._decode = self._space(0)
+        self._prompt = {}
+
+    def _space(self, tokens: int) -> StreamSpace:
+        w, c = ctypes.c_size_t(), ctypes.c_size_t()
+        check(self._lib.moe_attn_workspace(self.kv._ref, self._cfg, tokens, ctypes.byref(w),
+                                           ctypes.byref(c)), "workspace")
+        return StreamSpace(self.kv.device, w.value, c.value)
+
+    def decode(self, layer: int, q):
+        """q [batch, q_heads, head_dim], one new token of each of the first
+        sequences, whose keys and values are in the cache.  Returns (out, like
+        q; lse [batch, q_heads] f32)."""
+        kv = self.kv
+        ts, hs = _rows(q, "q", self.q_heads, kv.head_dim, kv.compute_dtypes, kv.device)
+        batch = q.shape[0]
+        require(1 <= batch <= self.batch, f"q: {batch} sequences, planned for {self.batch}")
+        require(0 <= layer < kv.layers, f"layer {layer} of {kv.layers}")
+        out = torch.empty(q.shape, dtype=q.dtype, device=kv.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=kv.device)
+        stream = raw_stream(kv.device)
+        w, c, _ = self._decode.get(stream)
+        check(self._lib.moe_attn_decode(kv._ref, self._cfg, layer, q.data_ptr(), DTYPES[q.dtype],
+                                        ts, hs, batch, out.data_ptr(), lse.data_ptr(), w, c,
+                                        stream), "decode")
+        return out, lse
+
+    def prompt(self, layer: int, q, cu, max_new: Optional[int] = None):
+        """q [tokens, q_heads, head_dim]; cu [batch + 1] i32: rows cu[b] ..
+        cu[b + 1] - 1 are the last positions of sequence b (at most max_new of
+        them, where it is given).  Returns (out, like q; lse [tokens, q_heads]
+        f32); rows that cu leaves out are not written."""
+        kv = self.kv
+        ts, hs = _rows(q, "q", self.q_heads, kv.head_dim, kv.compute_dtypes, kv.device)
+        tensor(cu, "cu", torch.int32, device=kv.device)
+        batch, tokens = cu.numel() - 1, q.shape[0]
+        require(cu.dim() == 1 and 1 <= batch <= self.batch,
+                f"cu: {batch} sequences, planned for {self.batch}")
+        require(max_new is None or 0 <= max_new <= tokens, f"max_new {max_new} of {tokens} tokens")
+        require(0 <= layer < kv.layers, f"layer {layer} of {kv.layers}")
+        out = torch.empty(q.shape, dtype=q.dtype, device=kv.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=kv.device)
+        if tokens == 0:
+            return out, lse
+        stream = raw_stream(kv.device)
+        space = self._prompt.get(tokens)
+        if space is None:
+            if len(self._prompt) >= 64:  # prompts of ever new sizes
+                self._prompt.clear()
+            space = self._prompt[tokens] = self._space(tokens)
+        w, c, _ = space.get(stream)
+        check(self._lib.moe_attn_prompt(kv._ref, self._cfg, layer, q.data_ptr(), DTYPES[q.dtype],
+                                        ts, hs, tokens, cu.data_ptr(), batch, out.data_ptr(),
+                                        lse.data_ptr(), w, c, stream), "prompt")
+        return out, lse

@@ -1,7 +1,9 @@
-"""Compile the HIP decode-step library (``libmoe_decode.so``) for gfx950.
+"""Compile the HIP libraries for gfx950: the decode step (``libmoe_decode.so``)
+and the serving operators around it (``libmoe_serve.so``).
 
-One translation unit (``csrc/moe_decode.hip``) holds the kernels and the C ABI
-declared in ``include/moe_decode.h``.  Packed-f32 instruction selection is
+Each is one translation unit (``csrc/moe_decode.hip``, ``csrc_serve/serve.hip``)
+with the kernels and the C ABI declared in ``include/moe_decode.h`` and
+``include/moe_serve.h``.  Packed-f32 instruction selection is
 switched off for the device code.
 """
 import hashlib
@@ -13,25 +15,35 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "moe_decode.hip")
 LIB = os.path.join(HERE, "libmoe_decode.so")
+SERVE_SRC = os.path.join(HERE, "csrc_serve", "serve.hip")
+SERVE_LIB = os.path.join(HERE, "libmoe_serve.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
-def command(out: str, extra=()) -> list:
+def command(out: str, extra=(), src: str = SRC) -> list:
     return [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
             "-Wall", "-Wno-unused-function",
             "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"),
-            *extra, SRC, "-o", out]
+            "-I", os.path.join(HERE, "csrc_serve"), *extra, src, "-o", out]
 
 
-def build(verbose: bool = False, extra=()) -> str:
-    tmp = LIB + ".tmp"
-    cmd = command(tmp, extra)
+def _build(src: str, lib: str, verbose: bool, extra) -> str:
+    tmp = lib + ".tmp"
+    cmd = command(tmp, extra, src)
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, lib)
+    return lib
+
+
+def build(verbose: bool = False, extra=()) -> str:
+    return _build(SRC, LIB, verbose, extra)
+
+
+def build_serve(verbose: bool = False, extra=()) -> str:
+    return _build(SERVE_SRC, SERVE_LIB, verbose, extra)
 
 
 def source_digest() -> str:
@@ -48,3 +60,4 @@ def source_digest() -> str:
 
 if __name__ == "__main__":
     print(build(verbose=True, extra=sys.argv[1:]))
+    print(build_serve(verbose=True, extra=sys.argv[1:]))

@@ -1,0 +1,483 @@
+// serve.hip - host side of the serving operators: argument checks, launch
+// rules and the C ABI declared in include/moe_serve.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "attn_decode.h"
+#include "attn_prompt.h"
+#include "kv_pages.h"
+#include "moe_serve.h"
+#include "w4_linear.h"
+
+using namespace moe::serve;
+
+namespace {
+
+thread_local int32_t g_last_hip = 0;
+
+moe_status hip_error(hipError_t e) {
+    g_last_hip = (int32_t)e;
+    return MOE_ERR_HIP;
+}
+moe_status launched() {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? MOE_OK : hip_error(e);
+}
+
+// Compute units of the current device (0: unknown yet, -1: not gfx950).
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_cus[kMaxDevices];
+
+moe_status compute_units(int *cus) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_error(e);
+    if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
+    int n = g_cus[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        hipDeviceProp_t p;
+        e = hipGetDeviceProperties(&p, dev);
+        if (e != hipSuccess) return hip_error(e);
+        const bool ours = p.gcnArchName[0] == 'g' && std::equal(p.gcnArchName, p.gcnArchName + 6, "gfx950");
+        n = ours ? p.multiProcessorCount : -1;
+        g_cus[dev].store(n, std::memory_order_relaxed);
+    }
+    if (n < 0) return MOE_ERR_UNSUPPORTED;
+    *cus = n;
+    return MOE_OK;
+}
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+int log2_of(int v) {
+    int r = 0;
+    while ((1 << r) < v) ++r;
+    return r;
+}
+int64_t plane_bytes(const moe_kv_cache &kv) {
+    return (int64_t)kv.pages * kv.kv_heads * kv.page * kv.head_dim * (kv.dtype == MOE_E4M3 ? 1 : 2);
+}
+char *plane(const moe_kv_cache &kv, int layer, int which) {
+    return (char *)kv.data + (2 * (int64_t)layer + which) * plane_bytes(kv);
+}
+
+constexpr int kMaxRows = 1 << 24;  // sequences, tokens of a call, pairs of a list
+
+// Workgroups that one decode call aims at: with four waves each, three of them
+// share a compute unit.
+constexpr int kUnitsPerCu = 4;
+// What a plan is made for; the device a plan runs on has the same number.
+constexpr int kPlanCus = 256;
+
+int decode_split(const moe_kv_cache &kv, const moe_attn_config &c) {
+    const int group = c.q_heads / kv.kv_heads, hg = (group + 15) / 16;
+    const int heads = kv.kv_heads * hg;
+    // No unit is smaller than a block per wave.
+    int64_t keys = c.longest;
+    if (c.window > 0) keys = std::min<int64_t>(keys, (int64_t)c.window + c.sinks + 62);
+    const int64_t most = (int64_t)c.batch * ((keys + 127) / 128);
+    return (int)std::max<int64_t>(
+        1, std::min<int64_t>(most, std::max(1, kPlanCus * kUnitsPerCu / heads)));
+}
+
+struct PromptPlan {
+    int64_t tiles;
+    int split;
+};
+PromptPlan prompt_plan(const moe_kv_cache &kv, const moe_attn_config &c, int tokens, int batch) {
+    PromptPlan p;
+    const int64_t rows = (int64_t)tokens * (c.q_heads / kv.kv_heads);
+    p.tiles = rows / kPromptRows + std::min<int64_t>(batch, tokens);
+    const int64_t sure = std::max<int64_t>(1, (rows + kPromptRows - 1) / kPromptRows) * kv.kv_heads;
+    // Two workgroups share a compute unit; a part has four tiles of keys at least.
+    int64_t keys = c.longest;
+    if (c.window > 0) keys = std::min<int64_t>(keys, (int64_t)c.window + c.sinks + kPromptRows);
+    const int64_t parts = std::max<int64_t>(1, (keys + kPromptKeys - 1) / kPromptKeys / 4);
+    p.split = (int)std::max<int64_t>(1, std::min<int64_t>({2 * kPlanCus / sure, parts, 64}));
+    return p;
+}
+
+template <class F>
+moe_status with_dim(int d, F f) {
+    switch (d) {
+        case 64: return f(std::integral_constant<int, 64>());
+        case 96: return f(std::integral_constant<int, 96>());
+        case 128: return f(std::integral_constant<int, 128>());
+        case 192: return f(std::integral_constant<int, 192>());
+        case 256: return f(std::integral_constant<int, 256>());
+    }
+    return MOE_ERR_UNSUPPORTED;
+}
+// Calls f with the compute type and whether the cache holds e4m3.
+template <class F>
+moe_status with_types(int dtype, bool f8, F f) {
+    if (dtype == MOE_BF16) return f8 ? f(Bf16(), std::true_type()) : f(Bf16(), std::false_type());
+    return f8 ? f(Fp16(), std::true_type()) : f(Fp16(), std::false_type());
+}
+
+moe_status check_types(const moe_kv_cache &kv, int dtype) {
+    if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_INVALID_ARG;
+    if (kv.dtype != MOE_E4M3 && kv.dtype != dtype) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+moe_status check_strides(int64_t token, int64_t head, int heads, int d) {
+    if (token < 0 || head < 0 || (token | head) % 8) return MOE_ERR_INVALID_ARG;
+    if (heads > 1 && head < d) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+AttnArgs attn_args(const moe_kv_cache &kv, const moe_attn_config &c, int layer) {
+    AttnArgs a = {};
+    a.k = plane(kv, layer, 0);
+    a.v = plane(kv, layer, 1);
+    a.tables = kv.tables;
+    a.lengths = kv.lengths;
+    a.k_scale = kv.k_scale;
+    a.v_scale = kv.v_scale;
+    a.scale = c.scale * moe::serve::kLog2e;
+    a.pages = kv.pages;
+    a.cols = kv.cols;
+    a.page_log2 = log2_of(kv.page);
+    a.kv_heads = kv.kv_heads;
+    a.group = c.q_heads / kv.kv_heads;
+    a.head_groups = (a.group + 15) / 16;
+    a.window = c.window;
+    a.sinks = c.window > 0 ? c.sinks : 0;
+    return a;
+}
+
+moe_status check_attn(const moe_kv_cache *kv, const moe_attn_config *c, int layer, const void *q,
+                      int dtype, int64_t token, int64_t head, int batch, const void *out,
+                      const void *lse, const void *ws, const void *counters) {
+    moe_status s = moe_attn_validate(kv, c);
+    if (s != MOE_OK) return s;
+    if (!q || !out || !lse || batch < 1 || batch > c->batch || layer < 0 || layer >= kv->layers)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return MOE_ERR_INVALID_ARG;
+    if ((s = check_types(*kv, dtype)) != MOE_OK) return s;
+    if ((s = check_strides(token, head, c->q_heads, kv->head_dim)) != MOE_OK) return s;
+    if (!aligned(ws, 16) || !aligned(counters, 16)) return MOE_ERR_WORKSPACE;
+    return MOE_OK;
+}
+
+PagesArgs pages_args(const moe_kv_cache &kv, int n, void *scratch) {
+    PagesArgs a = {};
+    a.tables = kv.tables;
+    a.lengths = kv.lengths;
+    a.refs = kv.refs;
+    a.flags = kv.flags;
+    a.scratch = (int32_t *)scratch;
+    a.n = n;
+    a.pages = kv.pages;
+    a.page_log2 = log2_of(kv.page);
+    a.seqs = kv.seqs;
+    a.cols = kv.cols;
+    return a;
+}
+MoveArgs move_args(const moe_kv_cache &kv) {
+    MoveArgs m = {};
+    m.data = (char *)kv.data;
+    m.plane_bytes = plane_bytes(kv);
+    m.page_bytes = m.plane_bytes / kv.pages;
+    m.planes = 2 * kv.layers;
+    m.pages = kv.pages;
+    return m;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t moe_serve_last_hip_error(void) { return g_last_hip; }
+
+moe_status moe_kv_validate(const moe_kv_cache *kv) {
+    if (!kv || !kv->data || !kv->tables || !kv->lengths || !kv->refs || !kv->flags)
+        return MOE_ERR_INVALID_ARG;
+    if (kv->layers < 1 || kv->pages < 1 || kv->kv_heads < 1 || kv->seqs < 1 || kv->cols < 1)
+        return MOE_ERR_INVALID_ARG;
+    if (kv->dtype < MOE_BF16 || kv->dtype > MOE_E4M3) return MOE_ERR_INVALID_ARG;
+    if (kv->dtype != MOE_E4M3 && (kv->k_scale || kv->v_scale)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(kv->data, 16)) return MOE_ERR_INVALID_ARG;
+    if (kv->page < 16 || kv->page > 1024 || (kv->page & (kv->page - 1))) return MOE_ERR_UNSUPPORTED;
+    if (kv->seqs > kMaxRows || kv->kv_heads > 1024 || kv->layers > 4096) return MOE_ERR_UNSUPPORTED;
+    if ((int64_t)kv->cols * kv->page >= (1ll << 31) - 2048 ||
+        (int64_t)kv->seqs * kv->cols >= (1ll << 31) / (kv->page / 16))
+        return MOE_ERR_UNSUPPORTED;
+    return with_dim(kv->head_dim, [](auto) { return MOE_OK; });
+}
+
+moe_status moe_kv_append(const moe_kv_cache *kv, int32_t layer, const void *k, const void *v,
+                         int32_t dtype, int64_t token_stride, int64_t head_stride, int32_t tokens,
+                         const int32_t *cu, int32_t batch, moe_stream_t stream) {
+    moe_status s = moe_kv_validate(kv);
+    if (s != MOE_OK) return s;
+    if (layer < 0 || layer >= kv->layers || tokens < 0 || batch < 0 || batch > kv->seqs ||
+        tokens > kMaxRows)
+        return MOE_ERR_INVALID_ARG;
+    if (!cu && tokens != batch) return MOE_ERR_INVALID_ARG;
+    if (tokens == 0 || batch == 0) return MOE_OK;
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return MOE_ERR_INVALID_ARG;
+    if ((s = check_types(*kv, dtype)) != MOE_OK) return s;
+    if ((s = check_strides(token_stride, head_stride, kv->kv_heads, kv->head_dim)) != MOE_OK)
+        return s;
+    int cus;
+    if ((s = compute_units(&cus)) != MOE_OK) return s;
+    AppendArgs a = {};
+    a.k = k;
+    a.v = v;
+    a.kc = plane(*kv, layer, 0);
+    a.vc = plane(*kv, layer, 1);
+    a.tables = kv->tables;
+    a.lengths = kv->lengths;
+    a.cu = cu;
+    a.k_scale = kv->k_scale;
+    a.v_scale = kv->v_scale;
+    a.token_stride = token_stride;
+    a.head_stride = head_stride;
+    a.tokens = tokens;
+    a.batch = batch;
+    a.pages = kv->pages;
+    a.cols = kv->cols;
+    a.page_log2 = log2_of(kv->page);
+    a.kv_heads = kv->kv_heads;
+    a.head_dim = kv->head_dim;
+    // Two rounds of the workgroup's threads, where there are tokens enough to
+    // fill the chip that way.
+    const int per_token = kv->kv_heads * kv->head_dim / 8;
+    a.per_block = std::max(1, std::min(512 / per_token, tokens / (4 * cus)));
+    const int grid = (tokens + a.per_block - 1) / a.per_block;
+    return with_types(dtype, kv->dtype == MOE_E4M3, [&](auto t, auto f8) {
+        k_kv_append<decltype(t), decltype(f8)::value><<<grid, 256, 0, stream>>>(a);
+        return launched();
+    });
+}
+
+size_t moe_kv_scratch_size(const moe_kv_cache *kv, int32_t n) {
+    if (moe_kv_validate(kv) != MOE_OK || n < 0 || n > kMaxRows) return 0;
+    return sizeof(int32_t) *
+           (kScratchHead + std::max<size_t>(3 * (size_t)kv->pages, 3 * (size_t)n + kv->pages));
+}
+
+moe_status moe_kv_free(const moe_kv_cache *kv, const int32_t *seqs, int32_t n,
+                       moe_stream_t stream) {
+    moe_status s = moe_kv_validate(kv);
+    if (s != MOE_OK) return s;
+    if (n < 0 || n > kv->seqs) return MOE_ERR_INVALID_ARG;
+    if (n == 0) return MOE_OK;
+    if (!seqs) return MOE_ERR_INVALID_ARG;
+    PagesArgs a = pages_args(*kv, n, nullptr);
+    a.from = seqs;
+    k_kv_free<<<n, 256, 0, stream>>>(a);
+    return launched();
+}
+
+moe_status moe_kv_fork(const moe_kv_cache *kv, const int32_t *parents, const int32_t *children,
+                       int32_t n, void *scratch, moe_stream_t stream) {
+    moe_status s = moe_kv_validate(kv);
+    if (s != MOE_OK) return s;
+    if (n < 0 || n > kv->seqs) return MOE_ERR_INVALID_ARG;
+    if (n == 0) return MOE_OK;
+    if (!parents || !children) return MOE_ERR_INVALID_ARG;
+    if (!scratch || !aligned(scratch, 16)) return MOE_ERR_WORKSPACE;
+    PagesArgs a = pages_args(*kv, n, scratch);
+    a.from = parents;
+    a.to = children;
+    k_kv_fork<<<1, kPagesThreads, 0, stream>>>(a);
+    if ((s = launched()) != MOE_OK) return s;
+    MoveArgs m = move_args(*kv);
+    m.n = n;
+    m.from = a.scratch + kScratchHead;
+    m.to = m.from + 1;
+    m.stride = 2;
+    const int64_t items = (int64_t)n * m.planes * ((m.page_bytes + kMoveChunk - 1) / kMoveChunk);
+    k_kv_move<<<(int)std::min<int64_t>(items, 2048), 256, 0, stream>>>(m);
+    return launched();
+}
+
+moe_status moe_kv_extend(const moe_kv_cache *kv, const int32_t *seqs, const int32_t *counts,
+                         int32_t n, void *scratch, moe_stream_t stream) {
+    moe_status s = moe_kv_validate(kv);
+    if (s != MOE_OK) return s;
+    if (n < 0 || n > kv->seqs) return MOE_ERR_INVALID_ARG;
+    if (n == 0) return MOE_OK;
+    if (!counts) return MOE_ERR_INVALID_ARG;
+    if (!scratch || !aligned(scratch, 16)) return MOE_ERR_WORKSPACE;
+    PagesArgs a = pages_args(*kv, n, scratch);
+    a.from = seqs;
+    a.counts = counts;
+    k_kv_extend<<<1, kPagesThreads, 0, stream>>>(a);
+    return launched();
+}
+
+moe_status moe_kv_compact(const moe_kv_cache *kv, int32_t *new_tables, int32_t *new_refs,
+                          void *scratch, moe_stream_t stream) {
+    moe_status s = moe_kv_validate(kv);
+    if (s != MOE_OK) return s;
+    if (!new_tables || !new_refs) return MOE_ERR_INVALID_ARG;
+    if (!scratch || !aligned(scratch, 16)) return MOE_ERR_WORKSPACE;
+    PagesArgs a = pages_args(*kv, 0, scratch);
+    a.new_tables = new_tables;
+    a.new_refs = new_refs;
+    k_kv_compact<<<1, kPagesThreads, 0, stream>>>(a);
+    if ((s = launched()) != MOE_OK) return s;
+    MoveArgs m = move_args(*kv);
+    m.count = a.scratch;
+    m.n = kv->pages / 2;
+    m.to = a.scratch + kScratchHead;
+    m.from = m.to + kv->pages;
+    m.place = m.from + kv->pages;
+    m.stride = 1;
+    m.tables = kv->tables;
+    m.new_tables = new_tables;
+    m.entries = (int64_t)kv->seqs * kv->cols;
+    k_kv_move<<<2048, 256, 0, stream>>>(m);
+    return launched();
+}
+
+moe_status moe_attn_validate(const moe_kv_cache *kv, const moe_attn_config *c) {
+    const moe_status s = moe_kv_validate(kv);
+    if (s != MOE_OK) return s;
+    if (!c || c->q_heads < 1 || c->q_heads % kv->kv_heads || c->batch < 1 || c->batch > kv->seqs ||
+        c->longest < 1 || c->window < 0 || c->sinks < 0 || !(c->scale > 0.f) ||
+        !(c->scale < 1e30f))
+        return MOE_ERR_INVALID_ARG;
+    if (c->q_heads / kv->kv_heads > 1024) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status moe_attn_workspace(const moe_kv_cache *kv, const moe_attn_config *c, int32_t tokens,
+                              size_t *workspace, size_t *counters) {
+    const moe_status s = moe_attn_validate(kv, c);
+    if (s != MOE_OK) return s;
+    if (!workspace || !counters || tokens < 0 || tokens > kMaxRows) return MOE_ERR_INVALID_ARG;
+    if (tokens == 0) {
+        const int hg = (c->q_heads / kv->kv_heads + 15) / 16;
+        const size_t heads = (size_t)kv->kv_heads * hg;
+        *workspace = sizeof(float) * 16 * (kv->head_dim + 2) * heads *
+                     ((size_t)decode_split(*kv, *c) + c->batch);
+        *counters = sizeof(uint32_t) * heads * c->batch;
+    } else {
+        const PromptPlan p = prompt_plan(*kv, *c, tokens, c->batch);
+        const size_t groups = (size_t)p.tiles * kv->kv_heads;
+        *workspace = p.split == 1 ? 0
+                                  : sizeof(float) * kPromptRows * (kv->head_dim + 2) * groups * p.split;
+        *counters = p.split == 1 ? 0 : sizeof(uint32_t) * groups;
+    }
+    return MOE_OK;
+}
+
+moe_status moe_attn_decode(const moe_kv_cache *kv, const moe_attn_config *c, int32_t layer,
+                           const void *q, int32_t dtype, int64_t token_stride, int64_t head_stride,
+                           int32_t batch, void *out, float *lse, void *workspace, uint32_t *counters,
+                           moe_stream_t stream) {
+    moe_status s = check_attn(kv, c, layer, q, dtype, token_stride, head_stride, batch, out, lse,
+                              workspace, counters);
+    if (s != MOE_OK) return s;
+    if (!workspace || !counters) return MOE_ERR_WORKSPACE;
+    int cus;
+    if ((s = compute_units(&cus)) != MOE_OK) return s;
+    AttnArgs a = attn_args(*kv, *c, layer);
+    a.q = q;
+    a.q_token = token_stride;
+    a.q_head = head_stride;
+    a.out = out;
+    a.lse = lse;
+    a.part = (float *)workspace;
+    a.counters = counters;
+    a.batch = batch;
+    a.split = decode_split(*kv, *c);
+    const int grid = (a.split + batch) * a.kv_heads * a.head_groups;
+    return with_types(dtype, kv->dtype == MOE_E4M3, [&](auto t, auto f8) {
+        return with_dim(kv->head_dim, [&](auto d) {
+            k_attn_decode<decltype(t), decltype(f8)::value, decltype(d)::value>
+                <<<grid, kDecodeThreads, 0, stream>>>(a);
+            return launched();
+        });
+    });
+}
+
+moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *c, int32_t layer,
+                           const void *q, int32_t dtype, int64_t token_stride, int64_t head_stride,
+                           int32_t tokens, const int32_t *cu, int32_t batch, void *out, float *lse,
+                           void *workspace, uint32_t *counters, moe_stream_t stream) {
+    if (tokens == 0 && moe_attn_validate(kv, c) == MOE_OK) return MOE_OK;
+    moe_status s = check_attn(kv, c, layer, q, dtype, token_stride, head_stride, batch, out, lse,
+                              workspace, counters);
+    if (s != MOE_OK) return s;
+    if (!cu || tokens < 0 || tokens > kMaxRows) return MOE_ERR_INVALID_ARG;
+    int cus;
+    if ((s = compute_units(&cus)) != MOE_OK) return s;
+    AttnArgs a = attn_args(*kv, *c, layer);
+    a.q = q;
+    a.q_token = token_stride;
+    a.q_head = head_stride;
+    a.cu = cu;
+    a.out = out;
+    a.lse = lse;
+    a.part = (float *)workspace;
+    a.counters = counters;
+    a.batch = batch;
+    a.tokens = tokens;
+    const PromptPlan p = prompt_plan(*kv, *c, tokens, c->batch);
+    a.split = p.split;
+    if (p.split > 1 && (!workspace || !counters)) return MOE_ERR_WORKSPACE;
+    const int64_t grid = p.tiles * kv->kv_heads * p.split;
+    if (grid >= 1ll << 31) return MOE_ERR_UNSUPPORTED;
+    return with_types(dtype, kv->dtype == MOE_E4M3, [&](auto t, auto f8) {
+        return with_dim(kv->head_dim, [&](auto d) {
+            k_attn_prompt<decltype(t), decltype(f8)::value, decltype(d)::value>
+                <<<(int)grid, kPromptThreads, 0, stream>>>(a);
+            return launched();
+        });
+    });
+}
+
+moe_status moe_w4_workspace(int32_t tokens, int32_t k, int32_t n, size_t *workspace,
+                            size_t *counters) {
+    if (!workspace || !counters || tokens < 0 || k < 1 || n < 1) return MOE_ERR_INVALID_ARG;
+    *workspace = *counters = 0;
+    return MOE_OK;
+}
+
+moe_status moe_w4_linear(const void *x, int64_t x_stride, int32_t dtype, const uint8_t *codes,
+                         const void *scales, const uint8_t *zeros, int32_t tokens, int32_t k,
+                         int32_t n, int32_t group, void *y, void *workspace, uint32_t *counters,
+                         moe_stream_t stream) {
+    (void)workspace;
+    (void)counters;
+    if ((dtype != MOE_BF16 && dtype != MOE_FP16) || !codes || !scales || tokens < 0 || k < 1 ||
+        n < 1 || tokens > kMaxRows)
+        return MOE_ERR_INVALID_ARG;
+    if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
+    if (k % group || k > 1 << 24 || n > 1 << 24) return MOE_ERR_UNSUPPORTED;
+    if (tokens == 0) return MOE_OK;
+    if (!x || !y || x_stride < 0 || x_stride % 8 || !aligned(x, 16) || !aligned(codes, 16))
+        return MOE_ERR_INVALID_ARG;
+    int cus;
+    moe_status s = compute_units(&cus);
+    if (s != MOE_OK) return s;
+    W4Args a = {};
+    a.x = (const uint16_t *)x;
+    a.scales = (const uint16_t *)scales;
+    a.codes = codes;
+    a.zeros = zeros;
+    a.y = (uint16_t *)y;
+    a.x_stride = x_stride;
+    a.tokens = tokens;
+    a.k = k;
+    a.n = n;
+    a.group_log2 = log2_of(group);
+    a.steps = (k + 127) / 128;
+    a.slices = 1;
+    return with_types(dtype, false, [&](auto t, auto) {
+        typedef decltype(t) T;
+        if (tokens <= 16)
+            k_w4<T, 1, 1><<<dim3((n + 15) / 16, 1), kW4Threads, 0, stream>>>(a);
+        else
+            k_w4<T, 2, 2><<<dim3((n + 31) / 32, (tokens + 31) / 32), kW4Threads, 0, stream>>>(a);
+        return launched();
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,56 @@
+"""Products with 4-bit weights: y = x W^T, W = (codes - zeros) * scales.
+
+codes [n, k / 2] u8 hold two columns per byte (2j in the low half), scales
+[n, k / group] one factor per group of 32, 64 or 128 columns in x's type, zeros
+[n, k / group] u8 the code that stands for zero (None: 8).
+"""
+from __future__ import annotations
+
+import torch
+
+from .serving import DTYPES, check, lib, raw_stream, require, tensor
+
+GROUPS = (32, 64, 128)
+
+
+class W4Linear:
+    """A linear layer over 4-bit weights; the tensors are kept as they are."""
+
+    def __init__(self, codes, scales, zeros=None):
+        tensor(codes, "codes", torch.uint8)
+        require(codes.dim() == 2, f"codes: shape {tuple(codes.shape)} given, (n, k / 2) needed")
+        dev = codes.device
+        tensor(scales, "scales", (torch.bfloat16, torch.float16), device=dev)
+        self.n, self.k = codes.shape[0], 2 * codes.shape[1]
+        require(scales.dim() == 2 and scales.shape[0] == self.n and scales.shape[1] > 0 and
+                self.k % scales.shape[1] == 0 and self.k // scales.shape[1] in GROUPS,
+                f"scales: shape {tuple(scales.shape)} for {self.n} rows of {self.k} columns: "
+                "(n, k / group) with groups of 32, 64 or 128 needed")
+        self.group = self.k // scales.shape[1]
+        if zeros is not None:
+            tensor(zeros, "zeros", torch.uint8, scales.shape, dev)
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.device, self.dtype = dev, scales.dtype
+        self._lib = lib()
+        self._ptrs = (codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None
+                      else None)
+
+    def __call__(self, x, out=None):
+        """x [tokens, k], rows contiguous -> [tokens, n]."""
+        require(isinstance(x, torch.Tensor) and x.dtype == self.dtype and x.device == self.device,
+                f"x: a {self.dtype} tensor on {self.device} is needed")
+        require(x.dim() == 2 and x.shape[1] == self.k,
+                f"x: shape {tuple(x.shape)} given, (tokens, {self.k}) needed")
+        stride = x.stride()
+        require(stride[1] == 1 and stride[0] % 8 == 0 and x.data_ptr() % 16 == 0,
+                f"x: strides {tuple(stride)}: contiguous rows, 16-byte aligned, are needed")
+        tokens = x.shape[0]
+        if out is None:
+            out = torch.empty((tokens, self.n), dtype=x.dtype, device=self.device)
+        else:
+            tensor(out, "out", x.dtype, (tokens, self.n), self.device)
+        codes, scales, zeros = self._ptrs
+        check(self._lib.moe_w4_linear(x.data_ptr(), stride[0], DTYPES[x.dtype], codes, scales,
+                                      zeros, tokens, self.k, self.n, self.group, out.data_ptr(),
+                                      None, None, raw_stream(self.device)), "w4")
+        return out

@@ -1,0 +1,151 @@
+"""Plain 64-bit implementations of the serving operators, and caches to try
+them on.  Everything here runs on the CPU, from the operators' definitions."""
+import math
+
+import torch
+
+E4M3 = torch.float8_e4m3fn
+
+
+def half_step(dtype) -> float:
+    return torch.finfo(dtype).eps / 2
+
+
+class HostCache:
+    """A paged cache on the CPU: random pages in random order; positions that no
+    sequence holds are NaN unless clean."""
+
+    def __init__(self, lengths, kv_heads, page, dim, dtype=torch.bfloat16, layers=1, spare=3,
+                 seed=0, clean=False, spare_cols=1):
+        g = torch.Generator().manual_seed(seed)
+        need = [-(-n // page) for n in lengths]
+        pages = sum(need) + spare
+        order = torch.randperm(pages, generator=g)
+        self.tables = torch.full((len(lengths), max(need) + spare_cols), -1, dtype=torch.int32)
+        self.refs = torch.zeros(pages, dtype=torch.int32)
+        self.lengths = torch.tensor(lengths, dtype=torch.int32)
+        shape = (layers, 2, pages, kv_heads, page, dim)
+        base = torch.bfloat16 if dtype == E4M3 else dtype
+        data = torch.randn(shape, generator=g).to(base)
+        if not clean:
+            keep = torch.zeros(pages, page, dtype=torch.bool)
+        at = 0
+        for b, n in enumerate(lengths):
+            ids = order[at:at + need[b]]
+            at += need[b]
+            self.tables[b, :need[b]] = ids.int()
+            self.refs[ids] = 1
+            if not clean:
+                for i, p in enumerate(ids.tolist()):
+                    keep[p, :min(page, n - i * page)] = True
+        if not clean:
+            data.masked_fill_(~keep[None, None, :, None, :, None], math.nan)
+        self.data = data.to(dtype)
+        self.k_scale = self.v_scale = None
+        if dtype == E4M3:
+            self.k_scale, self.v_scale = (0.5 + torch.rand(kv_heads, generator=g) for _ in range(2))
+        self.page, self.dim, self.kv_heads, self.dtype = page, dim, kv_heads, dtype
+
+    def row(self, layer, which, b, n):
+        """([n][kv_heads][dim] f64, which positions have a page)"""
+        t = torch.arange(n)
+        ids = self.tables[b].long()[t // self.page]
+        ok = (ids >= 0) & (ids < self.data.shape[2])
+        x = self.data[layer, which].to(torch.float64)[ids.clamp(0, self.data.shape[2] - 1), :,
+                                                      t % self.page]
+        scale = self.k_scale if which == 0 else self.v_scale
+        return (x if scale is None else x * scale.double()[None, :, None]), ok
+
+    def gpu(self):
+        from sparse_moe_decode_router_amd import attention
+        d = lambda t: None if t is None else t.cuda()  # noqa: E731
+        data = self.data.view(torch.uint8).cuda().view(E4M3) if self.dtype == E4M3 else \
+            self.data.cuda()
+        return attention.PagedKV(data, d(self.tables), d(self.lengths), d(self.refs),
+                                 d(self.k_scale), d(self.v_scale))
+
+
+def attention(cache, layer, q, cu, window=0, sinks=0, scale=None):
+    """(out, lse, bound of out's error without its own rounding and that of the
+    weights, sum of w |v|), all f64, for rows cu[b] .. cu[b + 1] of q."""
+    dim = cache.dim
+    scale = dim ** -0.5 if scale is None else scale
+    group = q.shape[1] // cache.kv_heads
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64)
+    err, mass = torch.zeros_like(lse), torch.zeros_like(out)
+    most = cache.tables.shape[1] * cache.page
+    for b in range(len(cu) - 1):
+        n, new = int(cache.lengths[b]), cu[b + 1] - cu[b]
+        seen_n = max(0, min(n, most))
+        if seen_n == 0 or new == 0:
+            continue
+        k, ok = cache.row(layer, 0, b, seen_n)
+        v, _ = cache.row(layer, 1, b, seen_n)
+        t = torch.arange(seen_n)
+        for i in range(new):
+            pos = n - new + i
+            sees = (t <= pos) & ok
+            if window:
+                sees &= (t > pos - window) | (t < sinks)
+            at = sees.nonzero()[:, 0]
+            if not len(at):
+                continue
+            for h in range(q.shape[1]):
+                qq, kk, vv = q[cu[b] + i, h].double(), k[at, h // group], v[at, h // group]
+                s = kk @ qq * scale
+                w = torch.softmax(s, 0)
+                out[cu[b] + i, h] = w @ vv
+                lse[cu[b] + i, h] = torch.logsumexp(s, 0)
+                mass[cu[b] + i, h] = w @ vv.abs()
+                # A score is a sum of dim products in f32: at most dim steps of
+                # 2^-24 of the sum of their magnitudes; the rest (scaling, the
+                # exponential, sums over the keys, the division) stays well
+                # below 2^-16 with a few thousand keys.
+                err[cu[b] + i, h] = 2 * (dim * 2.0 ** -24 * float((kk.abs() @ qq.abs()).max())
+                                         * scale + 2.0 ** -16)
+    return out, lse, err, mass
+
+
+def check_attention(got, want, dtype, weights_rounded):
+    """weights_rounded: the weights themselves are held in dtype."""
+    out, lse = (x.cpu().double() for x in got)
+    ref, ref_lse, err, mass = want
+    h = half_step(dtype)
+    tol = h * ref.abs() + (err[..., None] + (h if weights_rounded else 0.0)) * mass * (1 + h)
+    empty = ref_lse == -math.inf
+    assert torch.equal(lse == -math.inf, empty)
+    assert torch.all(out[empty] == 0)
+    bad = (out - ref).abs() / tol.clamp(min=1e-30)
+    bad[(out == ref)] = 0
+    assert not out.isnan().any(), f"{int(out.isnan().sum())} NaN"
+    assert float(bad.max()) <= 1, f"output {float(bad.max()):.2f} times the bound"
+    off = ((lse - ref_lse).abs() / (err + 2.0 ** -22 * ref_lse.abs()))[~empty]
+    assert not len(off) or float(off.max()) <= 1, f"lse {float(off.max()):.2f} times the bound"
+
+
+def w4_weights(codes, zeros, group):
+    """(codes - zeros) f64 [n][k]"""
+    n, half = codes.shape
+    w = torch.empty((n, 2 * half), dtype=torch.float64)
+    w[:, 0::2], w[:, 1::2] = (codes & 15).double(), (codes >> 4).double()
+    z = torch.full((n, 2 * half // group), 8.0, dtype=torch.float64) if zeros is None else \
+        zeros.double()
+    return w - z.repeat_interleave(group, 1)
+
+
+def w4(x, codes, scales, zeros, group):
+    """(y, bound of the f32 part of its error) f64.  Within a group the kernel
+    sums products x (code + 2^7) in bf16 (the zero point's share is taken off
+    after the sum) and x (code - zero) in fp16: magnitudes of at most 143 |x|,
+    twice, or 15 |x|, in as many f32 additions as the group has columns; then
+    one addition per group."""
+    w = w4_weights(codes, zeros, group)
+    xd, s = x.double(), scales.double()
+    y = xd @ (w * s.repeat_interleave(group, 1)).t()
+    big = 143.0 if x.dtype == torch.bfloat16 else 15.0
+    mass = xd.abs().unflatten(1, (-1, group)).sum(-1)                    # [T][groups]
+    inner = (2 * group + 4) * 2.0 ** -24 * big * (mass @ s.abs().t())
+    part = torch.einsum("tgj,ngj->tng", xd.unflatten(1, (-1, group)), w.unflatten(1, (-1, group)))
+    outer = (s.shape[1] + 8) * 2.0 ** -24 * (part.abs() * s.abs()[None]).sum(-1)
+    return y, inner + outer
