@@ -151,9 +151,9 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *cfg, i
 /* y = x W^T with W[n][j] = (code[n][j] - zero[n][j / group]) * scale[n][j / group]:
  * codes u8 [n][k / 2] (column 2j in the low half of byte j), scales [n][k /
  * group] in x's type, zeros u8 [n][k / group] below 16, or NULL for 8; x
- * [tokens][k] with rows x_stride apart (a multiple of 8), y [tokens][n].
- * group 32, 64 or 128; k a multiple of group; n any; x and codes 16-byte
- * aligned.  Integers times x are summed exactly as products in f32, the
+ * [tokens][k] of finite values with rows x_stride apart (a multiple of 8, at
+ * most 2^25), y [tokens][n].  group 32, 64 or 128; k a multiple of group; n
+ * any; x and codes 16-byte aligned.  Integers times x are summed exactly as products in f32, the
  * scale is applied to each group's sum in f32, and y is rounded once. */
 moe_status moe_w4_linear(const void *x, int64_t x_stride, int32_t dtype, const uint8_t *codes,
                          const void *scales, const uint8_t *zeros, int32_t tokens, int32_t k,

@@ -116,6 +116,47 @@ moe_status with_types(int dtype, bool f8, F f) {
     return f8 ? f(Fp16(), std::true_type()) : f(Fp16(), std::false_type());
 }
 
+template <class F>
+moe_status with_group(int group, bool z, F f) {
+    auto g = [&](auto gl) { return z ? f(gl, std::true_type()) : f(gl, std::false_type()); };
+    if (group == 32) return g(std::integral_constant<int, 5>());
+    if (group == 64) return g(std::integral_constant<int, 6>());
+    return g(std::integral_constant<int, 7>());
+}
+// The fewest rows per workgroup that leave no compute unit two workgroups: a
+// second one on some of them costs more than larger tiles do, and from there
+// on larger tiles spread x over more rows.  Measured with 7168 columns, in us,
+// 16 / 32 / 64 rows: 8 tokens, 1152 rows 6.1 / 8.0 / 12.1, 9216 rows 16.8 /
+// 17.3 / 15.7, 36864 rows 52.0 / 43.4 / 44.5; 64 tokens, 7168 rows 33.9 / 23.0 /
+// 31.4, 36864 rows - / 104 / 96.  A single token has next to no x to spread
+// (1152 rows 5.0, with half the waves 5.8; 36864 rows 38.8 and 35.7).
+template <class T, int GL, bool Z>
+moe_status w4_launch(const W4Args &a, int cus, hipStream_t stream) {
+    auto go = [&](auto kernel, int nt, int rt, int w) {
+        const dim3 grid((a.n + 16 * rt - 1) / (16 * rt), (a.tokens + 16 * nt - 1) / (16 * nt));
+        kernel<<<grid, 64 * w, 0, stream>>>(a);
+        return launched();
+    };
+    const int rt = a.n <= 16 * cus ? 1 : a.n <= 32 * cus ? 2 : 4;
+    if (a.tokens <= 4)
+        return rt == 1 ? go(k_w4<T, 1, 1, 1, 8, 4, GL, Z>, 1, 1, 8)
+                       : go(k_w4<T, 1, 1, 1, 4, 2, GL, Z>, 1, 1, 4);
+    if (a.tokens <= 8)
+        return rt == 1   ? go(k_w4<T, 1, 2, 1, 8, 2, GL, Z>, 1, 1, 8)
+               : rt == 2 ? go(k_w4<T, 1, 2, 2, 4, 2, GL, Z>, 1, 2, 4)
+                         : go(k_w4<T, 1, 2, 4, 4, 2, GL, Z>, 1, 4, 4);
+    if (a.tokens <= 16)
+        return rt == 1   ? go(k_w4<T, 1, 4, 1, 8, 2, GL, Z>, 1, 1, 8)
+               : rt == 2 ? go(k_w4<T, 1, 4, 2, 4, 2, GL, Z>, 1, 2, 4)
+                         : go(k_w4<T, 1, 4, 4, 4, 2, GL, Z>, 1, 4, 4);
+    if (a.tokens <= 32)
+        return rt == 1 ? go(k_w4<T, 2, 8, 1, 8, 2, GL, Z>, 2, 1, 8)
+                       : go(k_w4<T, 2, 8, 4, 8, 1, GL, Z>, 2, 4, 8);
+    return rt == 1   ? go(k_w4<T, 4, 16, 1, 8, 1, GL, Z>, 4, 1, 8)
+           : rt == 2 ? go(k_w4<T, 4, 16, 2, 8, 1, GL, Z>, 4, 2, 8)
+                     : go(k_w4<T, 4, 16, 4, 4, 1, GL, Z>, 4, 4, 4);
+}
+
 moe_status check_types(const moe_kv_cache &kv, int dtype) {
     if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_INVALID_ARG;
     if (kv.dtype != MOE_E4M3 && kv.dtype != dtype) return MOE_ERR_INVALID_ARG;
@@ -450,7 +491,7 @@ moe_status moe_w4_linear(const void *x, int64_t x_stride, int32_t dtype, const u
         n < 1 || tokens > kMaxRows)
         return MOE_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
-    if (k % group || k > 1 << 24 || n > 1 << 24) return MOE_ERR_UNSUPPORTED;
+    if (k % group || k > 1 << 24 || n > 1 << 24 || x_stride > 1 << 25) return MOE_ERR_UNSUPPORTED;
     if (tokens == 0) return MOE_OK;
     if (!x || !y || x_stride < 0 || x_stride % 8 || !aligned(x, 16) || !aligned(codes, 16))
         return MOE_ERR_INVALID_ARG;
@@ -467,16 +508,10 @@ moe_status moe_w4_linear(const void *x, int64_t x_stride, int32_t dtype, const u
     a.tokens = tokens;
     a.k = k;
     a.n = n;
-    a.group_log2 = log2_of(group);
-    a.steps = (k + 127) / 128;
-    a.slices = 1;
     return with_types(dtype, false, [&](auto t, auto) {
-        typedef decltype(t) T;
-        if (tokens <= 16)
-            k_w4<T, 1, 1><<<dim3((n + 15) / 16, 1), kW4Threads, 0, stream>>>(a);
-        else
-            k_w4<T, 2, 2><<<dim3((n + 31) / 32, (tokens + 31) / 32), kW4Threads, 0, stream>>>(a);
-        return launched();
+        return with_group(group, zeros != nullptr, [&](auto gl, auto z) {
+            return w4_launch<decltype(t), decltype(gl)::value, decltype(z)::value>(a, cus, stream);
+        });
     });
 }
 

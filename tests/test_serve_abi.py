@@ -113,6 +113,12 @@ def test_calls_refuse_before_any_launch():
     assert w(t=0) == 0
 
 
+def test_w4_refuses_strides_beyond_its_offsets():
+    args = lambda xs: (4096, xs, 0, 4096, 4096, None, 1, 128, 8, 64, 4096, None, None,  # noqa: E731
+                       None)
+    assert status("moe_w4_linear", *args((1 << 25) + 8)) == -2
+
+
 def test_workspace_sizes():
     c, cfg = cache(), serving.AttnConfig(14, 4, 500, 0, 0, 0.1)
     w, n = ctypes.c_size_t(), ctypes.c_size_t()

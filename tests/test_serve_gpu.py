@@ -391,6 +391,15 @@ def test_w4(case):
             assert float(off.max()) <= 1, f"{float(off.max()):.2f} times the bound"
 
 
+# More weight rows than compute units times 16 or 32: larger tiles of them.
+@pytest.mark.parametrize("rows", [4111, 8209])
+@pytest.mark.parametrize("tokens,k,group,zeros,dtype", [
+    (2, 640, 128, True, FP), (7, 672, 32, True, BF), (16, 384, 64, False, FP),
+    (29, 800, 32, False, BF), (64, 448, 64, True, BF), (70, 1152, 128, True, FP)])
+def test_w4_many_rows(rows, tokens, k, group, zeros, dtype):
+    test_w4((tokens, k, rows, group, zeros, dtype))
+
+
 def test_streams_have_their_own_workspace():
     """Two streams at work on the same plan: split rows and their counters."""
     cache, q, _, _ = decode_case(([4000, 3000], 1, 4, 128, 16, BF, BF, 0, 0))
