@@ -50,7 +50,6 @@ __device__ __forceinline__ int row_tiles(int tokens, int group) {
     return (int)(((int64_t)tokens * group + kPromptRows - 1) / kPromptRows);
 }
 
-typedef __attribute__((address_space(3))) void lds_void;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ u32x2 read_transposed(const char *p) {
@@ -58,22 +57,35 @@ __device__ __forceinline__ u32x2 read_transposed(const char *p) {
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
 }
 
-// Values that are all finite: pass 0: v where it is finite; 1: one where v is
-// +inf or NaN; 2: one where it is -inf or NaN.
+// 64 lanes bring 16 bytes each from base + off (off per lane) straight into
+// LDS: lane l's to lds + 16 l.  In assembly and without any output: behind the
+// builtin the compiler waits for the copy before the next read of LDS, also of
+// another buffer.  Whoever reads the copy waits for vmcnt itself.
+__device__ __forceinline__ void copy_to_lds(const void *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const char *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
+
+// What is not finite in two values: 1 (sign 0) or 2 (sign 1) marks, as values
+// that are one where v is +inf (or -inf) or NaN and zero elsewhere.
 template <class T>
-__device__ __forceinline__ u32x4 part_of(u32x4 v, int pass) {
+__device__ __forceinline__ uint32_t marks_of(uint32_t v, uint32_t sign) {
+    uint32_t out = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        uint32_t out = 0;
-#pragma unroll
-        for (int z = 0; z < 32; z += 16) {
-            const uint32_t h = v[e] >> z & 0xFFFFu;
-            const bool marked = T::odd(h) && (T::nan(h) || (h >> 15) == (uint32_t)(pass - 1));
-            out |= (pass == 0 ? (T::odd(h) ? 0u : h) : marked ? T::kOne : 0u) << z;
-        }
-        v[e] = out;
+    for (int z = 0; z < 32; z += 16) {
+        const uint32_t h = v >> z & 0xFFFFu;
+        out |= (T::odd(h) && (T::nan(h) || h >> 15 == sign) ? T::kOne : 0u) << z;
     }
-    return v;
+    return out;
+}
+template <class T>
+__device__ __forceinline__ uint32_t finite_of(uint32_t v) {
+    return (T::odd(v) ? 0u : v & 0xFFFFu) | (T::odd(v >> 16) ? 0u : v & 0xFFFF0000u);
 }
 
 template <class T, bool F8, int D>
@@ -85,7 +97,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
     __shared__ __attribute__((aligned(1024))) char s_v[2][Tile::kBytes];
     __shared__ float s_m[kPromptRows], s_den[kPromptRows];
     __shared__ uint32_t s_last;
-    __shared__ int s_odd[2];
+    __shared__ int s_odd;
 
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_index();
     const int col = lane & 31, half = lane >> 5;
@@ -163,35 +175,55 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
     constexpr int ES = F8 ? 1 : 2;
     const int64_t head_bytes = (int64_t)D * ES << a.page_log2;
     const int in_page = (1 << a.page_log2) - 1;
-    // Wave w brings the 16 keys 16w .. 16w + 15 of a tile: they share a page.
-    auto page_of = [&](int i) {
-        const int key = 64 * visible_block(vis, i) + 16 * wave;
-        return (uint32_t)table[min(key >> a.page_log2, a.cols - 1)];
+    // The pages of a tile's four groups of 16 keys, by scalar loads (the tables
+    // are not written here): they wait for nothing of the vector memory.  Wave w
+    // brings the keys of group w.
+    typedef __attribute__((address_space(4))) const int32_t const_i32;
+    const_i32 *table_c = (const_i32 *)(uintptr_t)table;
+    struct Pages {
+        uint32_t p[4];
     };
-    auto row_of = [&](const void *base, uint32_t p, int i) {
-        const int key = 64 * visible_block(vis, i) + 16 * wave;
+    auto pages_of = [&](int i) {
+        const int key = (int)uniform(64 * visible_block(vis, i));
+        Pages x;
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            x.p[y] = (uint32_t)table_c[min((key + 16 * y) >> a.page_log2, a.cols - 1)];
+        return x;
+    };
+    auto row_of = [&](const void *base, const Pages &x, int i) {
+        const int key = (int)uniform(64 * visible_block(vis, i) + 16 * wave);
+        const uint32_t w = wave;
+        uint32_t p = w == 0 ? x.p[0] : w == 1 ? x.p[1] : w == 2 ? x.p[2] : x.p[3];
         p = p < (uint32_t)a.pages ? p : 0u;
         return (const char *)base + ((int64_t)p * a.kv_heads + h) * head_bytes +
                (key & in_page) * (D * ES);
     };
-    auto copy_in = [&](const void *base, char *dst, uint32_t p, int i) {
-        const char *src = row_of(base, p, i);
-        constexpr int RPI = 64 / Tile::kSlots;  // rows per instruction
+    // Rows x RPI .. of a wave's share, and the piece a lane brings of them.
+    constexpr int RPI = 64 / Tile::kSlots, CP = 16 / RPI;
+    uint32_t copy_off[F8 ? 1 : CP];
+    if constexpr (!F8) {
 #pragma unroll
-        for (int x = 0; x < 16 / RPI; ++x) {
+        for (int x = 0; x < CP; ++x) {
             const int r = RPI * x + lane / Tile::kSlots;
-            const int ch = (lane % Tile::kSlots) ^ Tile::swizzle(16 * wave + r);
-            char *to = dst + (16 * wave + RPI * x) * Tile::kRowBytes;
-            if (ch < Tile::kChunks)
-                __builtin_amdgcn_global_load_lds(src + r * (2 * D) + 16 * ch, (lds_void *)to, 16, 0,
-                                                 0);
+            const int ch = (lane % Tile::kSlots) ^ Tile::swizzle(r);
+            copy_off[x] = ch < Tile::kChunks ? r * (2 * D) + 16 * ch : ~0u;
+        }
+    }
+    auto copy_in = [&](const void *base, const char *dst, const Pages &pg, int i) {
+        const char *src = row_of(base, pg, i);
+        const uint32_t to = uniform(lds_address(dst) + 16 * wave * Tile::kRowBytes);
+#pragma unroll
+        for (int x = 0; x < CP; ++x) {
+            if (Tile::kSlots == Tile::kChunks || copy_off[x] != ~0u)
+                copy_to_lds(src, copy_off[x], to + RPI * x * Tile::kRowBytes);
         }
     };
     // e4m3: a lane's share of 16 rows is 16 D / 64 codes, in chunks of 8.
     constexpr int NC = F8 ? D / 32 : 1;
     u32x2 raw_k[NC], raw_v[NC];
-    auto fetch = [&](const void *base, u32x2 *raw, uint32_t p, int i) {
-        const char *src = row_of(base, p, i);
+    auto fetch = [&](const void *base, u32x2 *raw, const Pages &pg, int i) {
+        const char *src = row_of(base, pg, i);
 #pragma unroll
         for (int x = 0; x < NC; ++x) raw[x] = *(const u32x2 *)(src + 8 * (64 * x + lane));
     };
@@ -227,9 +259,70 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         return (u32x4){x[0], x[1], y[0], y[1]};
     };
 
-    uint32_t page_next = 0;
+    // What rows see of a tile: which groups of 16 keys have a page, and whether
+    // every row sees all of it.
+    struct Seen {
+        int key0;
+        uint32_t have;
+        bool whole;
+    };
+    auto seen_of = [&](const Pages &pg, int i) {
+        Seen x;
+        x.key0 = (int)uniform(64 * visible_block(vis, i));
+        x.have = 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) x.have |= pg.p[y] < (uint32_t)a.pages ? 1u << y : 0u;
+        x.whole = x.have == 15u && x.key0 + 63 <= pos_lo && x.key0 + 64 <= n_seen &&
+                  (a.window <= 0 || x.key0 > pos_hi - a.window || x.key0 + 64 <= a.sinks);
+        return x;
+    };
+    // Scores: keys down (2 x 32), rows across.  Operands are read four at a
+    // time, one round ahead of the products that take them.
+    auto scores = [&](const char *sk, f32x16 *s) {
+        // Opaque, so that the operands' addresses are formed where they are
+        // used: kept from tile to tile they take some forty registers.
+        uint32_t ak = at_k;
+        asm("" : "+v"(ak));
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
+        u32x4 kb[2][4];
+        auto read_k = [&](u32x4 *d, int f0) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+                d[f] = ld16(sk + 32 * ((f0 + f) & 1) * Tile::kRowBytes + (ak ^ 32 * ((f0 + f) >> 1)));
+        };
+        read_k(kb[0], 0);
+#pragma unroll
+        for (int f = 0; f < 2 * KS; f += 4) {
+            if (f + 4 < 2 * KS) read_k(kb[f / 4 + 1 & 1], f + 4);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                s[x & 1] = T::mfma32(kb[f / 4 & 1][x], q[(f + x) >> 1], s[x & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto hide = [&](const Seen &see, f32x16 *s) {
+        int key0 = see.key0 + 4 * half;  // opaque, as above
+        asm("" : "+v"(key0));
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int key = key0 + 32 * u + 8 * (r >> 2) + (r & 3);
+                const bool sees = (key <= pos) & (key < n_seen) &
+                                  ((key > from) | (key < a.sinks)) &
+                                  ((see.have >> (2 * u + (r >> 3)) & 1) != 0);
+                s[u][r] = sees ? s[u][r] : hidden;
+            }
+    };
+
+    if (tid == 0) s_odd = 0;
+    Pages now = {}, next = {};
     if (i0 < i1) {
-        const uint32_t p = page_of(i0);
+        const Pages p = now = pages_of(i0);
         if constexpr (F8) {
             fetch(a.k, raw_k, p, i0);
             fetch(a.v, raw_v, p, i0);
@@ -239,7 +332,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
             copy_in(a.k, s_k[0], p, i0);
             copy_in(a.v, s_v[0], p, i0);
         }
-        page_next = page_of(min(i0 + 1, i1 - 1));
+        next = pages_of(min(i0 + 1, i1 - 1));
     }
     for (int i = i0; i < i1; ++i) {
         const int buf = (i - i0) & 1;
@@ -249,74 +342,48 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         const bool more = i + 1 < i1;
         if (more) {
             if constexpr (F8) {
-                fetch(a.k, raw_k, page_next, i + 1);
-                fetch(a.v, raw_v, page_next, i + 1);
+                fetch(a.k, raw_k, next, i + 1);
+                fetch(a.v, raw_v, next, i + 1);
             } else {
-                copy_in(a.k, s_k[buf ^ 1], page_next, i + 1);
-                copy_in(a.v, s_v[buf ^ 1], page_next, i + 1);
+                copy_in(a.k, s_k[buf ^ 1], next, i + 1);
+                copy_in(a.v, s_v[buf ^ 1], next, i + 1);
             }
-            page_next = page_of(min(i + 2, i1 - 1));
         }
-        const int key0 = 64 * visible_block(vis, i);
-        // Which of the tile's four groups of 16 keys have a page.
-        uint32_t have = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int at = (key0 + 16 * x) >> a.page_log2;
-            if (at < a.cols && (uint32_t)table[at] < (uint32_t)a.pages) have |= 1u << x;
-        }
-        const bool whole = have == 15u && key0 + 63 <= pos_lo && key0 + 64 <= n_seen &&
-                           (a.window <= 0 || key0 > pos_hi - a.window || key0 + 64 <= a.sinks);
-        bool odd_v = false;
-        if (!whole) {
-            // Values that no row sees become zero here; where values that some
-            // rows see are not finite, the product below is taken apart, so
-            // that they reach those rows alone.
-            if (tid < 2) s_odd[tid] = 0;
-            __syncthreads();
-            bool odd = false;
-            for (int x = tid; x < kPromptKeys * Tile::kChunks; x += kPromptThreads) {
+        const Seen see = seen_of(now, i);
+        now = next;
+        next = pages_of(min(i + 2, i1 - 1));
+        if (!see.whole) {
+            // Values that no row sees become zero, and so do those that are not
+            // finite: a row that does not see them would get NaN from them.
+            // What they mean for the rows that do see them comes at the end.
+            int x0 = tid;  // opaque, as in scores()
+            asm("" : "+v"(x0));
+#pragma unroll 1
+            for (int x = x0; x < kPromptKeys * Tile::kChunks; x += kPromptThreads) {
                 const int r = x / Tile::kChunks;
                 u32x4 *p = (u32x4 *)(sv + Tile::byte_of(r, x % Tile::kChunks));
-                if (key0 + r >= n_seen || !(have >> (r >> 4) & 1)) {
-                    *p = (u32x4){0, 0, 0, 0};
-                } else {
-                    const u32x4 w = *p;
+                u32x4 w = {0, 0, 0, 0};
+                if (see.key0 + r < n_seen && (see.have >> (r >> 4) & 1)) {
+                    const u32x4 v = *p;
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) odd = odd || T::odd(w[y]) || T::odd(w[y] >> 16);
+                    for (int y = 0; y < 4; ++y) w[y] = finite_of<T>(v[y]);
+                    if (w[0] != v[0] || w[1] != v[1] || w[2] != v[2] || w[3] != v[3]) s_odd = 1;
                 }
+                *p = w;
             }
-            if (__any(odd) && lane == 0) s_odd[0] = 1;
             __syncthreads();
-            odd_v = s_odd[0] != 0;
         }
-
-        // Opaque, so that the operands' addresses are formed where they are
-        // used: kept from tile to tile they take some forty registers.
-        uint32_t ak = at_k, av = at_v;
-        asm("" : "+v"(ak), "+v"(av));
-        // Scores: keys down (2 x 32), rows across.
         f32x16 s[2];
+        scores(sk, s);
+        uint32_t av = at_v;
+        asm("" : "+v"(av));
+        u32x4 vb[2][DT];
+        auto read_v = [&](u32x4 *d, int t) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
-#pragma unroll
-            for (int j = 0; j < KS; ++j)
-                s[u] = T::mfma32(ld16(sk + 32 * u * Tile::kRowBytes + (ak ^ 32 * j)), q[j], s[u]);
-        }
-        if (!whole) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int key = key0 + 32 * u + 8 * (r >> 2) + 4 * half + (r & 3);
-                    const bool sees = (key <= pos) & (key < n_seen) &
-                                      ((key > from) | (key < a.sinks)) &
-                                      ((have >> (2 * u + (r >> 3)) & 1) != 0);
-                    s[u][r] = sees ? s[u][r] : hidden;
-                }
-        }
+            for (int dt = 0; dt < DT; ++dt) d[dt] = v_op(sv, av, t, dt);
+        };
+        read_v(vb[0], 0);
+        if (!see.whole) hide(see, s);
         float top = s[0][0];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -351,11 +418,13 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                 l += p0 + p1;
                 p[2 * u + (r >> 3)][(r & 7) >> 1] = T::pack(p0, p1);
             }
-        if (!odd_v) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) {
+            if (t < 3) read_v(vb[t + 1 & 1], t + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt) o[dt] = T::mfma32(v_op(sv, av, t, dt), p[t], o[dt]);
+            for (int dt = 0; dt < DT; ++dt) o[dt] = T::mfma32(vb[t & 1][dt], p[t], o[dt]);
+            __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (F8) {
             if (more) {
@@ -363,25 +432,57 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                 convert(raw_v, s_v[buf ^ 1]);
             }
         }
-        if (odd_v) {
-            // Three products with values that are all finite: the finite part,
-            // then a mark wherever a value is +inf (or NaN), then wherever it
-            // is -inf (or NaN).  A row with weight on a mark gets that infinity,
-            // with both NaN.
+    }
+    __syncthreads();
+    if (s_odd) {
+        // Values that are not finite, in tiles that some rows see and others do
+        // not: a row gets the infinity (for NaN both) of every one on which it
+        // has weight.  Rare, so each tile is brought again, without haste.
 #pragma unroll 1
-            for (int pass = 0; pass < 3; ++pass) {
+        for (int i = i0; i < i1; ++i) {
+            const Pages pg = pages_of(i);
+            const Seen see = seen_of(pg, i);
+            if (see.whole) continue;
+            __syncthreads();
+            if constexpr (F8) {
+                fetch(a.k, raw_k, pg, i);
+                fetch(a.v, raw_v, pg, i);
+                convert(raw_k, s_k[0]);
+                convert(raw_v, s_v[0]);
+            } else {
+                copy_in(a.k, s_k[0], pg, i);
+                copy_in(a.v, s_v[0], pg, i);
+            }
+            wait_vm_all();
+            __syncthreads();
+            f32x16 s[2];
+            scores(s_k[0], s);
+            hide(see, s);
+            u32x4 p[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; r += 2)
+                    p[2 * u + (r >> 3)][(r & 7) >> 1] =
+                        T::pack(exp2_(fmaf(s[u][r], c2, T::kOff - m)),
+                                exp2_(fmaf(s[u][r + 1], c2, T::kOff - m)));
+#pragma unroll 1
+            for (uint32_t sign = 0; sign < 2; ++sign) {
+                const float add = sign ? -__builtin_inff() : __builtin_inff();
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt) {
                     f32x16 x;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) x[r] = 0.f;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        x = T::mfma32(part_of<T>(v_op(sv, av, t, dt), pass), p[t], x);
-                    const float add = pass == 1 ? __builtin_inff() : -__builtin_inff();
+                    for (int t = 0; t < 4; ++t) {
+                        u32x4 v = v_op(s_v[0], at_v, t, dt);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        o[dt][r] += pass == 0 ? x[r] : x[r] != 0.f ? add : 0.f;
+                        for (int y = 0; y < 4; ++y) v[y] = marks_of<T>(v[y], sign);
+                        x = T::mfma32(v, p[t], x);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[dt][r] += x[r] != 0.f ? add : 0.f;
                 }
             }
         }
