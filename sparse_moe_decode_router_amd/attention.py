@@ -225,11 +225,10 @@ class PagedAttention:
         if tokens == 0:
             return out, lse
         stream = raw_stream(kv.device)
-        space = self._prompt.get(tokens)
+        size = tokens.bit_length()  # more tokens never need less: one space up to each power of two
+        space = self._prompt.get(size)
         if space is None:
-            if len(self._prompt) >= 64:  # prompts of ever new sizes
-                self._prompt.clear()
-            space = self._prompt[tokens] = self._space(tokens)
+            space = self._prompt[size] = self._space(1 << size)
         w, c, _ = space.get(stream)
         check(self._lib.moe_attn_prompt(kv._ref, self._cfg, layer, q.data_ptr(), DTYPES[q.dtype],
                                         ts, hs, tokens, cu.data_ptr(), batch, out.data_ptr(),

@@ -98,6 +98,7 @@ struct AttnArgs {
     int32_t batch, tokens, pages, cols, page_log2, kv_heads, group, head_groups;
     int32_t window, sinks;
     int32_t split;             // decode: units aimed at per kv head; prompt: most splits
+    int32_t units;             // prompt: equal shares per kv head (0: row tiles)
 };
 
 // Blocks of 2^L keys that a row at the last position of n sees: the first

@@ -107,6 +107,36 @@ def attention(cache, layer, q, cu, window=0, sinks=0, scale=None):
     return out, lse, err, mass
 
 
+def attention_dense(cache, layer, q, cu, window=0, sinks=0):
+    """The same as attention(), for caches whose sequences have all their pages:
+    whole sequences at once."""
+    dim = cache.dim
+    scale = dim ** -0.5
+    group = q.shape[1] // cache.kv_heads
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64)
+    err, mass = torch.zeros_like(lse), torch.zeros_like(out)
+    for b in range(len(cu) - 1):
+        n, new = int(cache.lengths[b]), cu[b + 1] - cu[b]
+        if n == 0 or new == 0:
+            continue
+        k, v = cache.row(layer, 0, b, n)[0], cache.row(layer, 1, b, n)[0]
+        t, pos = torch.arange(n), torch.arange(n - new, n)[:, None]
+        sees = t <= pos
+        if window:
+            sees &= (t > pos - window) | (t < sinks)
+        rows = slice(cu[b], cu[b + 1])
+        for h in range(q.shape[1]):
+            qq, kk, vv = q[rows, h].double(), k[:, h // group], v[:, h // group]
+            s = (qq @ kk.t() * scale).masked_fill(~sees, -math.inf)
+            w = torch.softmax(s, 1)
+            out[rows, h], mass[rows, h] = w @ vv, w @ vv.abs()
+            lse[rows, h] = torch.logsumexp(s, 1)
+            big = (qq.abs() @ kk.abs().t()).masked_fill(~sees, 0.0).amax(1)
+            err[rows, h] = 2 * (dim * 2.0 ** -24 * big * scale + 2.0 ** -16)
+    return out, lse, err, mass
+
+
 def check_attention(got, want, dtype, weights_rounded):
     """weights_rounded: the weights themselves are held in dtype."""
     out, lse = (x.cpu().double() for x in got)

@@ -129,8 +129,11 @@ def test_workspace_sizes():
     # rows of outputs, maxima and sums; a counter per (sequence, kv head)
     assert (rc, ctr) == (0, 4 * 2 * 4) and 0 < ws <= 4 * 16 * 130 * 2 * (4 * 4 + 4)
     assert size(-1)[0] == -1
-    rc, ws, ctr = size(20000)             # enough rows: nothing is split
+    rc, ws, ctr = size(4000)              # a workgroup for every row tile: nothing is split
     assert (rc, ws, ctr) == (0, 0, 0)
+    rc, ws, ctr = size(20000)             # equal shares: two parts for each, whatever the tokens
+    assert (rc, ws) == (0, 4 * 128 * 130 * 2 * 512) and ctr >= 4 * 2 * (20000 * 7 // 128)
+    assert size(1 << 20)[:2] == (0, ws)
     assert serving.lib().moe_kv_scratch_size(ctypes.addressof(c), 4) >= 4 * 3 * 100
 
 
@@ -158,6 +161,16 @@ def test_reference_attention_is_softmax_attention():
     want = torch.nn.functional.scaled_dot_product_attention(q.double().transpose(0, 1), k, v,
                                                             attn_mask=sees)
     assert torch.allclose(win.transpose(0, 1), want, rtol=1e-12, atol=1e-12)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (9, 3)])
+def test_reference_attention_of_many_heads(window, sinks):
+    c = su.HostCache([50, 20, 0], 2, 16, 64, seed=2)
+    cu = [0, 30, 50, 52]
+    q = torch.randn(52, 6, 64).to(torch.bfloat16)
+    for a, b in zip(su.attention(c, 0, q, cu, window, sinks),
+                    su.attention_dense(c, 0, q, cu, window, sinks)):
+        assert torch.allclose(a, b, rtol=1e-9, atol=1e-12)
 
 
 def test_reference_w4():

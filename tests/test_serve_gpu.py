@@ -109,6 +109,35 @@ def test_prompt(case):
         su.check_attention(got, want, dtype, True)
 
 
+# More row tiles than fit on the chip at once: equal shares of all tiles of keys.
+# lengths, new tokens, kv heads, heads per kv head, head_dim, page, dtype, cache, window, sinks
+SHARES = [
+    ([900, 40, 0, 700], [300, 40, 5, 150], 40, 4, 64, 16, BF, BF, 0, 0),
+    ([1500, 130], [200, 130], 40, 8, 128, 64, FP, FP, 0, 0),
+    ([1500, 130], [200, 130], 40, 8, 128, 16, BF, E4, 500, 7),
+    ([2100], [150], 33, 8, 256, 32, BF, BF, 0, 0),
+    ([700, 350], [700, 350], 20, 4, 96, 16, BF, BF, 200, 20),
+]
+
+
+@pytest.mark.parametrize("case", SHARES, ids=str)
+def test_prompt_in_equal_shares(case):
+    lengths, new, kvh, group, dim, page, dtype, cdtype, window, sinks = case
+    cache = su.HostCache(lengths, kvh, page, dim, cdtype, seed=23)
+    cu = [0]
+    for x in new:
+        cu.append(cu[-1] + x)
+    q = queries((cu[-1], kvh * group, dim), dtype, 24)
+    att = attention.PagedAttention(cache.gpu(), kvh * group, len(new), max(lengths),
+                                   window=window, sinks=sinks)
+    want = su.attention_dense(cache, 0, q, cu, window, sinks)
+    qd, cud = q.cuda(), torch.tensor(cu, dtype=torch.int32).cuda()
+    for _ in range(3):
+        got = att.prompt(0, qd, cud)
+        torch.cuda.synchronize()
+        su.check_attention([x[:cu[-1]] for x in got], want, dtype, True)
+
+
 @pytest.mark.parametrize("kind", ["decode", "prompt"])
 @pytest.mark.parametrize("cdtype", [BF, E4])
 def test_what_a_row_does_not_see_may_be_anything(kind, cdtype):
