@@ -23,6 +23,7 @@ from typing import Optional, Tuple
 
 import torch
 
+from .binding import MoEError
 from .serving import (DTYPES, AttnConfig, Cache, StreamSpace, check, lib, raw_stream, require,
                       tensor)
 
@@ -32,17 +33,22 @@ E4M3_MAX = 448.0
 def _rows(t, name, heads, dim, dtypes, device) -> Tuple[int, int]:
     """Checks a [tokens][heads][dim] tensor whose rows are contiguous; returns
     its token and head strides."""
+    # What is right is passed without forming any message: a call takes as long
+    # as its smallest kernels.
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device:
+        shape, (ts, hs, one) = t.shape, t.stride() if t.dim() == 3 else (0, 0, 0)
+        if len(shape) == 3 and shape[1] == heads and shape[2] == dim and one == 1 and \
+                ts % 8 == 0 and hs % 8 == 0 and (heads == 1 or hs >= dim) and \
+                t.data_ptr() % 16 == 0:
+            return ts, hs
     require(isinstance(t, torch.Tensor), f"{name}: a tensor is needed, got {type(t).__name__}")
     require(t.dtype in dtypes, f"{name}: {t.dtype} given, {' or '.join(map(str, dtypes))} needed")
     require(t.device == device, f"{name}: on {t.device}, not on {device}")
     shape, stride = t.shape, t.stride()
     require(len(shape) == 3 and shape[1] == heads and shape[2] == dim,
             f"{name}: shape {tuple(shape)} given, (tokens, {heads}, {dim}) needed")
-    require(stride[2] == 1 and stride[0] % 8 == 0 and stride[1] % 8 == 0 and
-            (heads == 1 or stride[1] >= dim) and t.data_ptr() % 16 == 0,
-            f"{name}: strides {tuple(stride)}: rows of {dim} contiguous elements, 16-byte aligned, "
-            "are needed")
-    return stride[0], stride[1]
+    raise MoEError(f"{name}: strides {tuple(stride)}: rows of {dim} contiguous elements, 16-byte "
+                   "aligned, are needed")
 
 
 class PagedKV:
@@ -100,8 +106,10 @@ class PagedKV:
 
     def _list(self, t, name, n=None) -> int:
         tensor(t, name, torch.int32, None if n is None else (n,), self.device)
-        require(t.dim() == 1, f"{name}: one dimension is needed")
-        require(t.shape[0] <= self.seqs, f"{name}: {t.shape[0]} entries for {self.seqs} sequences")
+        if t.dim() != 1:
+            raise MoEError(f"{name}: one dimension is needed")
+        if t.shape[0] > self.seqs:
+            raise MoEError(f"{name}: {t.shape[0]} entries for {self.seqs} sequences")
         return t.shape[0]
 
     def append(self, layer: int, k, v, cu=None) -> None:
@@ -110,18 +118,22 @@ class PagedKV:
         position (where it has none, nothing is written); else cu [batch + 1]
         i32: tokens cu[b] .. cu[b + 1] - 1 are sequence b's last positions."""
         ts, hs = _rows(k, "k", self.kv_heads, self.head_dim, self.compute_dtypes, self.device)
-        require(_rows(v, "v", self.kv_heads, self.head_dim, (k.dtype,), self.device) == (ts, hs) and
-                v.shape == k.shape, "v: the shape and strides of k are needed")
+        if _rows(v, "v", self.kv_heads, self.head_dim, (k.dtype,), self.device) != (ts, hs) or \
+                v.shape != k.shape:
+            raise MoEError("v: the shape and strides of k are needed")
         tokens = k.shape[0]
         if cu is None:
             batch = tokens
-            require(batch <= self.seqs, f"k: {batch} tokens for {self.seqs} sequences")
+            if batch > self.seqs:
+                raise MoEError(f"k: {batch} tokens for {self.seqs} sequences")
         else:
             tensor(cu, "cu", torch.int32, device=self.device)
             batch = cu.numel() - 1
-            require(cu.dim() == 1 and 0 <= batch <= self.seqs,
-                    f"cu: 1 to {self.seqs + 1} entries are needed, got shape {tuple(cu.shape)}")
-        require(0 <= layer < self.layers, f"layer {layer} of {self.layers}")
+            if cu.dim() != 1 or not 0 <= batch <= self.seqs:
+                raise MoEError(f"cu: 1 to {self.seqs + 1} entries are needed, got shape "
+                               f"{tuple(cu.shape)}")
+        if not 0 <= layer < self.layers:
+            raise MoEError(f"layer {layer} of {self.layers}")
         check(self._lib.moe_kv_append(self._ref, layer, k.data_ptr(), v.data_ptr(),
                                       DTYPES[k.dtype], ts, hs, tokens,
                                       None if cu is None else cu.data_ptr(), batch,
@@ -196,10 +208,12 @@ class PagedAttention:
         kv = self.kv
         ts, hs = _rows(q, "q", self.q_heads, kv.head_dim, kv.compute_dtypes, kv.device)
         batch = q.shape[0]
-        require(1 <= batch <= self.batch, f"q: {batch} sequences, planned for {self.batch}")
-        require(0 <= layer < kv.layers, f"layer {layer} of {kv.layers}")
+        if not 1 <= batch <= self.batch:
+            raise MoEError(f"q: {batch} sequences, planned for {self.batch}")
+        if not 0 <= layer < kv.layers:
+            raise MoEError(f"layer {layer} of {kv.layers}")
         out = torch.empty(q.shape, dtype=q.dtype, device=kv.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=kv.device)
+        lse = torch.empty((batch, self.q_heads), dtype=torch.float32, device=kv.device)
         stream = raw_stream(kv.device)
         w, c, _ = self._decode.get(stream)
         check(self._lib.moe_attn_decode(kv._ref, self._cfg, layer, q.data_ptr(), DTYPES[q.dtype],
@@ -216,10 +230,12 @@ class PagedAttention:
         ts, hs = _rows(q, "q", self.q_heads, kv.head_dim, kv.compute_dtypes, kv.device)
         tensor(cu, "cu", torch.int32, device=kv.device)
         batch, tokens = cu.numel() - 1, q.shape[0]
-        require(cu.dim() == 1 and 1 <= batch <= self.batch,
-                f"cu: {batch} sequences, planned for {self.batch}")
-        require(max_new is None or 0 <= max_new <= tokens, f"max_new {max_new} of {tokens} tokens")
-        require(0 <= layer < kv.layers, f"layer {layer} of {kv.layers}")
+        if cu.dim() != 1 or not 1 <= batch <= self.batch:
+            raise MoEError(f"cu: {batch} sequences, planned for {self.batch}")
+        if max_new is not None and not 0 <= max_new <= tokens:
+            raise MoEError(f"max_new {max_new} of {tokens} tokens")
+        if not 0 <= layer < kv.layers:
+            raise MoEError(f"layer {layer} of {kv.layers}")
         out = torch.empty(q.shape, dtype=q.dtype, device=kv.device)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=kv.device)
         if tokens == 0:

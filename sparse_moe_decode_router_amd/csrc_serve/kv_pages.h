@@ -191,22 +191,26 @@ __global__ __launch_bounds__(kPagesThreads) void k_kv_fork(const PagesArgs a) {
         const int part = ok && (len & (page - 1)) ? 1 : 0;
         int all;
         const int at = need + block_scan(part, &all, s_wave);
-        if (i < a.n) copies[2 * i] = part ? at : -1;  // the rank, until pages are known
+        if (i < a.n) {  // the rank and the length, until pages are known
+            copies[2 * i] = part ? at : -1;
+            copies[2 * i + 1] = len;
+        }
         need += all;
     }
     const int found = take_lowest(a.pages, need, list, s_wave, [&](int p) { return a.refs[p] == 0; });
     __syncthreads();
     if (tid == 0 && found < need) atomicOr(a.flags, (uint32_t)MOE_KV_FLAG_NO_PAGES);
-    // Tables and references.  A pair's threads all read its rank before the
-    // last loop replaces it.
-    for (int64_t x = tid; x < (int64_t)a.n * a.cols; x += kPagesThreads) {
-        const int i = (int)(x / a.cols), col = (int)(x % a.cols);
-        const int child = a.to[i];
+    // Tables and references.  A pair's threads all read its rank and length
+    // before the last loop replaces them.  (All counts fit 32 bits.)
+    const uint32_t entries = (uint32_t)a.n * (uint32_t)a.cols;
+    for (uint32_t x = tid; x < entries; x += kPagesThreads) {
+        const int i = (int)(x / (uint32_t)a.cols), col = (int)(x % (uint32_t)a.cols);
+        const int child = a.to[i], parent = a.from[i];
+        const int rank = copies[2 * i], full = copies[2 * i + 1] >> a.page_log2;
         if (child < 0 || child >= a.seqs) continue;
-        const int len = length_of(a, a.from[i]), full = len >> a.page_log2, rank = copies[2 * i];
         int p = -1;
         if (col < full) {
-            p = a.tables[(int64_t)a.from[i] * a.cols + col];
+            p = a.tables[(int64_t)parent * a.cols + col];
             if (p >= 0 && p < a.pages) atomicAdd(a.refs + p, 1);
         } else if (col == full && rank >= 0 && rank < found) {
             p = list[rank];
@@ -216,8 +220,8 @@ __global__ __launch_bounds__(kPagesThreads) void k_kv_fork(const PagesArgs a) {
     }
     __syncthreads();
     for (int i = tid; i < a.n; i += kPagesThreads) {
-        const int child = a.to[i], rank = copies[2 * i];
-        const int len = length_of(a, a.from[i]), full = len >> a.page_log2;
+        const int child = a.to[i], rank = copies[2 * i], len = copies[2 * i + 1];
+        const int full = len >> a.page_log2;
         int src = -1, dst = -1;
         if (rank >= 0 && rank < found) {
             src = a.tables[(int64_t)a.from[i] * a.cols + full];

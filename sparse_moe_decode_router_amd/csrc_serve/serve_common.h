@@ -180,24 +180,20 @@ __device__ __forceinline__ void join_parts(const float *part, int64_t stride, in
         const int row = i / (D / 4), d = 4 * (i % (D / 4));
         const float m = mx[row], l = den[row];
         f32x4 sum = zero4();
-        int u = 0;
-        for (; u + 4 <= n_parts; u += 4) {
-            f32x4 x[4];
-            float f[4];
+        // Sixteen parts at a time, all of them on their way at once: one after
+        // the other they cost most of a microsecond each.
+        for (int u = 0; u < n_parts; u += 16) {
+            f32x4 x[16];
+            float f[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float *p = part + (u + j) * stride;
+            for (int j = 0; j < 16; ++j) {
+                const float *p = part + min(u + j, n_parts - 1) * stride;
                 x[j] = __builtin_bit_cast(f32x4, buf_ld16<true>(buf_rsrc(p), 4u * (row * D + d)));
                 f[j] = load_agent(p + (int64_t)row_slots * D + row);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum += x[j] * exp2_(f[j] - m);
-        }
-        for (; u < n_parts; ++u) {
-            const float *p = part + u * stride;
-            const f32x4 x =
-                __builtin_bit_cast(f32x4, buf_ld16<true>(buf_rsrc(p), 4u * (row * D + d)));
-            sum += x * exp2_(load_agent(p + (int64_t)row_slots * D + row) - m);
+            for (int j = 0; j < 16; ++j)
+                if (u + j < n_parts) sum += x[j] * exp2_(f[j] - m);
         }
         write(row, d, l != 0.f ? sum * (1.f / l) : zero4());
     }

@@ -105,6 +105,12 @@ def require(cond: bool, message: str) -> None:
 
 def tensor(t, name: str, dtype, shape=None, device=None) -> torch.Tensor:
     """A contiguous GPU tensor of that type (and shape, and device), or MoEError."""
+    # (What is right is passed without forming any message.)
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and \
+            (t.dtype in dtype if isinstance(dtype, tuple) else t.dtype == dtype) and \
+            (shape is None or tuple(t.shape) == tuple(shape)) and \
+            (device is None or t.device == device):
+        return t
     require(isinstance(t, torch.Tensor), f"{name}: a tensor is needed, got {type(t).__name__}")
     require(t.is_cuda, f"{name}: a GPU tensor is needed")
     types = dtype if isinstance(dtype, tuple) else (dtype,)

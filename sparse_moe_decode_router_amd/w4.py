@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import torch
 
+from .binding import MoEError
 from .serving import DTYPES, check, lib, raw_stream, require, tensor
 
 GROUPS = (32, 64, 128)
@@ -31,26 +32,28 @@ class W4Linear:
             tensor(zeros, "zeros", torch.uint8, scales.shape, dev)
         self.codes, self.scales, self.zeros = codes, scales, zeros
         self.device, self.dtype = dev, scales.dtype
-        self._lib = lib()
+        self._lib, self._dtype = lib(), DTYPES[self.dtype]
         self._ptrs = (codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None
                       else None)
 
     def __call__(self, x, out=None):
         """x [tokens, k], rows contiguous -> [tokens, n]."""
-        require(isinstance(x, torch.Tensor) and x.dtype == self.dtype and x.device == self.device,
-                f"x: a {self.dtype} tensor on {self.device} is needed")
-        require(x.dim() == 2 and x.shape[1] == self.k,
-                f"x: shape {tuple(x.shape)} given, (tokens, {self.k}) needed")
-        stride = x.stride()
-        require(stride[1] == 1 and stride[0] % 8 == 0 and x.data_ptr() % 16 == 0,
-                f"x: strides {tuple(stride)}: contiguous rows, 16-byte aligned, are needed")
-        tokens = x.shape[0]
+        if not isinstance(x, torch.Tensor) or x.dtype != self.dtype or x.device != self.device:
+            raise MoEError(f"x: a {self.dtype} tensor on {self.device} is needed")
+        shape, stride = x.shape, x.stride()
+        if len(shape) != 2 or shape[1] != self.k:
+            raise MoEError(f"x: shape {tuple(shape)} given, (tokens, {self.k}) needed")
+        address = x.data_ptr()
+        if stride[1] != 1 or stride[0] % 8 or address % 16:
+            raise MoEError(f"x: strides {tuple(stride)}: contiguous rows, 16-byte aligned, are "
+                           "needed")
+        tokens = shape[0]
         if out is None:
             out = torch.empty((tokens, self.n), dtype=x.dtype, device=self.device)
         else:
             tensor(out, "out", x.dtype, (tokens, self.n), self.device)
         codes, scales, zeros = self._ptrs
-        check(self._lib.moe_w4_linear(x.data_ptr(), stride[0], DTYPES[x.dtype], codes, scales,
+        check(self._lib.moe_w4_linear(address, stride[0], self._dtype, codes, scales,
                                       zeros, tokens, self.k, self.n, self.group, out.data_ptr(),
                                       None, None, raw_stream(self.device)), "w4")
         return out
