@@ -528,3 +528,43 @@ def test_refusals_on_the_gpu():
                                                               device="cuda"))):
         with pytest.raises(MoEError):
             bad()
+
+
+@pytest.mark.parametrize("cdtype", [BF, E4])
+def test_a_layer_serves_prompts_forks_and_tokens(cdtype):
+    """The operators together, in front of the expert step: a fork goes on as its
+    parent does, and neither freeing others nor moving pages changes anything."""
+    from sparse_moe_decode_router_amd import binding, serve_layer, synth
+    moe = binding.DeviceLayer(synth.make_layer(synth.TINY, 0), device="cuda:0")
+    layer = serve_layer.ServeLayer(moe, seqs=6, cols=40, pages=200, cache=cdtype)
+    kv = layer.kv
+    g = torch.Generator().manual_seed(30)
+    new = lambda n: torch.randn((n, moe.dims.hidden), generator=g).to(BF).cuda()  # noqa: E731
+    kv.extend(ints(300, 33))
+    prompt = layer(new(333), ints(0, 300, 333))
+    assert prompt.shape == (333, moe.dims.hidden) and prompt.isfinite().all()
+    kv.fork(ints(0, 1, 0), ints(2, 3, 4))
+    for _ in range(3):
+        x = new(2)
+        kv.extend(ints(1, 1, 1, 1, 1))
+        y = layer.attend(torch.cat([x, x, x[:1]]))
+        assert torch.equal(y[:2], y[2:4]) and torch.equal(y[0], y[4])
+        assert layer.experts(y).isfinite().all()
+    kv.extend(ints(1, 1, 1, 1, 1))
+    x = new(5)
+    before = layer.attend(x)
+    kv.free(ints(1, 3))
+    kv.compact()
+    after = layer.attend(x)                         # the same tokens once more
+    assert torch.equal(after[[0, 2, 4]], before[[0, 2, 4]])
+    assert int((kv.refs > 0).sum()) == int((kv.refs > 0).nonzero().max()) + 1
+    assert kv.read_flags() == 0
+    layer.close()
+
+
+def test_the_example_runs():
+    from sparse_moe_decode_router_amd import serve_layer
+    layer, x, us = serve_layer.run(steps=3)
+    assert x.isfinite().all() and us > 0
+    assert layer.kv.lengths.tolist() == [306, 23, 126, 70, 0, 0, 0, 0]
+    layer.close()
