@@ -124,7 +124,7 @@ typedef struct {
 moe_status moe_attn_validate(const moe_kv_cache *kv, const moe_attn_config *cfg);
 
 /* Bytes of workspace and of counters (both 16-byte aligned) of a decode call,
- * or of a prompt call with `tokens` new tokens (tokens = 0: decode).  Counters
+ * or of prompt calls with up to `tokens` new tokens (tokens = 0: decode).  Counters
  * are zero before the first call that uses them, and every call leaves them
  * zero; the workspace carries nothing from call to call.  Calls that may run
  * at the same time need their own of both. */

@@ -241,7 +241,7 @@ class PagedAttention:
         if tokens == 0:
             return out, lse
         stream = raw_stream(kv.device)
-        size = tokens.bit_length()  # more tokens never need less: one space up to each power of two
+        size = tokens.bit_length()  # one space for all calls up to a power of two
         space = self._prompt.get(size)
         if space is None:
             space = self._prompt[size] = self._space(1 << size)

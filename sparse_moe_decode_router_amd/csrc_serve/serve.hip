@@ -93,11 +93,13 @@ struct PromptPlan {
     int split, units;
     int64_t slots;  // of partial results
 };
-PromptPlan prompt_plan(const moe_kv_cache &kv, const moe_attn_config &c, int tokens, int batch) {
+// The plan for `row_tiles` full row tiles per kv head and at most `more` part-filled
+// ones beside them.
+PromptPlan prompt_plan_of(const moe_kv_cache &kv, const moe_attn_config &c, int64_t row_tiles,
+                          int64_t more) {
     PromptPlan p;
-    const int64_t rows = (int64_t)tokens * (c.q_heads / kv.kv_heads);
-    p.tiles = rows / kPromptRows + std::min<int64_t>(batch, tokens);
-    const int64_t sure = std::max<int64_t>(1, (rows + kPromptRows - 1) / kPromptRows) * kv.kv_heads;
+    p.tiles = row_tiles + more;
+    const int64_t sure = std::max<int64_t>(1, row_tiles) * kv.kv_heads;
     const int slots = prompt_slots(kv.head_dim);
     // A part has four tiles of keys at least.
     int64_t keys = c.longest;
@@ -108,6 +110,21 @@ PromptPlan prompt_plan(const moe_kv_cache &kv, const moe_attn_config &c, int tok
     p.slots = p.units ? 2 * (int64_t)p.units : p.split > 1 ? p.tiles * p.split : 0;
     p.slots *= kv.kv_heads;
     return p;
+}
+int64_t full_row_tiles(const moe_kv_cache &kv, const moe_attn_config &c, int tokens) {
+    return (int64_t)tokens * (c.q_heads / kv.kv_heads) / kPromptRows;
+}
+PromptPlan prompt_plan(const moe_kv_cache &kv, const moe_attn_config &c, int tokens, int batch) {
+    return prompt_plan_of(kv, c, full_row_tiles(kv, c, tokens), std::min(batch, tokens));
+}
+// Slots that no call of up to `tokens` tokens goes beyond: fewer row tiles are
+// split more finely, so the largest call need not be the one that takes most.
+int64_t prompt_slots_up_to(const moe_kv_cache &kv, const moe_attn_config &c, int tokens) {
+    const int64_t last = full_row_tiles(kv, c, tokens);
+    int64_t most = prompt_plan(kv, c, tokens, c.batch).slots;
+    for (int64_t r = 0; r <= std::min<int64_t>(last, prompt_slots(kv.head_dim)); ++r)
+        most = std::max(most, prompt_plan_of(kv, c, r, std::min(c.batch, tokens)).slots);
+    return most;
 }
 
 template <class F>
@@ -412,8 +429,9 @@ moe_status moe_attn_workspace(const moe_kv_cache *kv, const moe_attn_config *c, 
         *counters = sizeof(uint32_t) * heads * c->batch;
     } else {
         const PromptPlan p = prompt_plan(*kv, *c, tokens, c->batch);
-        *workspace = sizeof(float) * kPromptRows * (kv->head_dim + 2) * (size_t)p.slots;
-        *counters = p.slots ? sizeof(uint32_t) * (size_t)p.tiles * kv->kv_heads : 0;
+        *workspace = sizeof(float) * kPromptRows * (kv->head_dim + 2) *
+                     (size_t)prompt_slots_up_to(*kv, *c, tokens);
+        *counters = sizeof(uint32_t) * (size_t)p.tiles * kv->kv_heads;
     }
     return MOE_OK;
 }

@@ -129,12 +129,36 @@ def test_workspace_sizes():
     # rows of outputs, maxima and sums; a counter per (sequence, kv head)
     assert (rc, ctr) == (0, 4 * 2 * 4) and 0 < ws <= 4 * 16 * 130 * 2 * (4 * 4 + 4)
     assert size(-1)[0] == -1
-    rc, ws, ctr = size(4000)              # a workgroup for every row tile: nothing is split
-    assert (rc, ws, ctr) == (0, 0, 0)
     rc, ws, ctr = size(20000)             # equal shares: two parts for each, whatever the tokens
-    assert (rc, ws) == (0, 4 * 128 * 130 * 2 * 512) and ctr >= 4 * 2 * (20000 * 7 // 128)
+    assert rc == 0 and ws >= 4 * 128 * 130 * 2 * 512 and ctr >= 4 * 2 * (20000 * 7 // 128)
     assert size(1 << 20)[:2] == (0, ws)
     assert serving.lib().moe_kv_scratch_size(ctypes.addressof(c), 4) >= 4 * 3 * 100
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim,longest,window", [
+    (4, 1, 128, 8192, 0), (14, 2, 128, 8192, 4096), (7, 1, 256, 3000, 0), (64, 64, 64, 500, 0),
+    (1, 1, 128, 131072, 0)])
+def test_a_space_for_more_tokens_serves_fewer(heads, kv_heads, dim, longest, window):
+    """Fewer tokens are split into more parts, and still have room."""
+    c = cache(kv_heads=kv_heads, head_dim=dim, cols=8192)
+    cfg = serving.AttnConfig(heads, 3, longest, window, 0, 0.1)
+    w, n = ctypes.c_size_t(), ctypes.c_size_t()
+    slots, group = 512 if dim <= 128 else 256, heads // kv_heads
+    keys = min(longest, window + 128) if window else longest
+    last = (0, 0)
+    for t in sorted({*range(1, 300), *(2 ** i + d for i in range(4, 21) for d in (-1, 0, 1))}):
+        assert status("moe_attn_workspace", ctypes.addressof(c), ctypes.addressof(cfg), t,
+                      ctypes.byref(w), ctypes.byref(n)) == 0
+        assert (w.value, n.value) >= last and n.value >= last[1]
+        last = (w.value, n.value)
+        # What a call of that many tokens can take: a part for every row tile and
+        # split, as many as the chip holds at once, or two for each equal share.
+        full, tiles = t * group // 128, t * group // 128 + min(3, t)
+        sure = max(1, full) * kv_heads
+        split = max(1, min(slots // sure, -(-keys // 64) // 4, 64))
+        need = 2 * (slots // kv_heads) if sure > slots else tiles * split if split > 1 else 0
+        assert w.value >= 4 * 128 * (dim + 2) * need * kv_heads
+        assert n.value >= 4 * tiles * kv_heads
 
 
 def test_modules_refuse_cpu_tensors():
