@@ -66,9 +66,13 @@ __device__ __forceinline__ int row_tiles(int tokens, int group) {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ u32x2 read_transposed(const char *p) {
+// Reads at an address of LDS.
+__device__ __forceinline__ u32x2 read_transposed(uint32_t at) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
+}
+__device__ __forceinline__ u32x4 read_lds16(uint32_t at) {
+    return *(const __attribute__((address_space(3))) u32x4 *)at;
 }
 
 // 64 lanes bring N times 16 bytes each straight into LDS: lane l's x-th from base +
@@ -371,7 +375,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
             for (int r = 0; r < 16; ++r) o[j][r] = 0.f;
         float m = kNoMax, l = 0.f;
 
-        // Where this lane reads, in bytes of a tile.  Chunks of one row differ in
+        // Where this lane reads, in bytes of a tile (tiles start at multiples of
+        // 1024, so what follows holds for addresses, too).  Chunks of one row differ in
         // address bits of their own (the swizzle depends on the low bits of the row
         // alone), so operand j of K sits at (at_k ^ 32 j), and rows 32 further on at
         // a constant distance.  V is read transposed: a lane group of 16 brings keys
@@ -380,10 +385,10 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         const int dim_v = 16 * (lane >> 4 & 1) + 4 * (lane & 3);
         const uint32_t at_k = Tile::byte_of(col, half);
         const uint32_t at_v = Tile::byte_of(key_v, dim_v >> 3) + 2 * (dim_v & 7);
-        auto v_op = [&](const char *tile, uint32_t at, int t, int dt) {
-            const char *v = tile + 16 * t * Tile::kRowBytes;
-            const u32x2 x = read_transposed(v + (at ^ 64 * dt));
-            const u32x2 y = read_transposed(v + (at ^ (64 * dt ^ 32)) + 8 * Tile::kRowBytes);
+        auto v_op = [&](uint32_t at, int t, int dt) {  // at: at_v in a tile
+            const uint32_t row = 16 * t * Tile::kRowBytes;
+            const u32x2 x = read_transposed((at ^ 64 * dt) + row);
+            const u32x2 y = read_transposed((at ^ (64 * dt ^ 32)) + row + 8 * Tile::kRowBytes);
             return (u32x4){x[0], x[1], y[0], y[1]};
         };
 
@@ -415,7 +420,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         auto scores = [&](const char *sk, f32x16 *s) {
             // Opaque, so that the operands' addresses are formed where they are
             // used: kept from tile to tile they take some forty registers.
-            uint32_t ak = at_k;
+            uint32_t ak = lds_address(sk) + at_k;
             asm("" : "+v"(ak));
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -425,8 +430,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
             auto read_k = [&](u32x4 *d, int f0) {
 #pragma unroll
                 for (int f = 0; f < 4; ++f)
-                    d[f] = ld16(sk + 32 * ((f0 + f) & 1) * Tile::kRowBytes +
-                                (ak ^ 32 * ((f0 + f) >> 1)));
+                    d[f] = read_lds16((ak ^ 32 * ((f0 + f) >> 1)) +
+                                      32 * ((f0 + f) & 1) * Tile::kRowBytes);
             };
             read_k(kb[0], 0);
 #pragma unroll
@@ -533,16 +538,15 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                 }
             }
             const Seen see = seen_of(i);
-            next = offset_of(min(i + 2, i1 - 1));
             if (!see.whole) clean(see, sv);
             f32x16 s[2];
             scores(sk, s);
-            uint32_t av = at_v;
+            uint32_t av = lds_address(sv) + at_v;
             asm("" : "+v"(av));
             u32x4 vb[2][4];
             auto read_v = [&](u32x4 *d, int f0) {
 #pragma unroll
-                for (int f = 0; f < 4; ++f) d[f] = v_op(sv, av, (f0 + f) / DT, (f0 + f) % DT);
+                for (int f = 0; f < 4; ++f) d[f] = v_op(av, (f0 + f) / DT, (f0 + f) % DT);
             };
             read_v(vb[0], 0);
             if (!see.whole) hide(see, s);
@@ -594,6 +598,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                 __builtin_amdgcn_sched_barrier(0);
             }
             __builtin_amdgcn_s_setprio(0);
+            // Here, since behind a scalar load every wait for LDS is one for all of it.
+            next = offset_of(min(i + 2, i1 - 1));
             if constexpr (F8) {
                 if (more) {
                     convert(raw_k, s_k[buf ^ 1]);
@@ -644,7 +650,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                         for (int r = 0; r < 16; ++r) x[r] = 0.f;
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
-                            u32x4 v = v_op(s_v[0], at_v, t, dt);
+                            u32x4 v = v_op(lds_address(s_v[0]) + at_v, t, dt);
 #pragma unroll
                             for (int y = 0; y < 4; ++y) v[y] = marks_of<T>(v[y], sign);
                             x = T::mfma32(v, p[t], x);
