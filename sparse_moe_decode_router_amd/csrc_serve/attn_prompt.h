@@ -695,29 +695,50 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
             mine = s_last == (uint32_t)parts - 1;
             if (mine) {
                 if (tid == 0) store_agent(a.counters + group, 0u);
+                // Loads of several parts are on their way together: one after
+                // the other they cost most of a microsecond each.
+                const int ml = wave * 32 * (D + 2) + 32 * D + col;
                 m = kNoMax;
+                for (int k = 0; k < parts; k += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) x[y] = load_agent(slot_of(min(k + y, parts - 1)) + ml);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) m = fmaxf(m, x[y]);
+                }
                 l = 0.f;
-                for (int k = 0; k < parts; ++k)
-                    m = fmaxf(m, load_agent(slot_of(k) + wave * 32 * (D + 2) + 32 * D + col));
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) o[dt][r] = 0.f;
-                for (int k = 0; k < parts; ++k) {
-                    const float *ml = slot_of(k) + wave * 32 * (D + 2) + 32 * D + col;
-                    const float f = exp2_(load_agent(ml) - m);
-                    l += load_agent(ml + 32) * f;
-                    const rsrc_t of = buf_rsrc(slot_of(k));
+                constexpr int K = DT <= 4 ? 2 : 1;   // parts at a time
+                for (int k = 0; k < parts; k += K) {
+                    float pm[K], pl[K];
+                    f32x4 x[K][4 * DT];
 #pragma unroll
-                    for (int dt = 0; dt < DT; ++dt)
+                    for (int y = 0; y < K; ++y) {
+                        const float *slot = slot_of(min(k + y, parts - 1));
+                        const rsrc_t of = buf_rsrc(slot);
+                        pm[y] = load_agent(slot + ml);
+                        pl[y] = load_agent(slot + ml + 32);
 #pragma unroll
-                        for (int r = 0; r < 16; r += 4) {
-                            const f32x4 x = __builtin_bit_cast(
-                                f32x4,
-                                buf_ld16<true>(of, at_part + 1024 * (4 * dt + r / 4) + 16 * lane));
+                        for (int z = 0; z < 4 * DT; ++z)
+                            x[y][z] = __builtin_bit_cast(
+                                f32x4, buf_ld16<true>(of, at_part + 1024 * z + 16 * lane));
+                    }
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) o[dt][r + y] = fmaf(x[y], f, o[dt][r + y]);
-                        }
+                    for (int y = 0; y < K; ++y) {
+                        const float f = k + y < parts ? exp2_(pm[y] - m) : 0.f;
+                        l = fmaf(pl[y], f, l);
+#pragma unroll
+                        for (int z = 0; z < 4 * DT; ++z)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float sum = o[z >> 2][4 * (z & 3) + e];
+                                o[z >> 2][4 * (z & 3) + e] =
+                                    k + y < parts ? fmaf(x[y][z][e], f, sum) : sum;
+                            }
+                    }
                 }
             }
         }

@@ -2,6 +2,7 @@
 refusals of arguments, workspace sizes; and the 64-bit references the GPU tests
 rest on, against plain torch."""
 import ctypes
+import math
 import os
 import re
 
@@ -155,7 +156,8 @@ def test_a_space_for_more_tokens_serves_fewer(heads, kv_heads, dim, longest, win
         # split, as many as the chip holds at once, or two for each equal share.
         full, tiles = t * group // 128, t * group // 128 + min(3, t)
         sure = max(1, full) * kv_heads
-        split = max(1, min(slots // sure, -(-keys // 64) // 4, 64))
+        key_tiles = -(-keys // 64)
+        split = max(1, min(slots // sure, key_tiles // 4, math.isqrt(key_tiles - 1) + 1, 64))
         need = 2 * (slots // kv_heads) if sure > slots else tiles * split if split > 1 else 0
         assert w.value >= 4 * 128 * (dim + 2) * need * kv_heads
         assert n.value >= 4 * tiles * kv_heads
