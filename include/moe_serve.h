@@ -157,10 +157,7 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *cfg, i
  * scale is applied to each group's sum in f32, and y is rounded once. */
 moe_status moe_w4_linear(const void *x, int64_t x_stride, int32_t dtype, const uint8_t *codes,
                          const void *scales, const uint8_t *zeros, int32_t tokens, int32_t k,
-                         int32_t n, int32_t group, void *y, void *workspace, uint32_t *counters,
-                         moe_stream_t stream);
-moe_status moe_w4_workspace(int32_t tokens, int32_t k, int32_t n, size_t *workspace,
-                            size_t *counters);
+                         int32_t n, int32_t group, void *y, moe_stream_t stream);
 
 /* The HIP error behind the calling thread's last MOE_ERR_HIP. */
 int32_t moe_serve_last_hip_error(void);

@@ -23,6 +23,12 @@
 // blocks per unit = all visible blocks / the units aimed at, a multiple of
 // the workgroup's waves.  Rows that take one unit are written by it; of the
 // units of a longer row the last to arrive joins the others' results.
+//
+// Bound by memory: 64 sequences of up to 8192 on an e4m3 cache, 570 MB, take 126
+// us (4.6 TB/s), two of up to 131072 in bf16, 823 MB, 154 us (5.4 TB/s).  One
+// sequence of 1500 takes 8.8 us: a chain of length, pages, keys, the store of a
+// part, its arrival and the join, each about a memory latency (with the join's
+// loads one after the other it was 9.1).
 #pragma once
 
 #include "serve_common.h"

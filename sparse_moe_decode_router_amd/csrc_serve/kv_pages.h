@@ -3,8 +3,11 @@
 //
 // The bookkeeping of a call (which pages are free, who gets them) is done by
 // one workgroup: it is a scan over the pool's reference counts, 4096 of them a
-// round, and the results have to be the lowest pages in a fixed order.  The
-// pages' contents are moved by a second launch over the whole chip.
+// round, and the results have to be the lowest pages in a fixed order.  It is a
+// chain of dependent loads (fork of 32 pairs 6.5 us, compact of 1100 pages 6.0);
+// more workgroups would have to wait for each other several times.  The pages'
+// contents are moved by a second launch over the whole chip, bound by memory
+// (282 pages of 1 MB over 4 layers: 121 us, 4.9 TB/s).
 #pragma once
 
 #include "serve_common.h"
@@ -49,7 +52,9 @@ __device__ __forceinline__ u32x2 to_e4m3(u32x4 x, float scale) {
 
 // A workgroup takes `per_block` consecutive tokens, a thread chunks of eight
 // elements of one head's row (keys and values).  The first token's sequence is
-// found by bisection with uniform loads, later ones from there.
+// found by bisection with uniform loads, later ones from there.  Bound by memory:
+// 20750 tokens of 8 heads of 128 in bf16, 170 MB, take 37 us (4.6 TB/s); one
+// token of 64 sequences takes 3.3 us, most of it the launch.
 template <class T, bool F8>
 __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
     const int t0 = (int)blockIdx.x * a.per_block;

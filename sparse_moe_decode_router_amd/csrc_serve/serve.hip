@@ -86,7 +86,7 @@ int prompt_slots(int head_dim) { return kPlanCus * (head_dim <= 128 ? 2 : 1); }
 
 // Row tiles as workgroups, split over the keys where there are few of them.
 // With more of them than fit at once, long and short ones would leave the chip
-// part empty in the end (8192 tokens, window 4096, 14 heads: 18% of its time):
+// part empty in the end (8192 tokens, window 4096, 14 heads: 18% of their time):
 // then every workgroup takes an equal share of all tiles of keys.
 struct PromptPlan {
     int64_t tiles;
@@ -496,6 +496,7 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *c, int
     const PromptPlan p = prompt_plan(*kv, *c, tokens, c->batch);
     a.split = p.split;
     a.units = p.units;
+    a.row_tiles = (int32_t)std::min<int64_t>(p.tiles, 0x7FFFFFFF);
     if (p.slots && (!workspace || !counters)) return MOE_ERR_WORKSPACE;
     const int64_t grid = kv->kv_heads * (p.units ? p.units : p.tiles * p.split);
     if (grid >= 1ll << 31) return MOE_ERR_UNSUPPORTED;
@@ -508,19 +509,9 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *c, int
     });
 }
 
-moe_status moe_w4_workspace(int32_t tokens, int32_t k, int32_t n, size_t *workspace,
-                            size_t *counters) {
-    if (!workspace || !counters || tokens < 0 || k < 1 || n < 1) return MOE_ERR_INVALID_ARG;
-    *workspace = *counters = 0;
-    return MOE_OK;
-}
-
 moe_status moe_w4_linear(const void *x, int64_t x_stride, int32_t dtype, const uint8_t *codes,
                          const void *scales, const uint8_t *zeros, int32_t tokens, int32_t k,
-                         int32_t n, int32_t group, void *y, void *workspace, uint32_t *counters,
-                         moe_stream_t stream) {
-    (void)workspace;
-    (void)counters;
+                         int32_t n, int32_t group, void *y, moe_stream_t stream) {
     if ((dtype != MOE_BF16 && dtype != MOE_FP16) || !codes || !scales || tokens < 0 || k < 1 ||
         n < 1 || tokens > kMaxRows)
         return MOE_ERR_INVALID_ARG;

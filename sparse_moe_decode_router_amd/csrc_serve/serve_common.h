@@ -99,6 +99,7 @@ struct AttnArgs {
     int32_t window, sinks;
     int32_t split;             // decode: units aimed at per kv head; prompt: most splits
     int32_t units;             // prompt: equal shares per kv head (0: row tiles)
+    int32_t row_tiles;         // prompt: most of them that there are counters for
 };
 
 // Blocks of 2^L keys that a row at the last position of n sees: the first

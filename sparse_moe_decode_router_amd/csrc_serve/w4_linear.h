@@ -15,7 +15,13 @@
 // different rows, sixteen lines to a quarter of a wave: the texture addresser
 // takes 64 cycles for such a load instead of 16, and was what bounded the
 // kernel (9216 x 7168 codes, 8 tokens: 38 us).  So lanes load along the rows and
-// the wave reorders through LDS (17 us).
+// the wave reorders through LDS (17 us; 15 with more rows per workgroup).
+//
+// What bounds it then: a single token with 36864 rows streams its codes at 3.9
+// TB/s; with more tokens the vector unit, LDS and the addressers are each busy
+// for about half of the time (8 tokens) and nothing alone stands out, with 64
+// tokens x goes through LDS once per 32 weight rows.  More waves on a compute
+// unit, or more steps ahead, measured no faster.
 #pragma once
 
 #include "serve_common.h"

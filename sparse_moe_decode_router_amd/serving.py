@@ -23,7 +23,7 @@ STATUS = {-1: "invalid argument", -2: "unsupported shape or device", -3: "HIP er
 EXPORTED = ("moe_kv_validate", "moe_kv_append", "moe_kv_free", "moe_kv_scratch_size",
             "moe_kv_fork", "moe_kv_extend", "moe_kv_compact", "moe_attn_validate",
             "moe_attn_workspace", "moe_attn_decode", "moe_attn_prompt", "moe_w4_linear",
-            "moe_w4_workspace", "moe_serve_last_hip_error")
+            "moe_serve_last_hip_error")
 
 _lib = None
 
@@ -65,8 +65,7 @@ def lib() -> ctypes.CDLL:
         "moe_attn_workspace": [vp, vp, i32] + sizes,
         "moe_attn_decode": [vp, vp, i32, vp, i32, i64, i64, i32, vp, vp, vp, vp, vp],
         "moe_attn_prompt": [vp, vp, i32, vp, i32, i64, i64, i32, vp, i32, vp, vp, vp, vp, vp],
-        "moe_w4_linear": [vp, i64, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp],
-        "moe_w4_workspace": [i32, i32, i32] + sizes,
+        "moe_w4_linear": [vp, i64, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp],
         "moe_serve_last_hip_error": [],
     }
     for name in EXPORTED:

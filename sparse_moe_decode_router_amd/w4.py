@@ -55,5 +55,5 @@ class W4Linear:
         codes, scales, zeros = self._ptrs
         check(self._lib.moe_w4_linear(address, stride[0], self._dtype, codes, scales,
                                       zeros, tokens, self.k, self.n, self.group, out.data_ptr(),
-                                      None, None, raw_stream(self.device)), "w4")
+                                      raw_stream(self.device)), "w4")
         return out

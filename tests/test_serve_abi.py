@@ -106,7 +106,7 @@ def test_calls_refuse_before_any_launch():
     assert status("moe_kv_free", kv, None, 0, None) == 0
     w = lambda **k: status("moe_w4_linear", *{**dict(  # noqa: E731
         x=4096, xs=128, dtype=0, codes=4096, scales=4096, zeros=None, t=1, k=128, n=8, group=64,
-        y=4096, ws=None, ctr=None, stream=None), **k}.values())
+        y=4096, stream=None), **k}.values())
     for k in (dict(x=None), dict(x=8), dict(xs=12), dict(dtype=2), dict(codes=None), dict(y=None),
               dict(codes=8), dict(t=-1), dict(n=0)):
         assert w(**k) == -1, k
@@ -115,7 +115,7 @@ def test_calls_refuse_before_any_launch():
 
 
 def test_w4_refuses_strides_beyond_its_offsets():
-    args = lambda xs: (4096, xs, 0, 4096, 4096, None, 1, 128, 8, 64, 4096, None, None,  # noqa: E731
+    args = lambda xs: (4096, xs, 0, 4096, 4096, None, 1, 128, 8, 64, 4096,  # noqa: E731
                        None)
     assert status("moe_w4_linear", *args((1 << 25) + 8)) == -2
 
