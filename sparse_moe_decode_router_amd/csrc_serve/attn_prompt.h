@@ -79,17 +79,19 @@ __device__ __forceinline__ u32x4 read_lds16(uint32_t at) {
 // off[x] (+ 1024 x with Stride) to lds + 1024 x + 16 l.  In assembly and without any
 // output: behind the builtin the compiler waits for the copy before the next
 // read of LDS, also of another buffer.  Whoever reads the copy waits for vmcnt
-// itself.
+// itself.  The compiler does not look into it for hazards either: a base that a
+// vector instruction has just put into scalar registers (a restored spill) may
+// be read five wait states later.
 template <int N>
 __device__ __forceinline__ void copy_to_lds(const void *base, const uint32_t *off, uint32_t lds) {
     if constexpr (N == 1)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
                      :
                      : "s"(lds), "v"(off[0]), "s"(base)
                      : "memory", "m0");
     if constexpr (N == 2)
         asm volatile(
-            "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+            "s_mov_b32 m0, %0\n\ts_nop 4\n\t"
             "global_load_lds_dwordx4 %1, %3\n\t"
             "global_load_lds_dwordx4 %2, %3 offset:1024"
             :
@@ -97,7 +99,7 @@ __device__ __forceinline__ void copy_to_lds(const void *base, const uint32_t *of
             : "memory", "m0");
     if constexpr (N == 4)
         asm volatile(
-            "s_mov_b32 m0, %0\n\ts_nop 0\n\t"
+            "s_mov_b32 m0, %0\n\ts_nop 4\n\t"
             "global_load_lds_dwordx4 %1, %5\n\t"
             "global_load_lds_dwordx4 %2, %5 offset:1024\n\t"
             "global_load_lds_dwordx4 %3, %5 offset:2048\n\t"
