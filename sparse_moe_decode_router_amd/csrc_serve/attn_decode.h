@@ -21,7 +21,9 @@
 // Work split.  A unit is a run of blocks of one (sequence, kv head).  Lengths
 // live on the device, so every workgroup reads them and finds its own unit:
 // blocks per unit = all visible blocks / the units aimed at, a multiple of
-// the workgroup's waves.  Rows that take one unit are written by it; of the
+// the workgroup's waves, and more where one long row would be joined from
+// hundreds of parts (one sequence of 100000, 8 heads on 1: 782 parts 101 us, 87
+// parts 28 us).  Rows that take one unit are written by it; of the
 // units of a longer row the last to arrive joins the others' results.
 //
 // Bound by memory: 64 sequences of up to 8192 on an e4m3 cache, 570 MB, take 126
@@ -148,15 +150,23 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
         const int first = a.window > 0 ? max(0, n - a.window) : 0;
         return visible<5>(n, first, a.sinks);
     };
-    int sum = 0, n0 = 0;
+    int sum = 0, longest = 0, n0 = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         const int b = b0 + lane;
         n0 = b < a.batch ? min(max(a.lengths[b], 0), most) : 0;
-        sum += vis_of(n0).total;
+        const int total = vis_of(n0).total;
+        sum += total;
+        longest = max(longest, total);
     }
     sum = (int)uniform(wave_sum_i(sum));
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) longest = max(longest, __shfl_xor(longest, m));
     int c = (sum + a.split - 1) / a.split;
     c = max(1, (c + kDecodeWaves - 1) / kDecodeWaves) * kDecodeWaves;
+    // Joining a part takes 0.1 us, in one workgroup; a round of a unit's waves
+    // over four blocks takes half of one: no more parts than balance the two.
+    const int least = (int)uniform((uint32_t)__builtin_amdgcn_sqrtf(0.45f * (float)longest));
+    c = max(c, least / kDecodeWaves * kDecodeWaves);
     DecodeUnit u;
     u.b = -1;
     int base = 0;

@@ -43,6 +43,7 @@ DECODE = [
     ([500, 130], 1, 20, 128, 16, BF, BF, 100, 40),      # more than 16 heads per kv head
     ([5000], 1, 7, 128, 16, BF, BF, 0, 0),              # split over the cache
     ([3333, 40], 2, 2, 64, 64, FP, FP, 0, 0),
+    ([20011], 1, 3, 64, 128, BF, BF, 0, 0),             # fewer parts than the chip holds
     ([4100], 1, 4, 256, 128, BF, E4, 0, 0),
     ([5000, 3000], 1, 4, 96, 16, BF, BF, 2100, 100),
     ([(7 * i) % 40 for i in range(130)], 1, 2, 64, 16, BF, BF, 0, 0),   # over 64 sequences
