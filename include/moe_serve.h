@@ -23,7 +23,9 @@
  * t < sinks.  Query head i reads key-value head i / (q_heads / kv_heads).
  * lse is the natural logarithm of the sum of exponentials.  A row that sees
  * nothing gives zeros and -inf.  Keys and values that a row does not see have
- * no part in it, whatever they hold (NaN and infinities among them).
+ * no part in it, whatever they hold (NaN and infinities among them).  An
+ * infinite value that it sees makes its output that infinity, however small the
+ * weight; NaN, or infinities of both signs, make it NaN.
  *
  * Precision.  Products of 16-bit values are exact in f32; scores, the running
  * maximum and sum and the outputs are held in f32; the output is rounded once.

@@ -135,6 +135,48 @@ __device__ __forceinline__ void pv(const DecodeTile<T, F8, D> &t, u32x4 p_hi, u3
     }
 }
 
+// The sums over keys among whose values some are not finite, from 2 J on.
+// each(f) calls f(t0, t1, sees) for every block: its two halves of 16 values and
+// a bit for each of this lane's eight keys; put(j, r, sum) takes them.
+template <class T, int D, int J, class Each, class Put>
+__device__ __forceinline__ void sum_not_finite(Each each, Put put) {
+    if constexpr (J < D / 32) {
+        const int c = lane_id() & 15, g = lane_id() >> 4;
+        constexpr uint32_t one2 = T::kOne | T::kOne << 16;
+        const u32x4 ones = {one2, one2, one2, one2};
+        f32x4 x[2][2] = {{zero4(), zero4()}, {zero4(), zero4()}};
+        each([&](const char *t0, const char *t1, uint32_t sees) {
+            uint32_t w[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                w[r] = sees >> r & 1 ? *(const uint32_t *)((r < 4 ? t0 : t1) +
+                                                           (4 * g + (r & 3)) * (2 * D) +
+                                                           c * (D / 8) + 4 * J)
+                                     : 0u;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                u32x4 a, b;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t m0 = marks_of<T>(w[2 * i], s), m1 = marks_of<T>(w[2 * i + 1], s);
+                    a[i] = __builtin_amdgcn_perm(m1, m0, 0x05040100u);
+                    b[i] = __builtin_amdgcn_perm(m1, m0, 0x07060302u);
+                }
+                x[s][0] = T::mfma16(a, ones, x[s][0]);
+                x[s][1] = T::mfma16(b, ones, x[s][1]);
+            }
+        });
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool pos = x[0][j][r] != 0.f, neg = x[1][j][r] != 0.f;
+                if (pos || neg) put(2 * J + j, r, sum_of_marks(pos, neg));
+            }
+        sum_not_finite<T, D, J + 1>(each, put);
+    }
+}
+
 struct DecodeUnit {
     int b, n;        // sequence (-1: none), its length
     Visible vis;
@@ -251,6 +293,12 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
                ((x.key + 16 * t) & in_page) * (D * ES);
     };
 
+    // Whether key 16 (r / 4) + 4 g + r % 4 of a block is seen.
+    auto sees_of = [&](const Ids &x, int r) {
+        const int key = x.key + 16 * (r >> 2) + 4 * g + (r & 3);
+        return (key < u.n) & (x.p[r >> 2] < (uint32_t)a.pages) & ((key >= first) | (key < a.sinks));
+    };
+
     int i = u.i0 + wave;
     if (i < u.i1) {
         Tile t;
@@ -279,9 +327,7 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
             if (!whole) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const int key = now.key + 16 * (r >> 2) + 4 * g + (r & 3);
-                    const bool sees = (key < u.n) & (now.p[r >> 2] < (uint32_t)a.pages) &
-                                      ((key >= first) | (key < a.sinks));
+                    const bool sees = sees_of(now, r);
                     x[r] = sees ? x[r] : -__builtin_inff();
 #pragma unroll
                     for (int w = 0; w < Tile::VW; ++w) t.v[r][w] = sees ? t.v[r][w] : 0u;
@@ -329,6 +375,33 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
 #pragma unroll
             for (int j = 0; j < E; ++j) s_o[wave][c][dim_of<F8, D>(4 * g + r, j)] = o[j][r];
     }
+    // A visible value that is infinite has made NaN of its sums: the second half of
+    // a pair of weights is zero or negative, and weights and factors may be too
+    // small for their type.  By the definition they are positive, so the sum is
+    // that infinity, or NaN where both are seen.  Rare, so values are read again,
+    // without haste.  (e4m3 has no infinities, and NaN stays.)
+    if constexpr (!F8) {
+        float zero = 0.f;   // or NaN
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) zero = fmaf(o[j][r], 0.f, zero);
+        if (__any(zero != zero))
+            sum_not_finite<T, D, 0>(
+                [&](auto take) {
+#pragma unroll 1
+                    for (int y = u.i0 + wave; y < u.i1; y += W) {
+                        const Ids x = ids_of(y);
+                        uint32_t sees = 0;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) sees |= (uint32_t)sees_of(x, r) << r;
+                        take(at(a.v, x, 0), at(a.v, x, 1), sees);
+                    }
+                },
+                [&](int j, int r, float x) {
+                    if (c < n_heads) s_o[wave][c][dim_of<F8, D>(4 * g + r, j)] = x;
+                });
+    }
     __syncthreads();
     const float v_scale = F8 && a.v_scale ? a.v_scale[h] : 1.f;
     const int64_t out_row = (int64_t)u.b * a.kv_heads * a.group + head0;
@@ -350,7 +423,7 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
         float den = 0.f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float f = exp2_(s_m[w][head] - top);
+            const float f = part_factor(s_m[w][head] - top);
             sum += ldf4(&s_o[w][head][d]) * f;
             den += s_l[w][head] * f;
         }

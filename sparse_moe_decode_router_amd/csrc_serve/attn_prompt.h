@@ -112,18 +112,7 @@ __device__ __forceinline__ uint32_t lds_address(const char *p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
 }
 
-// What is not finite in two values: 1 (sign 0) or 2 (sign 1) marks, as values
-// that are one where v is +inf (or -inf) or NaN and zero elsewhere.
-template <class T>
-__device__ __forceinline__ uint32_t marks_of(uint32_t v, uint32_t sign) {
-    uint32_t out = 0;
-#pragma unroll
-    for (int z = 0; z < 32; z += 16) {
-        const uint32_t h = v >> z & 0xFFFFu;
-        out |= (T::odd(h) && (T::nan(h) || h >> 15 == sign) ? T::kOne : 0u) << z;
-    }
-    return out;
-}
+// Two values, those that are not finite as zero.
 template <class T>
 __device__ __forceinline__ uint32_t finite_of(uint32_t v) {
     return (T::odd(v) ? 0u : v & 0xFFFFu) | (T::odd(v >> 16) ? 0u : v & 0xFFFF0000u);
@@ -611,93 +600,130 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                 }
             }
         }
+        float zero = 0.f;   // or NaN
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) zero = fmaf(o[dt][r], 0.f, zero);
+        if (__any(zero != zero) && lane == 0) s_odd = 1;
         __syncthreads();
-        if (s_odd) {
-            // Values that are not finite, in tiles that some rows see and others do
-            // not: a row gets the infinity (for NaN both) of every one on which it
-            // has weight.  Rare, so each tile is brought again, without haste.
-#pragma unroll 1
-            for (int i = i0; i < i1; ++i) {
-                const Seen see = seen_of(i);
-                if (see.whole) continue;
-                const uint64_t off = offset_of(i);
-                __syncthreads();
-                if constexpr (F8) {
-                    fetch(k_head, raw_k, off);
-                    fetch(v_head, raw_v, off);
-                    convert(raw_k, s_k[0]);
-                    convert(raw_v, s_v[0]);
-                } else {
-                    copy_in(k_head, s_k[0], off);
-                    copy_in(v_head, s_v[0], off);
-                }
-                wait_vm_all();
-                __syncthreads();
-                f32x16 s[2];
-                scores(s_k[0], s);
-                hide(see, s);
-                u32x4 p[4];
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int r = 0; r < 16; r += 2)
-                        p[2 * u + (r >> 3)][(r & 7) >> 1] =
-                            T::pack(exp2_(fmaf(s[u][r], c2, T::kOff - m)),
-                                    exp2_(fmaf(s[u][r + 1], c2, T::kOff - m)));
-#pragma unroll 1
-                for (uint32_t sign = 0; sign < 2; ++sign) {
-                    const float add = sign ? -__builtin_inff() : __builtin_inff();
-#pragma unroll
-                    for (int dt = 0; dt < DT; ++dt) {
-                        f32x16 x;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x[r] = 0.f;
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            u32x4 v = v_op(lds_address(s_v[0]) + at_v, t, dt);
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) v[y] = marks_of<T>(v[y], sign);
-                            x = T::mfma32(v, p[t], x);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) o[dt][r] += x[r] != 0.f ? add : 0.f;
-                    }
-                }
-            }
-        }
+        const bool odd = s_odd;
         l += __shfl_xor(l, 32);
 
         const bool real = 32 * wave + col < rows;
-        bool mine = true;  // this workgroup writes the rows
+        uint16_t *op = (uint16_t *)a.out + out_row * D;
+        auto write = [&]() {
+            const float f = l != 0.f ? (F8 && a.v_scale ? a.v_scale[h] : 1.f) / l : 0.f;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4) {
+                    u32x2 w;
+                    if (l != 0.f)
+                        w = (u32x2){T::pack(o[dt][r] * f, o[dt][r + 1] * f),
+                                    T::pack(o[dt][r + 2] * f, o[dt][r + 3] * f)};
+                    else
+                        w = (u32x2){0, 0};
+                    *(u32x2 *)(op + 32 * dt + 2 * r + 4 * half) = w;
+                }
+            if (half == 0)
+                a.lse[out_row] = l != 0.f ? (m + log2_(l) - T::kOff) * kLn2 : -__builtin_inff();
+        };
+        // Parts are kept as the lanes hold them (the one that joins them has
+        // the same rows in the same places): every access is a whole block.
+        const uint32_t at_part = 4u * (wave * 32 * (D + 2));
         if (parts > 1) {
-            // Parts are kept as the lanes hold them (the one that joins them has
-            // the same rows in the same places): every access is a whole block.
-            const int64_t group = (int64_t)index * a.kv_heads + h;
-            const uint32_t at_part = 4u * (wave * 32 * (D + 2));
-            {
-                const rsrc_t to = buf_rsrc(slot_of(part));
+            const rsrc_t to = buf_rsrc(slot_of(part));
 #pragma unroll
-                for (int dt = 0; dt < DT; ++dt)
+            for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        const f32x4 x = {o[dt][r], o[dt][r + 1], o[dt][r + 2], o[dt][r + 3]};
-                        buf_st16<true>(to, at_part + 1024 * (4 * dt + r / 4) + 16 * lane,
-                                       __builtin_bit_cast(u32x4, x));
+                for (int r = 0; r < 16; r += 4) {
+                    const f32x4 x = {o[dt][r], o[dt][r + 1], o[dt][r + 2], o[dt][r + 3]};
+                    buf_st16<true>(to, at_part + 1024 * (4 * dt + r / 4) + 16 * lane,
+                                   __builtin_bit_cast(u32x4, x));
+                }
+            float *ml = slot_of(part) + wave * 32 * (D + 2) + 32 * D + col;
+            if (half == 0) {
+                store_agent(ml, m);
+                store_agent(ml + 32, l);
+            }
+        } else if (real) {
+            write();
+        }
+        if (odd) {
+            // Values that are not finite: a row's sum is the infinity (for NaN both)
+            // of all that it sees.  The products leave that out where tiles were
+            // cleaned, and make NaN of it where a weight or a factor is too small
+            // for its type.  Rare, so values are brought again, 32 dimensions at a
+            // time, and what was just written is written over.
+            wait_vm_all();
+            float *slot = slot_of(part) + wave * 32 * (D + 2) + 4 * lane;
+#pragma unroll 1
+            for (int dt = 0; dt < DT; ++dt) {
+                f32x16 x[2];   // how many of +inf and NaN, and of -inf and NaN
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[0][r] = x[1][r] = 0.f;
+#pragma unroll 1
+                for (int i = i0; i < i1; ++i) {
+                    const Seen see = seen_of(i);
+                    const uint64_t off = offset_of(i);
+                    __syncthreads();
+                    if constexpr (F8) {
+                        fetch(v_head, raw_v, off);
+                        convert(raw_v, s_v[0]);
+                    } else {
+                        copy_in(v_head, s_v[0], off);
                     }
-                float *ml = slot_of(part) + wave * 32 * (D + 2) + 32 * D + col;
-                if (half == 0) {
-                    store_agent(ml, m);
-                    store_agent(ml + 32, l);
+                    wait_vm_all();
+                    __syncthreads();
+                    f32x16 s[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) s[u][r] = 0.f;
+                    if (!see.whole) hide(see, s);
+                    u32x4 p[4];   // one for what the row sees
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < 16; r += 2)
+                            p[2 * u + (r >> 3)][(r & 7) >> 1] =
+                                (s[u][r] == 0.f ? T::kOne : 0u) |
+                                (s[u][r + 1] == 0.f ? T::kOne << 16 : 0u);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const u32x4 v = v_op(lds_address(s_v[0]) + at_v, t, dt);
+#pragma unroll
+                        for (int sign = 0; sign < 2; ++sign) {
+                            u32x4 marks;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) marks[y] = marks_of<T>(v[y], sign);
+                            x[sign] = T::mfma32(marks, p[t], x[sign]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    // (A row whose scores are not finite keeps its NaN.)
+                    if ((x[0][r] == 0.f && x[1][r] == 0.f) || l != l) continue;
+                    const float sum = sum_of_marks(x[0][r] != 0.f, x[1][r] != 0.f);
+                    if (parts > 1)
+                        store_agent(slot + 1024 * dt + 256 * (r / 4) + r % 4, sum);
+                    else if (real)
+                        op[32 * dt + 2 * (r & 12) + 4 * half + r % 4] =
+                            (uint16_t)T::pack(F8 && a.v_scale ? sum * a.v_scale[h] : sum, 0.f);
                 }
             }
+        }
+        if (parts > 1) {
+            const int64_t group = (int64_t)index * a.kv_heads + h;
             wait_vm_all();
             __syncthreads();
             if (tid == 0)
                 s_last = __hip_atomic_fetch_add(a.counters + group, 1u, __ATOMIC_RELAXED,
                                                 __HIP_MEMORY_SCOPE_AGENT);
             __syncthreads();
-            mine = s_last == (uint32_t)parts - 1;
-            if (mine) {
+            if (s_last == (uint32_t)parts - 1) {
                 if (tid == 0) store_agent(a.counters + group, 0u);
                 // Loads of several parts are on their way together: one after
                 // the other they cost most of a microsecond each.
@@ -732,7 +758,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                     }
 #pragma unroll
                     for (int y = 0; y < K; ++y) {
-                        const float f = k + y < parts ? exp2_(pm[y] - m) : 0.f;
+                        const float f = k + y < parts ? part_factor(pm[y] - m) : 0.f;
                         l = fmaf(pl[y], f, l);
 #pragma unroll
                         for (int z = 0; z < 4 * DT; ++z)
@@ -744,25 +770,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                             }
                     }
                 }
+                if (real) write();
             }
-        }
-        if (mine && real) {
-            const float f = l != 0.f ? (F8 && a.v_scale ? a.v_scale[h] : 1.f) / l : 0.f;
-            uint16_t *op = (uint16_t *)a.out + out_row * D;
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-                for (int r = 0; r < 16; r += 4) {
-                    u32x2 w;
-                    if (l != 0.f)
-                        w = (u32x2){T::pack(o[dt][r] * f, o[dt][r + 1] * f),
-                                    T::pack(o[dt][r + 2] * f, o[dt][r + 3] * f)};
-                    else
-                        w = (u32x2){0, 0};
-                    *(u32x2 *)(op + 32 * dt + 2 * r + 4 * half) = w;
-                }
-            if (half == 0)
-                a.lse[out_row] = l != 0.f ? (m + log2_(l) - T::kOff) * kLn2 : -__builtin_inff();
         }
         // On to the next row tile of an equal share.
         at += weight;

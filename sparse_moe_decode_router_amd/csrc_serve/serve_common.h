@@ -147,6 +147,28 @@ __device__ __forceinline__ void load_words(uint32_t *r, const void *p) {
     }
 }
 
+// The factor of a part whose maximum is `by` above the joined one (at most 0).
+// Never zero: an infinity stays one, since a weight is positive, however small.
+__device__ __forceinline__ float part_factor(float by) { return fmaxf(exp2_(by), 0x1p-149f); }
+
+// Which of two values are +inf (sign 0) or -inf (sign 1), or NaN: one where they
+// are, else zero.
+template <class T>
+__device__ __forceinline__ uint32_t marks_of(uint32_t v, uint32_t sign) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int z = 0; z < 32; z += 16) {
+        const uint32_t h = v >> z & 0xFFFFu;
+        out |= (T::odd(h) && (T::nan(h) || h >> 15 == sign) ? T::kOne : 0u) << z;
+    }
+    return out;
+}
+// The sum of values that are not finite: pos, neg: whether infinities of either
+// sign are among them (NaN counts as both).
+__device__ __forceinline__ float sum_of_marks(bool pos, bool neg) {
+    return pos ? (neg ? __builtin_nanf("") : __builtin_inff()) : -__builtin_inff();
+}
+
 // Joins the parts of a split row group.  Every part wrote `rows` rows of sums
 // [rows][D] and [rows] maxima and sums of weights with agent-scope stores, in
 // slots `stride` floats apart from `part`.  `write(row, d, f32x4)` and
@@ -194,7 +216,7 @@ __device__ __forceinline__ void join_parts(const float *part, int64_t stride, in
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                if (u + j < n_parts) sum += x[j] * exp2_(f[j] - m);
+                if (u + j < n_parts) sum += x[j] * part_factor(f[j] - m);
         }
         write(row, d, l != 0.f ? sum * (1.f / l) : zero4());
     }

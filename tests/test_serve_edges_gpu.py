@@ -1,0 +1,121 @@
+"""The serving operators on the GPU where inputs are unusual."""
+import math
+
+import pytest
+import torch
+
+import serve_util as su
+from sparse_moe_decode_router_amd import attention
+from test_serve_gpu import _gpu, queries  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+BF, FP, E4 = torch.bfloat16, torch.float16, su.E4M3
+
+
+def cumulative(new):
+    cu = [0]
+    for x in new:
+        cu.append(cu[-1] + x)
+    return cu
+
+
+def attend(kind, cache, q, cu, **plan):
+    """One call over the cache; the plan is made for its longest sequence."""
+    att = attention.PagedAttention(cache.gpu(), q.shape[1], len(cu) - 1,
+                                   max(1, int(cache.lengths.max())), **plan)
+    got = att.decode(0, q.cuda()) if kind == "decode" else \
+        att.prompt(0, q.cuda(), torch.tensor(cu, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    return got
+
+
+# ---- Values that are not finite ---------------------------------------------
+
+def plant(cache, spots):
+    """Puts values at (position, dimension) of sequence 0, head 0."""
+    for t, d, x in spots:
+        cache.data[0, 1, int(cache.tables[0, t // cache.page]), 0, t % cache.page, d] = x
+
+
+def check_planted(got, clean, q, cu, spots, rounded):
+    """Dimensions that hold planted values: their sum (a weight is positive,
+    however small) for rows that see them; all else as without them."""
+    out, lse = got[0].clone(), got[1]
+    want = su.attention(clean, 0, q, cu)
+    pos = int(clean.lengths[0]) - (cu[1] - cu[0]) + torch.arange(cu[1] - cu[0])
+    for d in {d for _, d, _ in spots}:
+        total = sum(torch.where(t <= pos, x, 0.0) for t, e, x in spots if e == d)
+        rows = ~total.isfinite()
+        seen = out[:cu[1], :, d].float().cpu()
+        for h in range(q.shape[1]):
+            assert torch.equal(seen[rows, h].nan_to_num(7.0, 8.0, 9.0),
+                               total[rows].nan_to_num(7.0, 8.0, 9.0)), (d, h)
+        patch = out[:cu[1], :, d]
+        patch[rows.cuda()] = want[0][:cu[1], :, d][rows].to(out.dtype).cuda()
+    su.check_attention((out, lse), want, q.dtype, rounded)
+
+
+def planted(n):
+    """(Of several at one place, in a sequence of one position, the last holds.)"""
+    inf = math.inf
+    spots = [(n // 3, 3, inf), (n // 3, 40, -inf), (n - 1, 17, math.nan), (0, 50, inf),
+            (n // 2, 50, inf), (n // 2, 60, inf), (n - 1, 60, -inf), (n - 1, 61, inf)]
+    return [(t, d, x) for (t, d), x in {(t, d): x for t, d, x in spots}.items()]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("lengths,dim,page", [([1], 64, 16), ([100, 7], 128, 16), ([96], 96, 32),
+                                              ([3000, 40], 128, 64), ([2000], 256, 16)])
+def test_decode_gives_the_infinities_that_it_sees(lengths, dim, page, dtype):
+    cache, clean = (su.HostCache(lengths, 1, page, dim, dtype, seed=40) for _ in range(2))
+    spots = planted(lengths[0])
+    plant(cache, spots)
+    cu = list(range(len(lengths) + 1))
+    q = queries((len(lengths), 3, dim), dtype, 41)
+    check_planted(attend("decode", cache, q, cu), clean, q, cu, spots, False)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("n,new,dim", [(400, 400, 128), (2500, 20, 64), (700, 300, 96)])
+def test_prompt_gives_the_infinities_that_it_sees(n, new, dim, dtype):
+    cache, clean = (su.HostCache([n, 33], 1, 16, dim, dtype, seed=42) for _ in range(2))
+    spots = planted(n)
+    plant(cache, spots)
+    cu = cumulative([new, 33])
+    q = queries((cu[-1], 2, dim), dtype, 43)
+    check_planted(attend("prompt", cache, q, cu), clean, q, cu, spots, True)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("factor", [1, 2, 4])
+@pytest.mark.parametrize("kind,n,new", [("decode", 300, 1), ("decode", 3000, 1),
+                                        ("prompt", 500, 200), ("prompt", 2500, 9)])
+def test_infinities_of_small_weights(kind, n, new, factor, dtype):
+    """Half of the keys point away from the query, so that their weights are
+    below what 16 bits hold, and then below what 32 bits hold."""
+    cache, clean = (su.HostCache([n], 1, 16, 128, dtype, seed=44) for _ in range(2))
+    q = queries((1, 1, 128), dtype, 45).expand(new, 1, 128).contiguous()
+    spots = [(5, 9, math.inf), (n // 4, 30, -math.inf), (n // 4 + 1, 31, math.inf),
+             (n // 4 + 2, 31, -math.inf)]
+    for c in (cache, clean):
+        for t in range(n // 2):
+            c.data[0, 0, int(c.tables[0, t // 16]), 0, t % 16] = -factor * q[0, 0]
+    plant(cache, spots)
+    cu = [0, new]
+    check_planted(attend(kind, cache, q, cu), clean, q, cu, spots, kind == "prompt")
+
+
+@pytest.mark.parametrize("kind", ["decode", "prompt"])
+@pytest.mark.parametrize("dim", [96, 128])
+def test_nan_codes_of_an_8_bit_cache(kind, dim):
+    n, new = 300, 1 if kind == "decode" else 150
+    cache, clean = (su.HostCache([n], 1, 16, dim, E4, seed=46) for _ in range(2))
+    spots = [(10, 5, math.nan), (n - new // 2 - 1, 80, math.nan)]
+    raw = cache.data.float()
+    for t, d, x in spots:
+        raw[0, 1, int(cache.tables[0, t // 16]), 0, t % 16, d] = x
+    cache.data = raw.to(E4)
+    cu = [0, new]
+    q = queries((new, 2, dim), BF, 47)
+    check_planted(attend(kind, cache, q, cu), clean, q, cu, spots, kind == "prompt")
