@@ -102,7 +102,8 @@ moe_status moe_kv_fork(const moe_kv_cache *kv, const int32_t *parents, const int
 /* Lengthens n distinct sequences by counts[i] >= 0 positions and gives them
  * the pages for it (the lowest free ones, in the order of the list; NULL seqs:
  * sequences 0 .. n - 1).  A sequence that pages or columns do not suffice for
- * keeps its length, and a flag is set.  The last page must not be shared. */
+ * keeps its length and takes no page, so that those after it may still get
+ * theirs, and a flag is set.  The last page must not be shared. */
 moe_status moe_kv_extend(const moe_kv_cache *kv, const int32_t *seqs, const int32_t *counts,
                          int32_t n, void *scratch, moe_stream_t stream);
 

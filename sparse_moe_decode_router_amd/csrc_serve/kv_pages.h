@@ -271,14 +271,29 @@ __global__ __launch_bounds__(kPagesThreads) void k_kv_extend(const PagesArgs a) 
     const int want = min(need, a.pages);
     const int found = take_lowest(a.pages, want, list, s_wave, [&](int p) { return a.refs[p] == 0; });
     __syncthreads();
+    if (found < need) {
+        // Too few for all: in the order of the list, who does not find enough left
+        // takes none.  Each choice depends on those before it, so one wave goes
+        // through them, 64 in its registers at a time.
+        for (int i0 = 0, used = 0; i0 < a.n && tid < 64; i0 += 64) {
+            const int i = i0 + tid, more = i < a.n ? ranks[2 * i + 1] : -1;
+            int at = 0;
+            for (int j = 0; j < 64; ++j) {
+                const int m = __builtin_amdgcn_readlane(more, j);
+                const bool fits = m <= found - used;
+                if (tid == j) at = fits ? used : -1;
+                if (fits) used += max(m, 0);
+            }
+            if (i < a.n) ranks[2 * i] = at;
+        }
+        __syncthreads();
+    }
     for (int i = tid; i < a.n; i += kPagesThreads) {
         const int at = ranks[2 * i], more = ranks[2 * i + 1];
         if (more < 0) continue;
-        if (at + more > found) {
-            if (more > 0) {
-                atomicOr(a.flags, (uint32_t)MOE_KV_FLAG_NO_PAGES);
-                continue;
-            }
+        if (more > 0 && at < 0) {
+            atomicOr(a.flags, (uint32_t)MOE_KV_FLAG_NO_PAGES);
+            continue;
         }
         const int s = seq(i), len = length_of(a, s);
         const int col = (len + up) >> a.page_log2;

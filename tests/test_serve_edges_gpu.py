@@ -6,7 +6,7 @@ import torch
 
 import serve_util as su
 from sparse_moe_decode_router_amd import attention
-from test_serve_gpu import _gpu, queries  # noqa: F401
+from test_serve_gpu import PageModel, _gpu, ints, queries  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,32 @@ def test_nan_codes_of_an_8_bit_cache(kind, dim):
     cu = [0, new]
     q = queries((new, 2, dim), BF, 47)
     check_planted(attend(kind, cache, q, cu), clean, q, cu, spots, kind == "prompt")
+
+
+# ---- Pools and tables ------------------------------------------------------
+
+def test_extend_serves_what_fits():
+    """Four free pages: a sequence that needs five of them goes without, and
+    takes none from those after it."""
+    cache = su.HostCache([20, 16, 3, 0, 30], 1, 16, 64, BF, spare=4, seed=50, clean=True,
+                         spare_cols=8)
+    m, kv = PageModel(cache), cache.gpu()
+    kv.extend(ints(80, 1, 5, 40, 40), ints(0, 1, 2, 3, 4))
+    m.extend([80, 1, 5, 40, 40], [0, 1, 2, 3, 4])
+    assert m.n.tolist() == [20, 17, 8, 40, 30]
+    m.same(kv)
+    assert kv.read_flags() == 1
+
+
+def test_extend_of_many_sequences_in_a_pool_too_small():
+    """More of them than a workgroup has threads; needs of none, few and many."""
+    g = torch.Generator().manual_seed(51)
+    lengths = torch.randint(0, 30, (1500,), generator=g).tolist()
+    cache = su.HostCache(lengths, 1, 16, 64, BF, spare=900, seed=51, clean=True, spare_cols=6)
+    m, kv = PageModel(cache), cache.gpu()
+    order = torch.randperm(1500, generator=g)[:1300].tolist()
+    counts = torch.randint(0, 60, (1300,), generator=g).tolist()
+    kv.extend(ints(*counts), ints(*order))
+    m.extend(counts, order)
+    m.same(kv)
+    assert kv.read_flags() == 1 and int((m.r == 0).sum()) < 5
