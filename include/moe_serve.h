@@ -93,9 +93,10 @@ size_t moe_kv_scratch_size(const moe_kv_cache *kv, int32_t n);
 /* Makes sequence children[i] a copy of parents[i], for n pairs; children are
  * distinct, hold nothing and are nobody's parent in the same call.  Full pages
  * are shared (one reference more); a last page that is not full is copied, in
- * every layer, into the lowest free page (in the order of the pairs).  Where
- * no page is free the child ends at its last full page, and the cache's flag
- * MOE_KV_FLAG_NO_PAGES is set. */
+ * every layer, into the lowest free page (in the order of the pairs); entries
+ * that are not pages are taken over as they are.  Where no page is free the
+ * child ends at its last full page, and the cache's flag MOE_KV_FLAG_NO_PAGES
+ * is set. */
 moe_status moe_kv_fork(const moe_kv_cache *kv, const int32_t *parents, const int32_t *children,
                        int32_t n, void *scratch, moe_stream_t stream);
 

@@ -116,7 +116,9 @@ struct PagesArgs {
 constexpr int kPagesThreads = 1024;
 constexpr int kPagesWaves = kPagesThreads / 64;
 
-// Scratch of fork: [0] pairs to copy, then (source, target) per pair.  Of
+// Scratch of fork: [0] pairs to copy, then (source, target) per pair (-1: none);
+// before that (rank among those that need a page, or -1: no last page in part, -2:
+// a missing one; length).  Of
 // extend and fork also the list of pages taken, from `list` on.  Of compact:
 // [0] pages to move, then the targets, the sources, and each page's new place.
 constexpr int kScratchHead = 4;
@@ -193,11 +195,16 @@ __global__ __launch_bounds__(kPagesThreads) void k_kv_fork(const PagesArgs a) {
         const int i = i0 + tid;
         const int len = i < a.n ? length_of(a, a.from[i]) : 0;
         const bool ok = i < a.n && a.to[i] >= 0 && a.to[i] < a.seqs;
-        const int part = ok && (len & (page - 1)) ? 1 : 0;
+        // A last page that the parent does not have needs no copy either.
+        const int part = ok && (len & (page - 1)) &&
+                                 (uint32_t)a.tables[(int64_t)a.from[i] * a.cols +
+                                                    (len >> a.page_log2)] < (uint32_t)a.pages
+                             ? 1
+                             : 0;
         int all;
         const int at = need + block_scan(part, &all, s_wave);
         if (i < a.n) {  // the rank and the length, until pages are known
-            copies[2 * i] = part ? at : -1;
+            copies[2 * i] = part ? at : len & (page - 1) ? -2 : -1;
             copies[2 * i + 1] = len;
         }
         need += all;
@@ -220,6 +227,8 @@ __global__ __launch_bounds__(kPagesThreads) void k_kv_fork(const PagesArgs a) {
         } else if (col == full && rank >= 0 && rank < found) {
             p = list[rank];
             a.refs[p] = 1;
+        } else if (col == full && rank == -2) {
+            p = a.tables[(int64_t)parent * a.cols + col];  // not a page
         }
         a.tables[(int64_t)child * a.cols + col] = p;
     }
@@ -232,7 +241,7 @@ __global__ __launch_bounds__(kPagesThreads) void k_kv_fork(const PagesArgs a) {
             src = a.tables[(int64_t)a.from[i] * a.cols + full];
             dst = list[rank];
         }
-        copies[2 * i] = src >= 0 && src < a.pages ? src : -1;
+        copies[2 * i] = src;
         copies[2 * i + 1] = dst;
         if (child >= 0 && child < a.seqs)
             a.lengths[child] = rank >= 0 && rank >= found ? full << a.page_log2 : len;

@@ -148,3 +148,25 @@ def test_extend_of_many_sequences_in_a_pool_too_small():
     m.extend(counts, order)
     m.same(kv)
     assert kv.read_flags() == 1 and int((m.r == 0).sum()) < 5
+
+
+def test_a_fork_keeps_a_missing_last_page_missing():
+    cache = su.HostCache([40, 40, 36, 0, 0, 0], 1, 16, 64, BF, spare=4, seed=52, clean=True)
+    cache.tables[0, 2] = -1                     # positions 32 .. 39 have no page
+    cache.tables[1, 2] = 10 ** 6
+    kv = cache.gpu()
+    before, refs = kv.data.clone(), kv.refs.cpu()
+    kv.fork(ints(0, 1, 2), ints(3, 4, 5))
+    torch.cuda.synchronize()
+    t = kv.tables.cpu()
+    assert torch.equal(t[3], t[0]) and torch.equal(t[4], t[1])
+    assert kv.lengths.tolist() == [40, 40, 36] * 2
+    free = int((refs == 0).nonzero()[0])        # the only page taken: the third child's
+    assert torch.equal(t[5, :3], torch.tensor([t[2, 0], t[2, 1], free], dtype=torch.int32))
+    for s in (0, 1, 2):
+        refs[cache.tables[s, :2].long()] += 1
+    refs[free] = 1
+    assert torch.equal(kv.refs.cpu(), refs)
+    before[:, :, free] = before[:, :, int(t[2, 2])]
+    assert torch.equal(kv.data.view(torch.int16), before.view(torch.int16))
+    assert kv.read_flags() == 0
