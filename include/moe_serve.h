@@ -78,10 +78,19 @@ moe_status moe_kv_validate(const moe_kv_cache *kv);
  * the last position of sequence i (a sequence of length 0 gets nothing).
  * Else cu is i32 [batch + 1] and tokens cu[b] .. cu[b + 1] - 1 are the last
  * positions of sequence b.  Into e4m3: code = e4m3(clamp(x / scale, -448,
- * 448)), to nearest even; NaN stays NaN. */
+ * 448)), to nearest even; NaN stays NaN.
+ * A sequence that extend could not lengthen has no new positions: its tokens
+ * would be written over its last ones, which in a full page may be those of the
+ * sequences that share it.  The second form takes what extend granted, i32
+ * [seqs] by sequence (NULL: as the first), and writes nothing for a sequence
+ * that has more tokens in the call than it was granted positions. */
 moe_status moe_kv_append(const moe_kv_cache *kv, int32_t layer, const void *k, const void *v,
                          int32_t dtype, int64_t token_stride, int64_t head_stride, int32_t tokens,
                          const int32_t *cu, int32_t batch, moe_stream_t stream);
+moe_status moe_kv_append_granted(const moe_kv_cache *kv, int32_t layer, const void *k,
+                                 const void *v, int32_t dtype, int64_t token_stride,
+                                 int64_t head_stride, int32_t tokens, const int32_t *cu,
+                                 int32_t batch, const int32_t *granted, moe_stream_t stream);
 
 /* Gives back the pages of n distinct sequences: each of their pages loses one
  * reference, their rows become -1 and their lengths 0. */
@@ -104,9 +113,15 @@ moe_status moe_kv_fork(const moe_kv_cache *kv, const int32_t *parents, const int
  * the pages for it (the lowest free ones, in the order of the list; NULL seqs:
  * sequences 0 .. n - 1).  A sequence that pages or columns do not suffice for
  * keeps its length and takes no page, so that those after it may still get
- * theirs, and a flag is set.  The last page must not be shared. */
+ * theirs, and a flag is set.  The last page must not be shared.  The second form
+ * also writes the positions that each of the sequences was given, counts[i] or
+ * none, to granted[its number] (i32 [seqs], NULL: as the first; the others'
+ * entries stay as they are). */
 moe_status moe_kv_extend(const moe_kv_cache *kv, const int32_t *seqs, const int32_t *counts,
                          int32_t n, void *scratch, moe_stream_t stream);
+moe_status moe_kv_extend_granted(const moe_kv_cache *kv, const int32_t *seqs,
+                                 const int32_t *counts, int32_t n, int32_t *granted,
+                                 void *scratch, moe_stream_t stream);
 
 /* Moves the pages in use together: with m pages in use, the i-th free page
  * below m receives the i-th used page from m on, in every layer.  new_tables

@@ -83,6 +83,9 @@ class PagedKV:
         self.seqs, self.cols = seqs, cols
         self.compute_dtypes = (torch.bfloat16, torch.float16) if f8 else (data.dtype,)
         self.flags = torch.zeros(1, dtype=torch.int32, device=dev)
+        # positions that a sequence's last extend gave it (before any: no limit)
+        self.granted = torch.full((seqs,), 2 ** 31 - 1, dtype=torch.int32, device=dev)
+        self._granted_ptr = self.granted.data_ptr()
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self.struct = Cache(data.data_ptr(), tables.data_ptr(), lengths.data_ptr(),
                             refs.data_ptr(), ptr(k_scale), ptr(v_scale), self.flags.data_ptr(),
@@ -112,11 +115,15 @@ class PagedKV:
             raise MoEError(f"{name}: {t.shape[0]} entries for {self.seqs} sequences")
         return t.shape[0]
 
-    def append(self, layer: int, k, v, cu=None) -> None:
+    def append(self, layer: int, k, v, cu=None, only_granted: bool = False) -> None:
         """Writes keys and values [tokens, kv_heads, head_dim] of new tokens,
         which the lengths count already.  cu None: token i is sequence i's last
         position (where it has none, nothing is written); else cu [batch + 1]
-        i32: tokens cu[b] .. cu[b + 1] - 1 are sequence b's last positions."""
+        i32: tokens cu[b] .. cu[b + 1] - 1 are sequence b's last positions.
+        A sequence that extend could not lengthen has no new positions, and its
+        tokens would go over its last ones, also in a full page that others
+        share.  only_granted: nothing is written for a sequence with more
+        tokens than its last extend gave it positions."""
         ts, hs = _rows(k, "k", self.kv_heads, self.head_dim, self.compute_dtypes, self.device)
         if _rows(v, "v", self.kv_heads, self.head_dim, (k.dtype,), self.device) != (ts, hs) or \
                 v.shape != k.shape:
@@ -134,10 +141,10 @@ class PagedKV:
                                f"{tuple(cu.shape)}")
         if not 0 <= layer < self.layers:
             raise MoEError(f"layer {layer} of {self.layers}")
-        check(self._lib.moe_kv_append(self._ref, layer, k.data_ptr(), v.data_ptr(),
-                                      DTYPES[k.dtype], ts, hs, tokens,
-                                      None if cu is None else cu.data_ptr(), batch,
-                                      raw_stream(self.device)), "append")
+        check(self._lib.moe_kv_append_granted(
+            self._ref, layer, k.data_ptr(), v.data_ptr(), DTYPES[k.dtype], ts, hs, tokens,
+            None if cu is None else cu.data_ptr(), batch,
+            self._granted_ptr if only_granted else None, raw_stream(self.device)), "append")
 
     def free(self, seqs) -> None:
         """Gives up the (distinct) sequences of an i32 list."""
@@ -154,13 +161,15 @@ class PagedKV:
 
     def extend(self, counts, seqs=None) -> None:
         """Lengthens sequences (the first ones, or the distinct ones of the list
-        seqs) by counts[i] positions, with pages for them."""
+        seqs) by counts[i] positions, with pages for them.  One that pages or
+        columns do not suffice for stays as it is; ``granted`` [seqs] holds what
+        each sequence's last call gave it, counts[i] or 0."""
         n = self._list(counts, "counts")
         if seqs is not None:
             self._list(seqs, "seqs", n)
-        check(self._lib.moe_kv_extend(self._ref, None if seqs is None else seqs.data_ptr(),
-                                      counts.data_ptr(), n, self._scratch_ptr,
-                                      raw_stream(self.device)), "extend")
+        check(self._lib.moe_kv_extend_granted(
+            self._ref, None if seqs is None else seqs.data_ptr(), counts.data_ptr(), n,
+            self._granted_ptr, self._scratch_ptr, raw_stream(self.device)), "extend")
 
     def compact(self, out=None) -> None:
         """Moves the used pages to the front of the pool.  out (tables, refs):

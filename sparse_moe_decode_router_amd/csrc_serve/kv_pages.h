@@ -20,6 +20,7 @@ struct AppendArgs {
     const void *k, *v;
     void *kc, *vc;             // the layer's pages
     const int32_t *tables, *lengths, *cu;
+    const int32_t *granted;    // or NULL: positions that a sequence was given
     const float *k_scale, *v_scale;
     int64_t token_stride, head_stride;
     int32_t tokens, batch, pages, cols, page_log2, kv_heads, head_dim;
@@ -73,16 +74,17 @@ __global__ __launch_bounds__(256) void k_kv_append(const AppendArgs a) {
     const int most = a.cols << a.page_log2;
     for (int x = threadIdx.x; x < (t1 - t0) * per_token; x += 256) {
         const int t = t0 + x / per_token, ch = x % per_token;
-        int b = t, pos;
+        int b = t, pos, n_new = 1;
         if (a.cu) {
             b = b0;
             while (b + 1 < a.batch && a.cu[b + 1] <= t) ++b;
             if (t < a.cu[b] || t >= a.cu[b + 1]) continue;
+            n_new = a.cu[b + 1] - a.cu[b];
             pos = a.lengths[b] - (a.cu[b + 1] - t);
         } else {
             pos = a.lengths[b] - 1;
         }
-        if (pos < 0 || pos >= most) continue;
+        if (pos < 0 || pos >= most || (a.granted && a.granted[b] < n_new)) continue;
         const uint32_t page = (uint32_t)a.tables[(int64_t)b * a.cols + (pos >> a.page_log2)];
         if (page >= (uint32_t)a.pages) continue;
         const int h = ch / per_head, d = 8 * (ch % per_head);
@@ -108,6 +110,7 @@ struct PagesArgs {
     uint32_t *flags;
     const int32_t *from, *to;      // fork: parents, children; extend / free: from = seqs
     const int32_t *counts;         // extend
+    int32_t *granted;              // extend: by sequence, or NULL
     int32_t *new_tables, *new_refs;  // compact
     int32_t *scratch;
     int32_t n, pages, page_log2, seqs, cols;
@@ -265,6 +268,7 @@ __global__ __launch_bounds__(kPagesThreads) void k_kv_extend(const PagesArgs a) 
                 more = (int)((to + up) >> a.page_log2) - ((len + up) >> a.page_log2);
             else if (s >= 0 && s < a.seqs) {
                 atomicOr(a.flags, (uint32_t)MOE_KV_FLAG_NO_COLS);
+                if (a.granted) a.granted[s] = 0;
                 more = -1;
             } else
                 more = -1;
@@ -300,17 +304,20 @@ __global__ __launch_bounds__(kPagesThreads) void k_kv_extend(const PagesArgs a) 
     for (int i = tid; i < a.n; i += kPagesThreads) {
         const int at = ranks[2 * i], more = ranks[2 * i + 1];
         if (more < 0) continue;
+        const int s = seq(i);
         if (more > 0 && at < 0) {
             atomicOr(a.flags, (uint32_t)MOE_KV_FLAG_NO_PAGES);
+            if (a.granted) a.granted[s] = 0;
             continue;
         }
-        const int s = seq(i), len = length_of(a, s);
+        const int len = length_of(a, s);
         const int col = (len + up) >> a.page_log2;
         for (int j = 0; j < more; ++j) {
             a.tables[(int64_t)s * a.cols + col + j] = list[at + j];
             a.refs[list[at + j]] = 1;
         }
         a.lengths[s] = len + max(a.counts[i], 0);
+        if (a.granted) a.granted[s] = max(a.counts[i], 0);
     }
 }
 

@@ -285,6 +285,14 @@ moe_status moe_kv_validate(const moe_kv_cache *kv) {
 moe_status moe_kv_append(const moe_kv_cache *kv, int32_t layer, const void *k, const void *v,
                          int32_t dtype, int64_t token_stride, int64_t head_stride, int32_t tokens,
                          const int32_t *cu, int32_t batch, moe_stream_t stream) {
+    return moe_kv_append_granted(kv, layer, k, v, dtype, token_stride, head_stride, tokens, cu,
+                                 batch, nullptr, stream);
+}
+
+moe_status moe_kv_append_granted(const moe_kv_cache *kv, int32_t layer, const void *k,
+                                 const void *v, int32_t dtype, int64_t token_stride,
+                                 int64_t head_stride, int32_t tokens, const int32_t *cu,
+                                 int32_t batch, const int32_t *granted, moe_stream_t stream) {
     moe_status s = moe_kv_validate(kv);
     if (s != MOE_OK) return s;
     if (layer < 0 || layer >= kv->layers || tokens < 0 || batch < 0 || batch > kv->seqs ||
@@ -306,6 +314,7 @@ moe_status moe_kv_append(const moe_kv_cache *kv, int32_t layer, const void *k, c
     a.tables = kv->tables;
     a.lengths = kv->lengths;
     a.cu = cu;
+    a.granted = granted;
     a.k_scale = kv->k_scale;
     a.v_scale = kv->v_scale;
     a.token_stride = token_stride;
@@ -372,6 +381,12 @@ moe_status moe_kv_fork(const moe_kv_cache *kv, const int32_t *parents, const int
 
 moe_status moe_kv_extend(const moe_kv_cache *kv, const int32_t *seqs, const int32_t *counts,
                          int32_t n, void *scratch, moe_stream_t stream) {
+    return moe_kv_extend_granted(kv, seqs, counts, n, nullptr, scratch, stream);
+}
+
+moe_status moe_kv_extend_granted(const moe_kv_cache *kv, const int32_t *seqs,
+                                 const int32_t *counts, int32_t n, int32_t *granted,
+                                 void *scratch, moe_stream_t stream) {
     moe_status s = moe_kv_validate(kv);
     if (s != MOE_OK) return s;
     if (n < 0 || n > kv->seqs) return MOE_ERR_INVALID_ARG;
@@ -381,6 +396,7 @@ moe_status moe_kv_extend(const moe_kv_cache *kv, const int32_t *seqs, const int3
     PagesArgs a = pages_args(*kv, n, scratch);
     a.from = seqs;
     a.counts = counts;
+    a.granted = granted;
     k_kv_extend<<<1, kPagesThreads, 0, stream>>>(a);
     return launched();
 }

@@ -53,10 +53,11 @@ class ServeLayer:
     def attend(self, x, cu=None):
         """The attention half for new tokens x [tokens, hidden] (bf16) that the
         lengths count already: of sequence i token i (cu None), or those that cu
-        says.  Returns x + out_rows(attention)."""
+        says.  Returns x + out_rows(attention).  Nothing is written for sequences
+        that could not be lengthened (their rows mean nothing: kv.granted)."""
         q, kv = self.q_heads, self.kv_heads
         y = self.qkv(x).unflatten(1, (-1, self.head_dim))
-        self.kv.append(0, y[:, q:q + kv], y[:, q + kv:], cu)
+        self.kv.append(0, y[:, q:q + kv], y[:, q + kv:], cu, only_granted=True)
         a, _ = self.attention.decode(0, y[:, :q]) if cu is None else \
             self.attention.prompt(0, y[:, :q], cu)
         return x + self.out(a.flatten(1))

@@ -20,10 +20,10 @@ LIB_PATH = os.path.join(HERE, "libmoe_serve.so")
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 STATUS = {-1: "invalid argument", -2: "unsupported shape or device", -3: "HIP error",
           -4: "workspace missing, too small or misaligned"}
-EXPORTED = ("moe_kv_validate", "moe_kv_append", "moe_kv_free", "moe_kv_scratch_size",
-            "moe_kv_fork", "moe_kv_extend", "moe_kv_compact", "moe_attn_validate",
-            "moe_attn_workspace", "moe_attn_decode", "moe_attn_prompt", "moe_w4_linear",
-            "moe_serve_last_hip_error")
+EXPORTED = ("moe_kv_validate", "moe_kv_append", "moe_kv_append_granted", "moe_kv_free",
+            "moe_kv_scratch_size", "moe_kv_fork", "moe_kv_extend", "moe_kv_extend_granted",
+            "moe_kv_compact", "moe_attn_validate", "moe_attn_workspace", "moe_attn_decode",
+            "moe_attn_prompt", "moe_w4_linear", "moe_serve_last_hip_error")
 
 _lib = None
 
@@ -56,10 +56,12 @@ def lib() -> ctypes.CDLL:
     args = {
         "moe_kv_validate": [vp],
         "moe_kv_append": [vp, i32, vp, vp, i32, i64, i64, i32, vp, i32, vp],
+        "moe_kv_append_granted": [vp, i32, vp, vp, i32, i64, i64, i32, vp, i32, vp, vp],
         "moe_kv_free": [vp, vp, i32, vp],
         "moe_kv_scratch_size": [vp, i32],
         "moe_kv_fork": [vp, vp, vp, i32, vp, vp],
         "moe_kv_extend": [vp, vp, vp, i32, vp, vp],
+        "moe_kv_extend_granted": [vp, vp, vp, i32, vp, vp, vp],
         "moe_kv_compact": [vp, vp, vp, vp, vp],
         "moe_attn_validate": [vp, vp],
         "moe_attn_workspace": [vp, vp, i32] + sizes,

@@ -170,3 +170,55 @@ def test_a_fork_keeps_a_missing_last_page_missing():
     before[:, :, free] = before[:, :, int(t[2, 2])]
     assert torch.equal(kv.data.view(torch.int16), before.view(torch.int16))
     assert kv.read_flags() == 0
+
+
+@pytest.mark.parametrize("cdtype", [BF, E4])
+@pytest.mark.parametrize("many", [False, True])
+def test_a_sequence_without_room_writes_over_nobody(many, cdtype):
+    """Two sequences share full pages and one page is left: the second cannot be
+    lengthened, and its new tokens go nowhere (not over the last shared ones)."""
+    cache = su.HostCache([32, 0, 40], 2, 16, 64, cdtype, spare=1, seed=53, clean=True)
+    new = [3, 4, 5] if many else [1, 1, 1]
+    kv = cache.gpu()
+    kv.fork(ints(0), ints(1))
+    kv.extend(ints(*new))
+    torch.cuda.synchronize()
+    assert kv.granted.tolist() == [new[0], 0, new[2]]
+    assert kv.lengths.tolist() == [32 + new[0], 32, 40 + new[2]] and kv.read_flags() == 1
+    bits = lambda: kv.data.view(torch.uint8).cpu().view(kv.dtype).float()  # noqa: E731
+    want = bits()
+    k, v = (queries((sum(new), 2, 64), BF, s).cuda() for s in (54, 55))
+    cu = cumulative(new)
+    kv.append(0, k, v, ints(*cu) if many else None, only_granted=True)
+    t = kv.tables.tolist()
+    for b in (0, 2):
+        for i in range(new[b]):
+            pos = int(kv.lengths[b]) - new[b] + i
+            for w, (x, s) in enumerate(((k, kv.k_scale), (v, kv.v_scale))):
+                row = x[cu[b] + i].float()
+                row = row if s is None else (row / s[:, None]).to(E4).float()
+                want[0, w, t[b][pos // 16], :, pos % 16] = row.cpu()
+    assert torch.equal(bits(), want)
+
+
+def test_a_layer_without_room_leaves_the_others_alone():
+    """The served layer with a pool for one of two forked sequences: the other
+    goes on as with room for both."""
+    from sparse_moe_decode_router_amd import binding, serve_layer, synth
+    got = []
+    for pages in (3, 40):
+        moe = binding.DeviceLayer(synth.make_layer(synth.TINY, 0), device="cuda:0")
+        layer = serve_layer.ServeLayer(moe, seqs=2, cols=8, pages=pages, seed=3)
+        g = torch.Generator().manual_seed(56)
+        new = lambda n: torch.randn((n, moe.dims.hidden), generator=g).to(BF).cuda()  # noqa: E731
+        layer.kv.extend(ints(32))
+        layer.attend(new(32), ints(0, 32))
+        layer.kv.fork(ints(0), ints(1))
+        for _ in range(3):
+            layer.kv.extend(ints(1, 1))
+            rows = layer.attend(new(2))
+        got.append(rows[0].clone())
+        assert layer.kv.lengths.tolist() == ([35, 32] if pages == 3 else [35, 35])
+        assert layer.kv.granted.tolist() == ([1, 0] if pages == 3 else [1, 1])
+        layer.close()
+    assert torch.equal(*got)
