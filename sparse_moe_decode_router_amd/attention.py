@@ -12,9 +12,10 @@ library's operators on them:
   compact  the pages in use moved together
 
 ``PagedAttention`` plans attention over such a cache: ``decode`` for one new
-token per sequence, ``prompt`` for many.  All of it runs on the current stream,
-reads lengths and tables on the device and never waits for it, so calls can be
-captured into a HIP graph.  include/moe_serve.h states layouts and formulas.
+token per sequence, ``prompt`` for many.  All of it runs on the cache's device,
+on that device's current stream, reads lengths and tables on the device and
+never waits for it, so calls can be captured into a HIP graph.
+include/moe_serve.h states layouts and formulas.
 """
 from __future__ import annotations
 
@@ -24,10 +25,13 @@ from typing import Optional, Tuple
 import torch
 
 from .binding import MoEError
-from .serving import (DTYPES, AttnConfig, Cache, StreamSpace, check, lib, raw_stream, require,
-                      tensor)
+from .serving import (DTYPES, AttnConfig, Cache, StreamSpace, check, current_device, lib,
+                      raw_stream, require, tensor)
 
 E4M3_MAX = 448.0
+
+# A kernel goes to the current device, and the default stream's handle, zero, is that
+# of every device: each method that launches one makes its tensors' device current.
 
 
 def _rows(t, name, heads, dim, dtypes, device) -> Tuple[int, int]:
@@ -77,7 +81,7 @@ class PagedKV:
                 tensor(t, name, torch.float32, (heads,), dev)
         self.data, self.tables, self.lengths, self.refs = data, tables, lengths, refs
         self.k_scale, self.v_scale = k_scale, v_scale
-        self.device, self.dtype = dev, data.dtype
+        self.device, self.dtype, self._index = dev, data.dtype, dev.index
         self.layers, self.pages, self.kv_heads, self.page, self.head_dim = \
             layers, pages, heads, page, dim
         self.seqs, self.cols = seqs, cols
@@ -124,6 +128,9 @@ class PagedKV:
         tokens would go over its last ones, also in a full page that others
         share.  only_granted: nothing is written for a sequence with more
         tokens than its last extend gave it positions."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.append(layer, k, v, cu, only_granted)
         ts, hs = _rows(k, "k", self.kv_heads, self.head_dim, self.compute_dtypes, self.device)
         if _rows(v, "v", self.kv_heads, self.head_dim, (k.dtype,), self.device) != (ts, hs) or \
                 v.shape != k.shape:
@@ -144,42 +151,54 @@ class PagedKV:
         check(self._lib.moe_kv_append_granted(
             self._ref, layer, k.data_ptr(), v.data_ptr(), DTYPES[k.dtype], ts, hs, tokens,
             None if cu is None else cu.data_ptr(), batch,
-            self._granted_ptr if only_granted else None, raw_stream(self.device)), "append")
+            self._granted_ptr if only_granted else None, raw_stream(self._index)), "append")
 
     def free(self, seqs) -> None:
         """Gives up the (distinct) sequences of an i32 list."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.free(seqs)
         n = self._list(seqs, "seqs")
-        check(self._lib.moe_kv_free(self._ref, seqs.data_ptr(), n, raw_stream(self.device)), "free")
+        check(self._lib.moe_kv_free(self._ref, seqs.data_ptr(), n, raw_stream(self._index)), "free")
 
     def fork(self, parents, children) -> None:
         """Sequence children[i], which holds nothing, becomes a copy of
         parents[i]: full pages are shared, a part-filled last page is copied."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.fork(parents, children)
         n = self._list(parents, "parents")
         self._list(children, "children", n)
         check(self._lib.moe_kv_fork(self._ref, parents.data_ptr(), children.data_ptr(), n,
-                                    self._scratch_ptr, raw_stream(self.device)), "fork")
+                                    self._scratch_ptr, raw_stream(self._index)), "fork")
 
     def extend(self, counts, seqs=None) -> None:
         """Lengthens sequences (the first ones, or the distinct ones of the list
         seqs) by counts[i] positions, with pages for them.  One that pages or
         columns do not suffice for stays as it is; ``granted`` [seqs] holds what
         each sequence's last call gave it, counts[i] or 0."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.extend(counts, seqs)
         n = self._list(counts, "counts")
         if seqs is not None:
             self._list(seqs, "seqs", n)
         check(self._lib.moe_kv_extend_granted(
             self._ref, None if seqs is None else seqs.data_ptr(), counts.data_ptr(), n,
-            self._granted_ptr, self._scratch_ptr, raw_stream(self.device)), "extend")
+            self._granted_ptr, self._scratch_ptr, raw_stream(self._index)), "extend")
 
     def compact(self, out=None) -> None:
         """Moves the used pages to the front of the pool.  out (tables, refs):
         where the new tables and references go; None: into the cache's own."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.compact(out)
         tables, refs = out if out is not None else (self.tables, self.refs)
         if out is not None:
             tensor(tables, "out tables", torch.int32, (self.seqs, self.cols), self.device)
             tensor(refs, "out refs", torch.int32, (self.pages,), self.device)
         check(self._lib.moe_kv_compact(self._ref, tables.data_ptr(), refs.data_ptr(),
-                                       self._scratch_ptr, raw_stream(self.device)), "compact")
+                                       self._scratch_ptr, raw_stream(self._index)), "compact")
 
     def read_flags(self) -> int:
         """Sticky flags (waits for the device): 1 fork or extend found too few
@@ -197,6 +216,7 @@ class PagedAttention:
     def __init__(self, kv: PagedKV, q_heads: int, batch: int, longest: int, window: int = 0,
                  sinks: int = 0, scale: Optional[float] = None):
         self.kv, self.q_heads, self.batch = kv, q_heads, batch
+        self.device, self._index = kv.device, kv.device.index
         self.config = AttnConfig(q_heads, batch, longest, window, sinks,
                                  kv.head_dim ** -0.5 if scale is None else scale)
         self._cfg, self._lib = ctypes.addressof(self.config), lib()
@@ -214,6 +234,9 @@ class PagedAttention:
         """q [batch, q_heads, head_dim], one new token of each of the first
         sequences, whose keys and values are in the cache.  Returns (out, like
         q; lse [batch, q_heads] f32)."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.decode(layer, q)
         kv = self.kv
         ts, hs = _rows(q, "q", self.q_heads, kv.head_dim, kv.compute_dtypes, kv.device)
         batch = q.shape[0]
@@ -223,7 +246,7 @@ class PagedAttention:
             raise MoEError(f"layer {layer} of {kv.layers}")
         out = torch.empty(q.shape, dtype=q.dtype, device=kv.device)
         lse = torch.empty((batch, self.q_heads), dtype=torch.float32, device=kv.device)
-        stream = raw_stream(kv.device)
+        stream = raw_stream(self._index)
         w, c, _ = self._decode.get(stream)
         check(self._lib.moe_attn_decode(kv._ref, self._cfg, layer, q.data_ptr(), DTYPES[q.dtype],
                                         ts, hs, batch, out.data_ptr(), lse.data_ptr(), w, c,
@@ -235,6 +258,9 @@ class PagedAttention:
         cu[b + 1] - 1 are the last positions of sequence b (at most max_new of
         them, where it is given).  Returns (out, like q; lse [tokens, q_heads]
         f32); rows that cu leaves out are not written."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.prompt(layer, q, cu, max_new)
         kv = self.kv
         ts, hs = _rows(q, "q", self.q_heads, kv.head_dim, kv.compute_dtypes, kv.device)
         tensor(cu, "cu", torch.int32, device=kv.device)
@@ -249,7 +275,7 @@ class PagedAttention:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=kv.device)
         if tokens == 0:
             return out, lse
-        stream = raw_stream(kv.device)
+        stream = raw_stream(self._index)
         size = tokens.bit_length()  # one space for all calls up to a power of two
         space = self._prompt.get(size)
         if space is None:

@@ -86,17 +86,12 @@ def check(rc: int, what: str) -> None:
         raise MoEError(f"{what}: {STATUS.get(rc, 'error')}{extra} [{rc}]")
 
 
-def raw_stream(device: torch.device) -> int:
-    """The handle of the device's current stream."""
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-# The same without the Python objects in between, where this torch has it: a
-# call of a few microseconds notices the difference.
-_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-if _raw is not None:
-    def raw_stream(device: torch.device) -> int:  # noqa: F811
-        return _raw(device.index)
+# By a device's index: the handle of its current stream; and the current device.
+# (Without the Python objects in between, where this torch has it: a call of a few
+# microseconds notices the difference.)
+raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                     lambda index: torch.cuda.current_stream(index).cuda_stream)
+current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def require(cond: bool, message: str) -> None:

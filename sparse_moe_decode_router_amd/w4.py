@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from .binding import MoEError
-from .serving import DTYPES, check, lib, raw_stream, require, tensor
+from .serving import DTYPES, check, current_device, lib, raw_stream, require, tensor
 
 GROUPS = (32, 64, 128)
 
@@ -31,13 +31,16 @@ class W4Linear:
         if zeros is not None:
             tensor(zeros, "zeros", torch.uint8, scales.shape, dev)
         self.codes, self.scales, self.zeros = codes, scales, zeros
-        self.device, self.dtype = dev, scales.dtype
+        self.device, self._index, self.dtype = dev, dev.index, scales.dtype
         self._lib, self._dtype = lib(), DTYPES[self.dtype]
         self._ptrs = (codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None
                       else None)
 
     def __call__(self, x, out=None):
         """x [tokens, k], rows contiguous -> [tokens, n]."""
+        if current_device() != self._index:  # kernels go to the current device
+            with torch.cuda.device(self.device):
+                return self(x, out)
         if not isinstance(x, torch.Tensor) or x.dtype != self.dtype or x.device != self.device:
             raise MoEError(f"x: a {self.dtype} tensor on {self.device} is needed")
         shape, stride = x.shape, x.stride()
@@ -55,5 +58,5 @@ class W4Linear:
         codes, scales, zeros = self._ptrs
         check(self._lib.moe_w4_linear(address, stride[0], self._dtype, codes, scales,
                                       zeros, tokens, self.k, self.n, self.group, out.data_ptr(),
-                                      raw_stream(self.device)), "w4")
+                                      raw_stream(self._index)), "w4")
         return out

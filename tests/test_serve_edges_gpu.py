@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import serve_util as su
-from sparse_moe_decode_router_amd import attention
+from sparse_moe_decode_router_amd import attention, w4
 from test_serve_gpu import PageModel, _gpu, ints, queries  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -222,3 +222,52 @@ def test_a_layer_without_room_leaves_the_others_alone():
         assert layer.kv.granted.tolist() == ([1, 0] if pages == 3 else [1, 1])
         layer.close()
     assert torch.equal(*got)
+
+
+# ---- Devices, streams and spaces --------------------------------------------
+
+def test_calls_run_on_the_tensors_device(monkeypatch):
+    """Another device is current: every call switches to the cache's for its
+    launch (seen here by what is asked for, since there may be one device)."""
+    now, entered = [7], []
+    real = torch.cuda.device
+
+    class Switch:
+        def __init__(self, device):
+            self.device = torch.device(device)
+
+        def __enter__(self):
+            entered.append(self.device)
+            self.inner, self.before = real(self.device), now[0]
+            now[0] = self.device.index
+            self.inner.__enter__()
+
+        def __exit__(self, *a):
+            now[0] = self.before
+            return self.inner.__exit__(*a)
+
+    cache = su.HostCache([20, 30], 2, 16, 64, BF, seed=57, spare=9, spare_cols=2)
+    kv = cache.gpu()
+    att = attention.PagedAttention(kv, 4, 2, 64)
+    q = queries((2, 4, 64), BF, 58).cuda()
+    lin = w4.W4Linear(torch.zeros((8, 64), dtype=torch.uint8, device="cuda"),
+                      torch.ones((8, 1), dtype=BF, device="cuda"))
+    x = torch.zeros((1, 128), dtype=BF, device="cuda")
+    two = ints(0, 1, 2)
+    want = att.decode(0, q)
+    with monkeypatch.context() as m:
+        for module in (attention, w4):
+            m.setattr(module, "current_device", lambda: now[0])
+        m.setattr(torch.cuda, "device", Switch)
+        for i, call in enumerate((
+                lambda: att.decode(0, q), lambda: att.prompt(0, q, two), lambda: kv.extend(ints(1, 1)),
+                lambda: kv.append(0, q[:, :2], q[:, 2:]), lambda: kv.free(ints(1)),
+                lambda: kv.fork(ints(0), ints(1)), lambda: kv.compact(), lambda: lin(x))):
+            got = call()
+            assert entered == [kv.device] * (i + 1) and now == [7]
+            if i == 0:
+                assert torch.equal(got[0], want[0])
+        now[0] = kv.device.index                      # and does not where it is current
+        att.decode(0, q)
+        assert len(entered) == 8
+    torch.cuda.synchronize()
