@@ -29,6 +29,7 @@ from .serving import (DTYPES, AttnConfig, Cache, StreamSpace, check, current_dev
                       raw_stream, require, tensor)
 
 E4M3_MAX = 448.0
+MAX_TOKENS = 1 << 24  # of a prompt call
 
 # A kernel goes to the current device, and the default stream's handle, zero, is that
 # of every device: each method that launches one makes its tensors' device current.
@@ -222,7 +223,7 @@ class PagedAttention:
         self._cfg, self._lib = ctypes.addressof(self.config), lib()
         check(self._lib.moe_attn_validate(kv._ref, self._cfg), "PagedAttention")
         self._decode = self._space(0)
-        self._prompt = {}
+        self._prompt, self._prompt_tokens = None, 0
 
     def _space(self, tokens: int) -> StreamSpace:
         w, c = ctypes.c_size_t(), ctypes.c_size_t()
@@ -276,11 +277,12 @@ class PagedAttention:
         if tokens == 0:
             return out, lse
         stream = raw_stream(self._index)
-        size = tokens.bit_length()  # one space for all calls up to a power of two
-        space = self._prompt.get(size)
-        if space is None:
-            space = self._prompt[size] = self._space(1 << size)
-        w, c, _ = space.get(stream)
+        if tokens > self._prompt_tokens:
+            # One space for all calls, of the largest one so far (what its work on a
+            # stream still uses is not given to another stream before that is done).
+            size = max(tokens, min(1 << (tokens - 1).bit_length(), MAX_TOKENS))
+            self._prompt, self._prompt_tokens = self._space(size), size
+        w, c, _ = self._prompt.get(stream)
         check(self._lib.moe_attn_prompt(kv._ref, self._cfg, layer, q.data_ptr(), DTYPES[q.dtype],
                                         ts, hs, tokens, cu.data_ptr(), batch, out.data_ptr(),
                                         lse.data_ptr(), w, c, stream), "prompt")

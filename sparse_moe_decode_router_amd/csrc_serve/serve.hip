@@ -93,14 +93,14 @@ struct PromptPlan {
     int split, units;
     int64_t slots;  // of partial results
 };
-// The plan for `row_tiles` full row tiles per kv head and at most `more` part-filled
-// ones beside them.
-PromptPlan prompt_plan_of(const moe_kv_cache &kv, const moe_attn_config &c, int64_t row_tiles,
-                          int64_t more) {
-    PromptPlan p;
-    p.tiles = row_tiles + more;
+// Partial results of a call that splits row tiles, for each workgroup that the
+// chip holds at once: bounds the workspace (512 such workgroups, head_dim 128: 136
+// MB), and the work of joining where many sequences have few new tokens.
+constexpr int kPromptPartsPerSlot = 4;
+
+// Parts of a row tile, where `row_tiles` of them per kv head are sure to be full.
+int64_t prompt_parts(const moe_kv_cache &kv, const moe_attn_config &c, int64_t row_tiles) {
     const int64_t sure = std::max<int64_t>(1, row_tiles) * kv.kv_heads;
-    const int slots = prompt_slots(kv.head_dim);
     // T tiles of keys in P parts take about T / P rounds and as many again as P to
     // join them: the square root of T parts, and four tiles in each at least
     // (300 tokens of 8192, 14 heads: 8, 10 and 15 parts 46, 48 and 58 us; 100 of
@@ -110,25 +110,52 @@ PromptPlan prompt_plan_of(const moe_kv_cache &kv, const moe_attn_config &c, int6
     const int64_t tiles = (keys + kPromptKeys - 1) / kPromptKeys;
     int64_t parts = 1;
     while (parts < 64 && parts * parts < tiles) ++parts;
-    p.split = (int)std::max<int64_t>(1, std::min<int64_t>({slots / sure, parts, tiles / 4}));
-    p.units = sure > slots ? std::max(1, slots / kv.kv_heads) : 0;
+    return std::min<int64_t>({prompt_slots(kv.head_dim) / sure, parts, tiles / 4});
+}
+// The plan for `row_tiles` full row tiles per kv head and at most `more` part-filled
+// ones beside them.
+PromptPlan prompt_plan_of(const moe_kv_cache &kv, const moe_attn_config &c, int64_t row_tiles,
+                          int64_t more) {
+    PromptPlan p;
+    p.tiles = row_tiles + more;
+    const int slots = prompt_slots(kv.head_dim);
+    const int64_t most = (int64_t)slots * kPromptPartsPerSlot;
+    p.split = (int)std::max<int64_t>(
+        1, std::min(prompt_parts(kv, c, row_tiles),
+                    most / std::max<int64_t>(1, p.tiles * kv.kv_heads)));
+    p.units = std::max<int64_t>(1, row_tiles) * kv.kv_heads > slots
+                  ? std::max(1, slots / kv.kv_heads)
+                  : 0;
     p.slots = p.units ? 2 * (int64_t)p.units : p.split > 1 ? p.tiles * p.split : 0;
     p.slots *= kv.kv_heads;
     return p;
 }
-int64_t full_row_tiles(const moe_kv_cache &kv, const moe_attn_config &c, int tokens) {
-    return (int64_t)tokens * (c.q_heads / kv.kv_heads) / kPromptRows;
+int64_t full_row_tiles(const moe_kv_cache &kv, const moe_attn_config &c, int64_t tokens) {
+    return tokens * (c.q_heads / kv.kv_heads) / kPromptRows;
 }
 PromptPlan prompt_plan(const moe_kv_cache &kv, const moe_attn_config &c, int tokens, int batch) {
     return prompt_plan_of(kv, c, full_row_tiles(kv, c, tokens), std::min(batch, tokens));
 }
 // Slots that no call of up to `tokens` tokens goes beyond: fewer row tiles are
 // split more finely, so the largest call need not be the one that takes most.
+// (A call has as many part-filled row tiles as sequences or fewer, and with r full
+// row tiles no more tokens than those and one more would hold.)
 int64_t prompt_slots_up_to(const moe_kv_cache &kv, const moe_attn_config &c, int tokens) {
-    const int64_t last = full_row_tiles(kv, c, tokens);
-    int64_t most = prompt_plan(kv, c, tokens, c.batch).slots;
-    for (int64_t r = 0; r <= std::min<int64_t>(last, prompt_slots(kv.head_dim)); ++r)
-        most = std::max(most, prompt_plan_of(kv, c, r, std::min(c.batch, tokens)).slots);
+    const int64_t last = full_row_tiles(kv, c, tokens), group = c.q_heads / kv.kv_heads;
+    const int slots = prompt_slots(kv.head_dim);
+    int64_t most = 0;
+    // (From slots + 1 full row tiles on, all take equal shares.)
+    for (int64_t r = 0; r <= std::min<int64_t>(last, slots + 1); ++r) {
+        const int64_t more = std::min<int64_t>(
+            {c.batch, tokens, ((r + 1) * kPromptRows - 1) / group});
+        const PromptPlan p = prompt_plan_of(kv, c, r, 0);
+        const int64_t parts = prompt_parts(kv, c, r);   // before it is bounded
+        if (p.units)
+            most = std::max(most, p.slots);
+        else if (parts > 1)
+            most = std::max(most, std::min((r + more) * parts * kv.kv_heads,
+                                           (int64_t)slots * kPromptPartsPerSlot));
+    }
     return most;
 }
 
@@ -509,7 +536,7 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *c, int
     a.counters = counters;
     a.batch = batch;
     a.tokens = tokens;
-    const PromptPlan p = prompt_plan(*kv, *c, tokens, c->batch);
+    const PromptPlan p = prompt_plan(*kv, *c, tokens, batch);
     a.split = p.split;
     a.units = p.units;
     a.row_tiles = (int32_t)std::min<int64_t>(p.tiles, 0x7FFFFFFF);

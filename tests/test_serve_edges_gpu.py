@@ -271,3 +271,25 @@ def test_calls_run_on_the_tensors_device(monkeypatch):
         att.decode(0, q)
         assert len(entered) == 8
     torch.cuda.synchronize()
+
+
+def test_a_plan_for_many_sequences_serves_few_and_many():
+    """Split row tiles where a call has one sequence of those planned for, and
+    where it has all of them; and what the plan keeps in the end."""
+    b, kvh, group, dim = 40, 4, 2, 64
+    lengths = [1500] + [(37 * i) % 300 + 1 for i in range(1, b)]
+    cache = su.HostCache(lengths, kvh, 16, dim, BF, seed=60)
+    kv = cache.gpu()
+    att = attention.PagedAttention(kv, kvh * group, b, 60000)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for new in ([1], [100], [5] + [1] * (b - 1), [33] + [min(7, n) for n in lengths[1:]], [700]):
+        cu = cumulative(new)
+        q = queries((cu[-1], kvh * group, dim), BF, 61)
+        want = su.attention_dense(cache, 0, q, cu)
+        got = att.prompt(0, q.cuda(), ints(*cu))
+        torch.cuda.synchronize()
+        su.check_attention(got, want, BF, True)
+    del got
+    # four partial results of 128 rows for 512 workgroups
+    assert torch.cuda.memory_allocated() - before <= 4 * 512 * 128 * (dim + 2) * 4 + (1 << 20)
