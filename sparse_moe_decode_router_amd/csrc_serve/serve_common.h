@@ -14,9 +14,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A running maximum before any score was seen.  Finite, so that differences
-// from it are never NaN; scores are in units of log 2.
-constexpr float kNoMax = -1e30f;
+// A running maximum before any score was seen: the lowest finite value, so that
+// differences from it are never NaN and every score is above it.  Scores are in
+// units of log 2.
+constexpr float kNoMax = -0x1.fffffep+127f;
 
 // Compute types.  kOff: weights are held as 2^(s - max + kOff), kSlack: how far
 // a score may exceed the running maximum before the accumulators are rescaled

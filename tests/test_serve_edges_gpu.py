@@ -121,6 +121,48 @@ def test_nan_codes_of_an_8_bit_cache(kind, dim):
     check_planted(attend(kind, cache, q, cu), clean, q, cu, spots, kind == "prompt")
 
 
+# ---- Scores of any size -----------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["decode"])
+@pytest.mark.parametrize("dtype,q0,k0", [(BF, 2, 3), (BF, 6, 6), (BF, 7, 7), (FP, 13, 13), (FP, 14, 14),
+                                         (BF, 20, 20), (BF, 60, 55)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(kind, dtype, q0, k0, sign):
+    """Every third key has the score +-a 2^(q0 + k0) scale, the others half of it or
+    twice it, below: the weights are equal (but for those others', which the
+    oracle has, too), and the output is the mean of the values."""
+    a, b = 165 / 128, 181 / 128                 # of 8 bits each, so a b has 16
+    n, new, dim, scale = 300, 1 if kind == "decode" else 200, 64, 0.37
+    cache = su.HostCache([n], 1, 16, dim, dtype, seed=48)
+    for t in range(n):
+        row = cache.data[0, 0, int(cache.tables[0, t // 16]), 0, t % 16]
+        row.zero_()
+        row[0] = sign * a * 2.0 ** k0 * (1 if t % 3 == 0 else 0.5 if sign > 0 else 2)
+    heads = torch.tensor([1.0, 0.5, 2.0])
+    q = torch.zeros((new, 3, dim))
+    q[:, :, 0] = b * 2.0 ** q0 * heads
+    q = q.to(dtype)
+    got = attend(kind, cache, q, [0, new], scale=scale)
+    v, half = cache.row(0, 1, 0, n)[0][:, 0], su.half_step(dtype)
+    score = a * b * 2.0 ** (q0 + k0) * scale * heads.double()
+    other = torch.exp(-score * (0.5 if sign > 0 else 1))
+    out, lse = (x.cpu().double() for x in got)
+    for i in range(new):
+        seen = n - new + i + 1
+        w = torch.where(torch.arange(seen) % 3 == 0, 1.0, other[:, None])    # [heads][seen]
+        total = w.sum(1, keepdim=True)
+        mean, mass = w / total @ v[:seen], w / total @ v[:seen].abs()
+        # The output's rounding, that of a prompt's weights, sums in 32 bits, and
+        # the weights' own: of a score up to 1024 its rounding, else none (equal
+        # scores have equal roundings) but for the others, which are nothing then.
+        near = 2.0 ** -22 * torch.clamp(score, max=1024.0)[:, None]
+        tol = half * mean.abs() + ((half if kind == "prompt" else 0) + 2.0 ** -16 + near) * mass
+        assert torch.all((out[i] - mean).abs() <= tol), i
+        want = sign * score + torch.log(total[:, 0])
+        # scale, its product with log2(e), the score and the way back: four steps
+        assert torch.all((lse[i] - want).abs() <= 2.0 ** -22 * want.abs() + 2.0 ** -16), i
+
+
 # ---- Pools and tables ------------------------------------------------------
 
 def test_extend_serves_what_fits():
