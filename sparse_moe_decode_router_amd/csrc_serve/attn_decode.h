@@ -348,6 +348,10 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
             u32x4 hi, lo;
 #pragma unroll
             for (int r = 0; r < 8; r += 2) {
+                // The rounded scores less their rounded maximum: a fused product
+                // would leave the maximum's own rounding, which is no small number
+                // where scores are large.
+#pragma clang fp contract(off)
                 const float p0 = exp2_(x[r] - m + T::kOff), p1 = exp2_(x[r + 1] - m + T::kOff);
                 l += p0 + p1;
                 hi[r / 2] = T::pack(p0, p1);

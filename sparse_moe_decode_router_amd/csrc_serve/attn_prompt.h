@@ -43,6 +43,10 @@ constexpr int kPromptKeys = 64;
 // Equal shares: what a row tile costs beside its tiles of keys, in such tiles, and
 // the smallest share.
 constexpr int kPromptFixed = 6, kPromptLeast = 16;
+// A weight is one fused product, 2^(s c - max): exact but for the rounding of the
+// maximum, 2^-14 of the weight where that is up to this.  Beyond, s c is rounded
+// as the maximum was.
+constexpr float kLargeMax = 1024.f;
 
 template <int D>
 struct PromptTile {
@@ -367,6 +371,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[j][r] = 0.f;
         float m = kNoMax, l = 0.f;
+        bool large = false;   // some row's maximum is
 
         // Where this lane reads, in bytes of a tile (tiles start at multiples of
         // 1024, so what follows holds for addresses, too).  Chunks of one row differ in
@@ -560,6 +565,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                 top = fmaxf(top, __shfl_xor(top, 32));
                 const float to = fmaxf(m, top), f = exp2_(m - to);
                 m = to;
+                large = __any(fabsf(m) > kLargeMax && m > kNoMax);
                 l *= f;
 #pragma unroll
                 for (int j = 0; j < DT; ++j)
@@ -567,13 +573,22 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                     for (int r = 0; r < 16; ++r) o[j][r] *= f;
             }
             u32x4 p[4];
-            const float shift = T::kOff - m;
+            float by = c2, shift = T::kOff - m;
+            if (large) {
+#pragma clang fp contract(off)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[u][r] = s[u][r] * c2 - m;
+                by = 1.f;
+                shift = T::kOff;
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) {
-                    const float p0 = exp2_(fmaf(s[u][r], c2, shift));
-                    const float p1 = exp2_(fmaf(s[u][r + 1], c2, shift));
+                    const float p0 = exp2_(fmaf(s[u][r], by, shift));
+                    const float p1 = exp2_(fmaf(s[u][r + 1], by, shift));
                     l += p0 + p1;
                     p[2 * u + (r >> 3)][(r & 7) >> 1] = T::pack(p0, p1);
                 }

@@ -123,7 +123,7 @@ def test_nan_codes_of_an_8_bit_cache(kind, dim):
 
 # ---- Scores of any size -----------------------------------------------------
 
-@pytest.mark.parametrize("kind", ["decode"])
+@pytest.mark.parametrize("kind", ["decode", "prompt"])
 @pytest.mark.parametrize("dtype,q0,k0", [(BF, 2, 3), (BF, 6, 6), (BF, 7, 7), (FP, 13, 13), (FP, 14, 14),
                                          (BF, 20, 20), (BF, 60, 55)])
 @pytest.mark.parametrize("sign", [1, -1])
