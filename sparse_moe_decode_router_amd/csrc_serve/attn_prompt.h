@@ -122,9 +122,18 @@ __device__ __forceinline__ uint32_t finite_of(uint32_t v) {
     return (T::odd(v) ? 0u : v & 0xFFFFu) | (T::odd(v >> 16) ? 0u : v & 0xFFFF0000u);
 }
 
+// The kernel's arguments, read again by what follows: kept in scalar registers from
+// the start on, they have to make room for others in lanes of vector registers.
+typedef __attribute__((address_space(4))) const AttnArgs PromptArgs;
+__device__ __forceinline__ PromptArgs &prompt_args() {
+    PromptArgs *a = (PromptArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(a));
+    return *a;
+}
+
 template <class T, bool F8, int D>
 __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_prompt(
-    const AttnArgs a) {
+    const AttnArgs) {
     typedef PromptTile<D> Tile;
     constexpr int KS = D / 16, DT = D / 32;
     __shared__ __attribute__((aligned(1024))) char s_k[2][Tile::kBytes];
@@ -134,6 +143,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
 
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_index();
     const int col = lane & 31, half = lane >> 5;
+    PromptArgs &a = prompt_args();
 
     // The length as the caller counts it: a table that is too short hides
     // positions (n_seen), it does not move the new tokens.
@@ -236,6 +246,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         if (b < 0) return;
     }
     for (;;) {
+        PromptArgs &a = prompt_args();
         // More than the tokens make up: a cu that decreases counts rows twice.
         if (index >= a.row_tiles) return;
         const int n_new = seq.n_new, tok0 = seq.tok0;
@@ -269,12 +280,6 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
             // before it, in its first slot, and one that goes on after it.
             slot0 = (first * 2 * a.kv_heads + h) * kSlot;
         }
-        // Part k's slot; of equal shares, part 0 has the second slot of its unit.
-        auto slot_of = [&](int k) {
-            if (a.units == 0) return a.part + slot0 + (int64_t)k * a.kv_heads * kSlot;
-            return a.part + slot0 + (int64_t)(k == 0 ? 1 : 2 * k) * a.kv_heads * kSlot;
-        };
-
         // This lane's row.
         const int my = row0 + min(32 * wave + col, rows - 1);
         const int my_tok = my / a.group, pos = past + my_tok;
@@ -625,10 +630,16 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         const bool odd = s_odd;
         l += __shfl_xor(l, 32);
 
+        PromptArgs &z = prompt_args();
+        // Part k's slot; of equal shares, part 0 has the second slot of its unit.
+        auto slot_of = [&](int k) {
+            if (z.units == 0) return z.part + slot0 + (int64_t)k * z.kv_heads * kSlot;
+            return z.part + slot0 + (int64_t)(k == 0 ? 1 : 2 * k) * z.kv_heads * kSlot;
+        };
         const bool real = 32 * wave + col < rows;
-        uint16_t *op = (uint16_t *)a.out + out_row * D;
+        uint16_t *op = (uint16_t *)z.out + out_row * D;
         auto write = [&]() {
-            const float f = l != 0.f ? (F8 && a.v_scale ? a.v_scale[h] : 1.f) / l : 0.f;
+            const float f = l != 0.f ? (F8 && z.v_scale ? z.v_scale[h] : 1.f) / l : 0.f;
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -642,7 +653,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                     *(u32x2 *)(op + 32 * dt + 2 * r + 4 * half) = w;
                 }
             if (half == 0)
-                a.lse[out_row] = l != 0.f ? (m + log2_(l) - T::kOff) * kLn2 : -__builtin_inff();
+                z.lse[out_row] = l != 0.f ? (m + log2_(l) - T::kOff) * kLn2 : -__builtin_inff();
         };
         // Parts are kept as the lanes hold them (the one that joins them has
         // the same rows in the same places): every access is a whole block.
@@ -726,20 +737,20 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                         store_agent(slot + 1024 * dt + 256 * (r / 4) + r % 4, sum);
                     else if (real)
                         op[32 * dt + 2 * (r & 12) + 4 * half + r % 4] =
-                            (uint16_t)T::pack(F8 && a.v_scale ? sum * a.v_scale[h] : sum, 0.f);
+                            (uint16_t)T::pack(F8 && z.v_scale ? sum * z.v_scale[h] : sum, 0.f);
                 }
             }
         }
         if (parts > 1) {
-            const int64_t group = (int64_t)index * a.kv_heads + h;
+            const int64_t group = (int64_t)index * z.kv_heads + h;
             wait_vm_all();
             __syncthreads();
             if (tid == 0)
-                s_last = __hip_atomic_fetch_add(a.counters + group, 1u, __ATOMIC_RELAXED,
+                s_last = __hip_atomic_fetch_add(z.counters + group, 1u, __ATOMIC_RELAXED,
                                                 __HIP_MEMORY_SCOPE_AGENT);
             __syncthreads();
             if (s_last == (uint32_t)parts - 1) {
-                if (tid == 0) store_agent(a.counters + group, 0u);
+                if (tid == 0) store_agent(z.counters + group, 0u);
                 // Loads of several parts are on their way together: one after
                 // the other they cost most of a microsecond each.
                 const int ml = wave * 32 * (D + 2) + 32 * D + col;
@@ -790,12 +801,12 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         }
         // On to the next row tile of an equal share.
         at += weight;
-        if (a.units == 0 || at >= x1) return;
+        if (z.units == 0 || at >= x1) return;
         ++index;
         if (++tile == seq.tiles) {
             tile = 0;
             do {
-                if (++b >= a.batch) return;
+                if (++b >= z.batch) return;
                 seq = seq_of(b);
             } while (seq.tiles == 0);
         }
