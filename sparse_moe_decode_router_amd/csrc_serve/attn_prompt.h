@@ -164,8 +164,10 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
     auto visible_of = [&](const Seq &x, int row0) {
         const int rows = min(kPromptRows, x.n_new * a.group - row0), past = x.n - x.n_new;
         const int lo = past + row0 / a.group, hi = past + (row0 + rows - 1) / a.group;
+        // (Rows before the first position see nothing: they must not move the window
+        // over the ends of an integer.)
         return visible<6>(max(0, min(min(x.n, most), hi + 1)),
-                          a.window > 0 ? max(0, lo - a.window + 1) : 0, a.sinks);
+                          a.window > 0 ? max(0, max(lo, 0) - a.window + 1) : 0, a.sinks);
     };
 
     // Equal shares: workgroups go round the XCDs, so neighbours in the sequence,
@@ -283,7 +285,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         // This lane's row.
         const int my = row0 + min(32 * wave + col, rows - 1);
         const int my_tok = my / a.group, pos = past + my_tok;
-        const int from = a.window > 0 ? pos - a.window : -1;        // sees keys above it
+        const int from = a.window > 0 ? max(pos, -1) - a.window : -1;   // sees keys above it
         const int64_t out_row =
             (int64_t)(tok0 + my_tok) * a.kv_heads * a.group + h * a.group + (my - my_tok * a.group);
         u32x4 q[KS];
@@ -403,7 +405,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
             bool whole;
         };
         const int whole_to = min(pos_lo - 63, n_seen - 64);
-        const int whole_from = a.window > 0 ? pos_hi - a.window + 1 : 0;
+        const int whole_from = a.window > 0 ? max(pos_hi, 0) - a.window + 1 : 0;
         auto seen_of = [&](int i) {
             Seen x;
             x.key0 = (int)uniform(64 * visible_block(vis, i));
@@ -486,8 +488,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
             asm("" : "+v"(key0));
             if (see.have == 15u && (a.window <= 0 || see.key0 >= a.sinks)) {
                 // One run of keys: those from first on, and fewer than count of them.
-                const int below = from - key0, count = max(0, min(pos, n_seen - 1) - from);
-                const uint32_t first = (uint32_t)(-1 - below);
+                const int count = max(0, min(pos, n_seen - 1) - from);
+                const uint32_t first = (uint32_t)key0 - (uint32_t)from - 1u;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll

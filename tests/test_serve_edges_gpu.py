@@ -163,6 +163,24 @@ def test_scores_of_any_size(kind, dtype, q0, k0, sign):
         assert torch.all((lse[i] - want).abs() <= 2.0 ** -22 * want.abs() + 2.0 ** -16), i
 
 
+# ---- Windows ----------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 10, 2 ** 30])
+@pytest.mark.parametrize("sinks", [0, 3, 2 ** 31 - 1])
+def test_a_window_as_large_as_an_integer(window, sinks):
+    """It hides nothing, also where a sequence is shorter than its new tokens, the
+    first of which then stand before its first position and see nothing."""
+    cache = su.HostCache([5, 40, 0, 150], 1, 16, 64, BF, seed=49)
+    cu = cumulative([20, 60, 3, 150])
+    q = queries((cu[-1], 2, 64), BF, 50)
+    want = su.attention(cache, 0, q, cu)
+    su.check_attention(attend("prompt", cache, q, cu, window=window, sinks=sinks), want, BF, True)
+    d = queries((4, 2, 64), BF, 51)
+    want = su.attention(cache, 0, d, [0, 1, 2, 3, 4])
+    su.check_attention(attend("decode", cache, d, [0, 1, 2, 3, 4], window=window, sinks=sinks),
+                       want, BF, False)
+
+
 # ---- Pools and tables ------------------------------------------------------
 
 def test_extend_serves_what_fits():
