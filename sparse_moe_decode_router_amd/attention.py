@@ -37,15 +37,19 @@ MAX_TOKENS = 1 << 24  # of a prompt call
 
 def _rows(t, name, heads, dim, dtypes, device) -> Tuple[int, int]:
     """Checks a [tokens][heads][dim] tensor whose rows are contiguous; returns
-    its token and head strides."""
+    its token and head strides (0 where there is only one, which may have any)."""
     # What is right is passed without forming any message: a call takes as long
     # as its smallest kernels.
     if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device:
         shape, (ts, hs, one) = t.shape, t.stride() if t.dim() == 3 else (0, 0, 0)
-        if len(shape) == 3 and shape[1] == heads and shape[2] == dim and one == 1 and \
-                ts % 8 == 0 and hs % 8 == 0 and (heads == 1 or hs >= dim) and \
-                t.data_ptr() % 16 == 0:
-            return ts, hs
+        if len(shape) == 3 and shape[1] == heads and shape[2] == dim and one == 1:
+            if shape[0] <= 1:
+                ts = 0
+            if heads == 1:
+                hs = 0
+            if ts % 8 == 0 and hs % 8 == 0 and (heads == 1 or hs >= dim) and \
+                    t.data_ptr() % 16 == 0:
+                return ts, hs
     require(isinstance(t, torch.Tensor), f"{name}: a tensor is needed, got {type(t).__name__}")
     require(t.dtype in dtypes, f"{name}: {t.dtype} given, {' or '.join(map(str, dtypes))} needed")
     require(t.device == device, f"{name}: on {t.device}, not on {device}")

@@ -46,17 +46,17 @@ class W4Linear:
         shape, stride = x.shape, x.stride()
         if len(shape) != 2 or shape[1] != self.k:
             raise MoEError(f"x: shape {tuple(shape)} given, (tokens, {self.k}) needed")
-        address = x.data_ptr()
-        if stride[1] != 1 or stride[0] % 8 or address % 16:
+        address, tokens = x.data_ptr(), shape[0]
+        step = stride[0] if tokens > 1 else 0  # (that of a single row may be any)
+        if stride[1] != 1 or step % 8 or address % 16:
             raise MoEError(f"x: strides {tuple(stride)}: contiguous rows, 16-byte aligned, are "
                            "needed")
-        tokens = shape[0]
         if out is None:
             out = torch.empty((tokens, self.n), dtype=x.dtype, device=self.device)
         else:
             tensor(out, "out", x.dtype, (tokens, self.n), self.device)
         codes, scales, zeros = self._ptrs
-        check(self._lib.moe_w4_linear(address, stride[0], self._dtype, codes, scales,
+        check(self._lib.moe_w4_linear(address, step, self._dtype, codes, scales,
                                       zeros, tokens, self.k, self.n, self.group, out.data_ptr(),
                                       raw_stream(self._index)), "w4")
         return out

@@ -284,6 +284,35 @@ def test_a_layer_without_room_leaves_the_others_alone():
     assert torch.equal(*got)
 
 
+# ---- Strides ----------------------------------------------------------------
+
+def test_strides_that_no_row_uses():
+    """A single token's and a single head's stride may be any."""
+    dim = 64
+    cache = su.HostCache([20], 1, 16, dim, BF, seed=54)
+    kv = cache.gpu()
+    odd = queries((1, 4 * dim + 4), BF, 55).cuda()
+    q = odd[:, :2 * dim].unflatten(1, (2, dim))            # a token stride of 4 dim + 4
+    k, v = (odd[:, i * dim:(i + 1) * dim].as_strided((1, 1, dim), (s, 3, 1), i * dim)
+            for i, s in ((2, 1), (3, 7)))
+    kv.append(0, k, v)
+    cache.data = kv.data.cpu()
+    att = attention.PagedAttention(kv, 2, 1, 20)
+    want = su.attention(cache, 0, q.cpu(), [0, 1])
+    last = cache.data[0, :, int(cache.tables[0, 1]), 0, 3]
+    assert torch.equal(last, torch.stack([k[0, 0], v[0, 0]]).cpu())
+    su.check_attention(att.decode(0, q), want, BF, False)
+    su.check_attention(att.prompt(0, q, ints(0, 1)), want, BF, True)
+    codes = torch.full((8, 64), 0x98, dtype=torch.uint8, device="cuda")     # 0 and 1
+    lin = w4.W4Linear(codes, torch.ones((8, 1), dtype=BF, device="cuda"))
+    x = odd[:, :128]
+    for one in (x, x.as_strided((1, 128), (1, 1))):
+        y = lin(one).double()
+        # at most 128 products and sums of 143 |x| in 32 bits, and the output's step
+        exact, mass = x[0, 1::2].double().sum(), x.double().abs().sum()
+        assert torch.all((y - exact).abs() <= 2 ** -8 * exact.abs() + 260 * 2 ** -24 * 143 * mass)
+
+
 # ---- Devices, streams and spaces --------------------------------------------
 
 def test_calls_run_on_the_tensors_device(monkeypatch):
