@@ -170,17 +170,19 @@ __device__ __forceinline__ int take_lowest(int pages, int want, int32_t *list, i
 }
 
 __global__ __launch_bounds__(256) void k_kv_free(const PagesArgs a) {
-    const int s = a.from[blockIdx.x];
-    if (s < 0 || s >= a.seqs) return;
-    int32_t *row = a.tables + (int64_t)s * a.cols;
-    for (int i = threadIdx.x; i < a.cols; i += 256) {
-        const int p = row[i];
-        if (p >= 0) {
-            if (p < a.pages) atomicAdd(a.refs + p, -1);
-            row[i] = -1;
+    for (int x = blockIdx.x; x < a.n; x += gridDim.x) {
+        const int s = a.from[x];
+        if (s < 0 || s >= a.seqs) continue;
+        int32_t *row = a.tables + (int64_t)s * a.cols;
+        for (int i = threadIdx.x; i < a.cols; i += 256) {
+            const int p = row[i];
+            if (p >= 0) {
+                if (p < a.pages) atomicAdd(a.refs + p, -1);
+                row[i] = -1;
+            }
         }
+        if (threadIdx.x == 0) a.lengths[s] = 0;
     }
-    if (threadIdx.x == 0) a.lengths[s] = 0;
 }
 
 // Length of sequence s, cut to its table; 0 for one the cache does not have.

@@ -63,6 +63,9 @@ char *plane(const moe_kv_cache &kv, int layer, int which) {
 }
 
 constexpr int kMaxRows = 1 << 24;  // sequences, tokens of a call, pairs of a list
+// A grid's first axis has below 2^32 threads, its second up to 2^16 workgroups.
+constexpr int64_t kMaxGrid256 = (1ll << 24) - 1;   // of 256 threads each
+constexpr int kMaxW4Tokens = 1 << 21;              // of one launch: 2^15 times 64
 
 // Workgroups that one decode call aims at: with four waves each, three of them
 // share a compute unit.
@@ -356,7 +359,7 @@ moe_status moe_kv_append_granted(const moe_kv_cache *kv, int32_t layer, const vo
     // Two rounds of the workgroup's threads, where there are tokens enough to
     // fill the chip that way.
     const int per_token = kv->kv_heads * kv->head_dim / 8;
-    a.per_block = std::max(1, std::min(512 / per_token, tokens / (4 * cus)));
+    a.per_block = std::max(1 + (tokens >> 23), std::min(512 / per_token, tokens / (4 * cus)));
     const int grid = (tokens + a.per_block - 1) / a.per_block;
     return with_types(dtype, kv->dtype == MOE_E4M3, [&](auto t, auto f8) {
         k_kv_append<decltype(t), decltype(f8)::value><<<grid, 256, 0, stream>>>(a);
@@ -379,7 +382,7 @@ moe_status moe_kv_free(const moe_kv_cache *kv, const int32_t *seqs, int32_t n,
     if (!seqs) return MOE_ERR_INVALID_ARG;
     PagesArgs a = pages_args(*kv, n, nullptr);
     a.from = seqs;
-    k_kv_free<<<n, 256, 0, stream>>>(a);
+    k_kv_free<<<std::min(n, 1 << 20), 256, 0, stream>>>(a);
     return launched();
 }
 
@@ -492,9 +495,12 @@ moe_status moe_attn_decode(const moe_kv_cache *kv, const moe_attn_config *c, int
                               workspace, counters);
     if (s != MOE_OK) return s;
     if (!workspace || !counters) return MOE_ERR_WORKSPACE;
+    AttnArgs a = attn_args(*kv, *c, layer);
+    a.split = decode_split(*kv, *c);
+    const int64_t grid = ((int64_t)a.split + batch) * a.kv_heads * a.head_groups;
+    if (grid > kMaxGrid256) return MOE_ERR_UNSUPPORTED;
     int cus;
     if ((s = compute_units(&cus)) != MOE_OK) return s;
-    AttnArgs a = attn_args(*kv, *c, layer);
     a.q = q;
     a.q_token = token_stride;
     a.q_head = head_stride;
@@ -503,12 +509,10 @@ moe_status moe_attn_decode(const moe_kv_cache *kv, const moe_attn_config *c, int
     a.part = (float *)workspace;
     a.counters = counters;
     a.batch = batch;
-    a.split = decode_split(*kv, *c);
-    const int grid = (a.split + batch) * a.kv_heads * a.head_groups;
     return with_types(dtype, kv->dtype == MOE_E4M3, [&](auto t, auto f8) {
         return with_dim(kv->head_dim, [&](auto d) {
             k_attn_decode<decltype(t), decltype(f8)::value, decltype(d)::value>
-                <<<grid, kDecodeThreads, 0, stream>>>(a);
+                <<<(int)grid, kDecodeThreads, 0, stream>>>(a);
             return launched();
         });
     });
@@ -542,7 +546,7 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *c, int
     a.row_tiles = (int32_t)std::min<int64_t>(p.tiles, 0x7FFFFFFF);
     if (p.slots && (!workspace || !counters)) return MOE_ERR_WORKSPACE;
     const int64_t grid = kv->kv_heads * (p.units ? p.units : p.tiles * p.split);
-    if (grid >= 1ll << 31) return MOE_ERR_UNSUPPORTED;
+    if (grid > kMaxGrid256) return MOE_ERR_UNSUPPORTED;
     return with_types(dtype, kv->dtype == MOE_E4M3, [&](auto t, auto f8) {
         return with_dim(kv->head_dim, [&](auto d) {
             k_attn_prompt<decltype(t), decltype(f8)::value, decltype(d)::value>
@@ -567,20 +571,24 @@ moe_status moe_w4_linear(const void *x, int64_t x_stride, int32_t dtype, const u
     moe_status s = compute_units(&cus);
     if (s != MOE_OK) return s;
     W4Args a = {};
-    a.x = (const uint16_t *)x;
     a.scales = (const uint16_t *)scales;
     a.codes = codes;
     a.zeros = zeros;
-    a.y = (uint16_t *)y;
     a.x_stride = x_stride;
-    a.tokens = tokens;
     a.k = k;
     a.n = n;
-    return with_types(dtype, false, [&](auto t, auto) {
-        return with_group(group, zeros != nullptr, [&](auto gl, auto z) {
-            return w4_launch<decltype(t), decltype(gl)::value, decltype(z)::value>(a, cus, stream);
+    for (int64_t t = 0; t < tokens && s == MOE_OK; t += kMaxW4Tokens) {
+        a.x = (const uint16_t *)x + t * x_stride;
+        a.y = (uint16_t *)y + t * n;
+        a.tokens = (int32_t)std::min<int64_t>(tokens - t, kMaxW4Tokens);
+        s = with_types(dtype, false, [&](auto ty, auto) {
+            return with_group(group, zeros != nullptr, [&](auto gl, auto z) {
+                return w4_launch<decltype(ty), decltype(gl)::value, decltype(z)::value>(a, cus,
+                                                                                        stream);
+            });
         });
-    });
+    }
+    return s;
 }
 
 }  // extern "C"

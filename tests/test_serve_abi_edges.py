@@ -32,3 +32,12 @@ def test_the_workspace_of_prompts_has_a_bound(heads, kv_heads, dim, longest, win
         assert w <= row_tile * 4 * slots
         tiles = tokens * group // 128 + min(batch, tokens)
         assert w <= row_tile * 64 * tiles * kv_heads and n == 4 * tiles * kv_heads
+
+
+def test_decode_refuses_more_workgroups_than_a_grid_has():
+    """(Their number used to wrap round; here it would be 4096 times 2^24.)"""
+    c = cache(kv_heads=64, head_dim=64, seqs=1 << 24, cols=1)
+    for batch, want in ((1 << 24, -2), (1 << 13, -2)):
+        cfg = serving.AttnConfig(64 * 1024, batch, 16, 0, 0, 0.1)
+        assert status("moe_attn_decode", ctypes.addressof(c), ctypes.addressof(cfg), 0, 4096, 0,
+                      64 * 1024 * 64, 64, batch, 4096, 4096, 4096, 4096, None) == want

@@ -382,3 +382,20 @@ def test_a_plan_for_many_sequences_serves_few_and_many():
     del got
     # four partial results of 128 rows for 512 workgroups
     assert torch.cuda.memory_allocated() - before <= 4 * 512 * 128 * (dim + 2) * 4 + (1 << 20)
+
+
+# ---- Sizes at the ends of a grid's axes -------------------------------------
+
+def test_w4_of_millions_of_tokens():
+    """More tokens than one launch takes, of small whole numbers, so that the results
+    are exact (but for the rounding of sums above 256)."""
+    t, n = (1 << 22) + 65, 5
+    x = torch.zeros((t, 32), dtype=BF, device="cuda")
+    i = torch.arange(t, device="cuda")
+    x[:, 0], x[:, 1] = (i % 251).to(BF), (i // 251 % 241).to(BF)
+    codes = torch.full((n, 16), 0x88, dtype=torch.uint8, device="cuda")
+    codes[:, 0] = torch.tensor([0x89, 0x98, 0x99, 0x87, 0x78], dtype=torch.uint8)
+    y = w4.W4Linear(codes, torch.ones((n, 1), dtype=BF, device="cuda"))(x)
+    a, b = x[:, 0].float(), x[:, 1].float()
+    want = torch.stack([a, b, a + b, -a, -b], 1).to(BF)
+    assert torch.equal(y, want)
