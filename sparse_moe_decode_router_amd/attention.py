@@ -222,6 +222,11 @@ class PagedAttention:
                  sinks: int = 0, scale: Optional[float] = None):
         self.kv, self.q_heads, self.batch = kv, q_heads, batch
         self.device, self._index = kv.device, kv.device.index
+        # (The structure's 32 bits would take any integer, cut to them.)
+        for name, v in (("q_heads", q_heads), ("batch", batch), ("longest", longest),
+                        ("window", window), ("sinks", sinks)):
+            require(isinstance(v, int) and 0 <= v < 1 << 31,
+                    f"{name}: an integer from 0 to 2^31 - 1 is needed, got {v!r}")
         self.config = AttnConfig(q_heads, batch, longest, window, sinks,
                                  kv.head_dim ** -0.5 if scale is None else scale)
         self._cfg, self._lib = ctypes.addressof(self.config), lib()

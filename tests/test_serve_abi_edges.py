@@ -1,10 +1,13 @@
 """Host-side checks of the serving operators at the ends of their ranges (no GPU
 needed)."""
 import ctypes
+import types
 
 import pytest
+import torch
 
-from sparse_moe_decode_router_amd import serving
+from sparse_moe_decode_router_amd import attention, serving
+from sparse_moe_decode_router_amd.binding import MoEError
 from test_serve_abi import cache, status
 
 
@@ -41,3 +44,17 @@ def test_decode_refuses_more_workgroups_than_a_grid_has():
         cfg = serving.AttnConfig(64 * 1024, batch, 16, 0, 0, 0.1)
         assert status("moe_attn_decode", ctypes.addressof(c), ctypes.addressof(cfg), 0, 4096, 0,
                       64 * 1024 * 64, 64, batch, 4096, 4096, 4096, 4096, None) == want
+
+
+@pytest.mark.parametrize("kw", [dict(window=(1 << 32) + 5), dict(longest=(1 << 32) + 500),
+                                dict(sinks=-(1 << 32)), dict(batch=(1 << 32) + 1), dict(window=1.5),
+                                dict(window=-1), dict(q_heads=(1 << 32) + 4)])
+def test_plans_refuse_numbers_beyond_32_bits(kw):
+    """They used to be cut to their low 32 bits."""
+    c = cache(head_dim=64)
+    kv = types.SimpleNamespace(_ref=ctypes.addressof(c), head_dim=64, kv_heads=2,
+                               device=torch.device("cuda", 0))
+    plan = dict(q_heads=4, batch=2, longest=100)
+    attention.PagedAttention(kv, **plan)
+    with pytest.raises(MoEError):
+        attention.PagedAttention(kv, **{**plan, **kw})
