@@ -30,8 +30,8 @@
  * Precision.  Products of 16-bit values are exact in f32; scores, the running
  * maximum and sum and the outputs are held in f32; the output is rounded once.
  * The weights exp(s - max) enter the second product as a pair of 16-bit values
- * (decode) or as one 16-bit value (prompt), beside which the output's own
- * rounding is of the same size.
+ * (decode) or as one 16-bit value (prompt: of the size of the output's own
+ * rounding; together they are off by 0.0022 in bf16, where decode is by 0.0016).
  *
  * Contents out of range (a page number outside the pool, a length beyond the
  * table, a sequence number outside the cache) are never followed: positions
@@ -170,8 +170,9 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *cfg, i
 /* y = x W^T with W[n][j] = (code[n][j] - zero[n][j / group]) * scale[n][j / group]:
  * codes u8 [n][k / 2] (column 2j in the low half of byte j), scales [n][k /
  * group] in x's type, zeros u8 [n][k / group] below 16, or NULL for 8; x
- * [tokens][k] of finite values with rows x_stride apart (a multiple of 8, at
- * most 2^25), y [tokens][n].  group 32, 64 or 128; k a multiple of group; n
+ * [tokens][k] of finite values (in bf16 of magnitudes up to 2^112: sums of (code +
+ * 128) x over a group have to be finite, too) with rows x_stride apart (a multiple
+ * of 8, at most 2^25), y [tokens][n].  group 32, 64 or 128; k a multiple of group; n
  * any; x and codes 16-byte aligned.  Integers times x are summed exactly as products in f32, the
  * scale is applied to each group's sum in f32, and y is rounded once. */
 moe_status moe_w4_linear(const void *x, int64_t x_stride, int32_t dtype, const uint8_t *codes,

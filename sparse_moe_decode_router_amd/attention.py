@@ -65,7 +65,9 @@ class PagedKV:
     at 0, values at 1), tables [seqs, cols] i32 (-1: no page), lengths [seqs]
     i32, refs [pages] i32; k_scale, v_scale [kv_heads] f32 for e4m3: a code c
     stands for c * scale.  The tensors stay the caller's and are changed in
-    place; operations on them are ordered by the stream they run on."""
+    place; operations on them are ordered by the stream they run on.  The object
+    (its flags, granted and scratch) is kept until its work on every stream is
+    done."""
 
     def __init__(self, data, tables, lengths, refs, k_scale=None, v_scale=None):
         tensor(data, "data", tuple(DTYPES))
@@ -265,9 +267,10 @@ class PagedAttention:
 
     def prompt(self, layer: int, q, cu, max_new: Optional[int] = None):
         """q [tokens, q_heads, head_dim]; cu [batch + 1] i32: rows cu[b] ..
-        cu[b + 1] - 1 are the last positions of sequence b (at most max_new of
-        them, where it is given).  Returns (out, like q; lse [tokens, q_heads]
-        f32); rows that cu leaves out are not written."""
+        cu[b + 1] - 1 are the last positions of sequence b.  max_new: the most
+        rows of one sequence, as other plans need it; this one reads cu, and
+        answers do not depend on it.  Returns (out, like q; lse [tokens,
+        q_heads] f32); rows that cu leaves out are not written."""
         if current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.prompt(layer, q, cu, max_new)

@@ -26,11 +26,13 @@
 // parts 28 us).  Rows that take one unit are written by it; of the
 // units of a longer row the last to arrive joins the others' results.
 //
-// Bound by memory: 64 sequences of up to 8192 on an e4m3 cache, 570 MB, take 126
-// us (4.6 TB/s), two of up to 131072 in bf16, 823 MB, 154 us (5.4 TB/s).  One
-// sequence of 1500 takes 8.8 us: a chain of length, pages, keys, the store of a
-// part, its arrival and the join, each about a memory latency (with the join's
-// loads one after the other it was 9.1).
+// Bound by memory: 64 sequences of up to 8192 on an e4m3 cache, 570 MB, take 125
+// us (4.6 TB/s), two of up to 131072 in bf16, 823 MB, 156 us (5.3 TB/s).  One
+// sequence of 1500 takes 9.1 us: a chain of length, pages, keys, the store of a
+// part, its arrival and the join, each about a memory latency.  Long single rows
+// do not fill the chip (25000 positions, 8 heads on 1: 17 us, 100000: 27, of
+// which memory needs 2.5 and 10): one workgroup joins their parts.  No registers
+// are spilled but at head_dim 256 on a 16-bit cache (17).
 #pragma once
 
 #include "serve_common.h"

@@ -98,7 +98,9 @@ struct PromptPlan {
 };
 // Partial results of a call that splits row tiles, for each workgroup that the
 // chip holds at once: bounds the workspace (512 such workgroups, head_dim 128: 136
-// MB), and the work of joining where many sequences have few new tokens.
+// MB), and the work of joining where many sequences have few new tokens (3 parts
+// against 8, 64 sequences of up to 4 new ones of 4096, 56 heads on 8: 155 and 195
+// us; 4 against 9, 16 of up to 3 of 32768: 295 and 331).
 constexpr int kPromptPartsPerSlot = 4;
 
 // Parts of a row tile, where `row_tiles` of them per kv head are sure to be full.
@@ -189,11 +191,24 @@ moe_status with_group(int group, bool z, F f) {
 }
 // The fewest rows per workgroup that leave no compute unit two workgroups: a
 // second one on some of them costs more than larger tiles do, and from there
-// on larger tiles spread x over more rows.  Measured with 7168 columns, in us,
-// 16 / 32 / 64 rows: 8 tokens, 1152 rows 6.1 / 8.0 / 12.1, 9216 rows 16.8 /
-// 17.3 / 15.7, 36864 rows 52.0 / 43.4 / 44.5; 64 tokens, 7168 rows 33.9 / 23.0 /
-// 31.4, 36864 rows - / 104 / 96.  A single token has next to no x to spread
-// (1152 rows 5.0, with half the waves 5.8; 36864 rows 38.8 and 35.7).
+// on larger tiles spread x over more rows.  Measured with 7168 columns, bf16, zero
+// points, in us of device time:
+//   weight rows            4096  4111  6144  8192  9216 12288 18432 36864
+//    8 tokens, 16 rows      6.9   8.8  10.2  11.9  15.9  19.0  27.7  49.9
+//              32           9.0   9.1   9.2   9.8  14.4  16.6  24.5  40.1
+//              64          12.9  12.9  13.1  13.5  14.4  15.9  27.2  40.8
+//   16 tokens, 16           7.9  11.0  12.0  14.6  20.0  23.3  35.5  63.4
+//              32           9.9  10.0  10.1  11.0  17.6  20.0  28.5  46.7
+//              64          14.0  14.1  14.3  15.6  16.4  17.9  29.7  44.8
+//   32 tokens, 16          11.3  18.8  19.9  22.2  31.7  36.6  57.8 105.2
+//              64          15.9  15.9  16.1  19.2  20.8  22.1  40.1  61.9
+//   64 tokens, 16          17.3  28.4  30.2  34.1  47.4  53.7  84.2 155.5
+//              32          19.6  19.7  20.4  24.4  41.0  44.2  64.9 108.9
+//              64          30.6  30.7  30.9  32.3  33.0  33.9  64.4  96.3
+// (A form of 32 rows for 17 to 32 tokens, which there is not, would take 11.7 to
+// 15.2 from 4111 to 8192 rows.)  A single token has next to no x to spread: 8
+// waves of four steps ahead against 4 of two, 1152 rows 5.2 and 6.6, 4096 6.1 and
+// 7.0, 4111 7.7 and 7.9, 9216 12.4 and 11.6, 36864 39.7 and 37.7.
 template <class T, int GL, bool Z>
 moe_status w4_launch(const W4Args &a, int cus, hipStream_t stream) {
     auto go = [&](auto kernel, int nt, int rt, int w) {

@@ -7,7 +7,10 @@
 // conversion: bf16 0x4300 | q is 128 + q, fp16 0x6400 | q is 1024 + q, both
 // exact, two at a time.  fp16 then subtracts 1024 + zero (exact, packed).
 // bf16 has no packed subtraction: sum_j (128 + q_j) x_j - (128 + zero) sum_j
-// x_j in f32, with the sums of x from one more MFMA against ones.
+// x_j in f32, with the sums of x from one more MFMA against ones.  Partial sums
+// are then up to 143 / 8 times larger than the result of a group, and lose that
+// in f32: at most some 2^-18 of the sum of |x| scale, 2^-20 of the results as a
+// whole, beside the output's own 2^-8.
 // Pairs come out as (0,4)(1,5)(2,6)(3,7) of each eight codes, so x is put in
 // that order.
 //

@@ -120,7 +120,8 @@ def tensor(t, name: str, dtype, shape=None, device=None) -> torch.Tensor:
 
 class StreamSpace:
     """Workspace and zeroed counters, one of each per stream: calls on one stream
-    are ordered, so they share; calls on different streams never do.  A call
+    are ordered, so they share; calls on different streams never do (those of a
+    stream that is gone stay for the next one of its handle).  A call
     that is being captured into a graph gets its own, which the graph keeps
     (its counters are cleared within the graph, by a fill kernel)."""
 
