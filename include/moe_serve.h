@@ -35,8 +35,9 @@
  *
  * Contents out of range (a page number outside the pool, a length beyond the
  * table, a sequence number outside the cache) are never followed: positions
- * without a page are not seen and not written, lengths are cut to cols * page,
- * and unknown sequences are skipped.
+ * without a page, and those beyond cols * page, are not seen and not written (new
+ * tokens stay at the positions that the length gives them; fork and extend cut
+ * it), and unknown sequences are skipped.
  *
  * Calls only enqueue work on `stream`, which belongs to the current device,
  * and may be captured into a HIP graph.  Every call returns a moe_status.

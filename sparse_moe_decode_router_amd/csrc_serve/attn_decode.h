@@ -180,24 +180,24 @@ __device__ __forceinline__ void sum_not_finite(Each each, Put put) {
 }
 
 struct DecodeUnit {
-    int b, n;        // sequence (-1: none), its length
+    int b, n;        // sequence (-1: none), its length as far as its table goes
+    int first;       // of its window's positions (0: no window)
     Visible vis;
     int i0, i1;      // visible blocks of this unit
-    int first, parts;  // the row's first unit (per kv head), and how many there are
+    int unit0, parts;  // the row's first unit (per kv head), and how many there are
 };
 
 // The unit of index `want` among all sequences' units (per kv head).
 __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
     const int lane = lane_id();
     const int most = a.cols << a.page_log2;
-    auto vis_of = [&](int n) {
-        const int first = a.window > 0 ? max(0, n - a.window) : 0;
-        return visible<5>(n, first, a.sinks);
-    };
+    // The token's position is the length's, also where the table is too short for it.
+    auto first_of = [&](int n) { return a.window > 0 ? max(0, n - a.window) : 0; };
+    auto vis_of = [&](int n) { return visible<5>(min(n, most), first_of(n), a.sinks); };
     int sum = 0, longest = 0, n0 = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         const int b = b0 + lane;
-        n0 = b < a.batch ? min(max(a.lengths[b], 0), most) : 0;
+        n0 = b < a.batch ? max(a.lengths[b], 0) : 0;
         const int total = vis_of(n0).total;
         sum += total;
         longest = max(longest, total);
@@ -216,7 +216,7 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
     int base = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         const int b = b0 + lane;
-        const int n = a.batch <= 64 ? n0 : b < a.batch ? min(max(a.lengths[b], 0), most) : 0;
+        const int n = a.batch <= 64 ? n0 : b < a.batch ? max(a.lengths[b], 0) : 0;
         const Visible vis = vis_of(n);
         const int parts = b < a.batch ? max(1, (vis.total + c - 1) / c) : 0;
         int all;
@@ -225,11 +225,13 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
         if (mine) {
             const int l = __builtin_ctzll(mine);
             u.b = b0 + l;
-            u.n = __builtin_amdgcn_readlane(n, l);
-            u.first = __builtin_amdgcn_readlane(at, l);
+            const int length = __builtin_amdgcn_readlane(n, l);
+            u.n = min(length, most);
+            u.first = first_of(length);
+            u.unit0 = __builtin_amdgcn_readlane(at, l);
             u.parts = __builtin_amdgcn_readlane(parts, l);
-            u.vis = vis_of(u.n);
-            u.i0 = (want - u.first) * c;
+            u.vis = vis_of(length);
+            u.i0 = (want - u.unit0) * c;
             u.i1 = min(u.vis.total, u.i0 + c);
             break;
         }
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
     const int32_t *row = a.tables + (int64_t)u.b * a.cols;
     const int64_t head_bytes = (int64_t)D * ES << a.page_log2;   // of one head of one page
     const int in_page = (1 << a.page_log2) - 1;
-    const int first = a.window > 0 ? u.n - a.window : 0;          // of the window
+    const int first = u.first;
     struct Ids {
         int key;
         uint32_t p[2];
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
     __syncthreads();
     if (s_last != (uint32_t)u.parts - 1) return;
     if (threadIdx.x == 0) store_agent(counter, 0u);
-    join_parts<T, D, kDecodeThreads>(a.part + ((int64_t)u.first * heads + hh) * kSlot,
+    join_parts<T, D, kDecodeThreads>(a.part + ((int64_t)u.unit0 * heads + hh) * kSlot,
                                      kSlot * heads, u.parts, n_heads, 16, s_m[0], s_den, write,
                                      write_lse);
 }

@@ -181,6 +181,21 @@ def test_a_window_as_large_as_an_integer(window, sinks):
                        want, BF, False)
 
 
+@pytest.mark.parametrize("cdtype", [BF, E4])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 0), (40, 20), (1000, 3)])
+def test_lengths_beyond_the_table_leave_positions_where_they_are(window, sinks, cdtype):
+    """The window of a token at position 79, or 500, of a table for 64 reaches back from
+    there, in decode as in a prompt of one token."""
+    cache = su.HostCache([64, 64, 64, 30], 1, 16, 64, cdtype, seed=52, clean=True, spare_cols=0)
+    cache.lengths = torch.tensor([64, 80, 501, 30], dtype=torch.int32)
+    q = queries((4, 3, 64), BF, 53)
+    cu = [0, 1, 2, 3, 4]
+    want = su.attention(cache, 0, q, cu, window, sinks)
+    for kind in ("decode", "prompt"):
+        got = attend(kind, cache, q, cu, window=window, sinks=sinks)
+        su.check_attention(got, want, BF, kind == "prompt")
+
+
 # ---- Pools and tables ------------------------------------------------------
 
 def test_extend_serves_what_fits():
