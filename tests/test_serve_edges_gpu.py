@@ -38,21 +38,22 @@ def plant(cache, spots):
         cache.data[0, 1, int(cache.tables[0, t // cache.page]), 0, t % cache.page, d] = x
 
 
-def check_planted(got, clean, q, cu, spots, rounded):
+def check_planted(got, clean, q, cu, spots, rounded, reference=su.attention):
     """Dimensions that hold planted values: their sum (a weight is positive,
     however small) for rows that see them; all else as without them."""
     out, lse = got[0].clone(), got[1]
-    want = su.attention(clean, 0, q, cu)
+    want = reference(clean, 0, q, cu)
+    heads = q.shape[1] // clean.kv_heads        # those that read head 0
     pos = int(clean.lengths[0]) - (cu[1] - cu[0]) + torch.arange(cu[1] - cu[0])
     for d in {d for _, d, _ in spots}:
         total = sum(torch.where(t <= pos, x, 0.0) for t, e, x in spots if e == d)
         rows = ~total.isfinite()
         seen = out[:cu[1], :, d].float().cpu()
-        for h in range(q.shape[1]):
+        for h in range(heads):
             assert torch.equal(seen[rows, h].nan_to_num(7.0, 8.0, 9.0),
                                total[rows].nan_to_num(7.0, 8.0, 9.0)), (d, h)
-        patch = out[:cu[1], :, d]
-        patch[rows.cuda()] = want[0][:cu[1], :, d][rows].to(out.dtype).cuda()
+        patch = out[:cu[1], :heads, d]
+        patch[rows.cuda()] = want[0][:cu[1], :heads, d][rows].to(out.dtype).cuda()
     su.check_attention((out, lse), want, q.dtype, rounded)
 
 
@@ -85,6 +86,16 @@ def test_prompt_gives_the_infinities_that_it_sees(n, new, dim, dtype):
     cu = cumulative([new, 33])
     q = queries((cu[-1], 2, dim), dtype, 43)
     check_planted(attend("prompt", cache, q, cu), clean, q, cu, spots, True)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_equal_shares_give_the_infinities_that_they_see(dtype):
+    cache, clean = (su.HostCache([900, 40], 40, 16, 64, dtype, seed=62) for _ in range(2))
+    spots = planted(900)
+    plant(cache, spots)
+    cu = cumulative([300, 40])
+    q = queries((cu[-1], 160, 64), dtype, 63)
+    check_planted(attend("prompt", cache, q, cu), clean, q, cu, spots, True, su.attention_dense)
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
