@@ -1,8 +1,9 @@
 /*
  * moe_serve.h - C ABI of the serving operators around the expert layer on
  * MI355X (gfx950): attention over a paged key-value cache (one new token per
- * sequence, or whole prompts), the cache's own upkeep (append, extend, fork,
- * free, compact) and products with 4-bit weights.
+ * sequence, with or without prefixes that sequences share, or whole prompts), the
+ * cache's own upkeep (append, with or without rotary positions, extend, fork,
+ * free, compact), products with 4-bit weights, and the sampling of tokens.
  *
  * The cache.  Keys and values sit in pages of `page` consecutive positions:
  *   data     [layers][2][pages][kv_heads][page][head_dim]; index 0 of the
@@ -51,7 +52,7 @@
 extern "C" {
 #endif
 
-enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_E4M3 = 2 };
+enum { MOE_BF16 = 0, MOE_FP16 = 1, MOE_E4M3 = 2, MOE_F32 = 3 /* logits only */ };
 
 /* Sticky flags of a cache. */
 enum {
@@ -92,6 +93,32 @@ moe_status moe_kv_append_granted(const moe_kv_cache *kv, int32_t layer, const vo
                                  const void *v, int32_t dtype, int64_t token_stride,
                                  int64_t head_stride, int32_t tokens, const int32_t *cu,
                                  int32_t batch, const int32_t *granted, moe_stream_t stream);
+
+/* Rotary positions: of a head, dimensions first .. first + rot - 1 (both multiples of
+ * 16) are turned, in pairs (2j, 2j + 1) of them (interleaved) or (j, j + rot / 2).
+ * Pair j of a token at position p becomes, with t = turns[j] p turns,
+ *   amplitude (x0 cos t - x1 sin t), amplitude (x1 cos t + x0 sin t).
+ * turns: device memory, f64 [rot / 2], the pair's frequency over 2 pi, finite. */
+typedef struct {
+    const double *turns;
+    int32_t first, rot, interleaved;
+    float amplitude;
+} moe_rotary;
+
+/* As moe_kv_append_granted, with the keys, and the queries q beside them, turned by
+ * the tokens' positions in their sequences: q [tokens][q_heads][head_dim] with
+ * strides like k's, q_out the same without gaps (q itself where that has none; it
+ * overlaps nothing else).  Positions times frequencies are formed in 64 bits, the rest
+ * in f32, and what is turned is rounded once (an e4m3 key straight to its code).
+ * Keys and values that append leaves out are left out here too; the queries of their
+ * tokens are turned all the same.  Queries of a sequence without positions (length
+ * 0) come back as they are, rows outside [cu[0], cu[batch]) are not written. */
+moe_status moe_kv_append_rotated(const moe_kv_cache *kv, int32_t layer, const moe_rotary *rotary,
+                                 const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                 int32_t q_heads, const void *k, const void *v, int32_t dtype,
+                                 int64_t token_stride, int64_t head_stride, int32_t tokens,
+                                 const int32_t *cu, int32_t batch, const int32_t *granted,
+                                 void *q_out, moe_stream_t stream);
 
 /* Gives back the pages of n distinct sequences: each of their pages loses one
  * reference, their rows become -1 and their lengths 0. */
@@ -167,6 +194,75 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *cfg, i
                            const void *q, int32_t dtype, int64_t token_stride, int64_t head_stride,
                            int32_t tokens, const int32_t *cu, int32_t batch, void *out, float *lse,
                            void *workspace, uint32_t *counters, moe_stream_t stream);
+
+/* Decode where groups of sequences share a prefix: its keys and values are read once
+ * for a group instead of once for each sequence.  A plan says which: group g has
+ * the members members[cu[g]] .. members[cu[g + 1] - 1], each of the sequences 0 ..
+ * batch - 1 in one group at most, and positions 0 .. prefix[g] - 1 of all of them hold
+ * the same keys and values (as after fork; the pages of the member that is longest
+ * there are read, the first one of equal ones).  Lengths and tables are read when the
+ * call runs, so a plan holds while the members share their prefix: they may grow, pages
+ * may move, and a member may be freed (it then sees nothing), but not become another
+ * sequence.
+ * Host only: cu [groups + 1], members and prefix are host memory.  data NULL: only the
+ * sizes; else it receives plan->ints integers, which the caller copies to the device and
+ * puts the address of into plan->data. */
+typedef struct {
+    const int32_t *data;  /* device memory, 16-byte aligned */
+    int64_t ints;         /* its size */
+    int32_t batch, q_heads, kv_heads, head_dim;
+    int32_t units;        /* workgroups per kv head that read prefixes */
+    int32_t slots;        /* their partial results per kv head */
+    int32_t members;
+    int32_t window, sinks;
+    int32_t tail;         /* most positions that a sequence has by itself */
+} moe_attn_shared;
+moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *cfg, int32_t batch,
+                          int32_t groups, const int32_t *cu, const int32_t *members,
+                          const int32_t *prefix, moe_attn_shared *plan, int32_t *data);
+/* As moe_attn_workspace, of moe_attn_decode_shared. */
+moe_status moe_attn_shared_workspace(const moe_kv_cache *kv, const moe_attn_config *cfg,
+                                     const moe_attn_shared *plan, size_t *workspace,
+                                     size_t *counters);
+/* As moe_attn_decode, of plan->batch sequences. */
+moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config *cfg,
+                                  const moe_attn_shared *plan, int32_t layer, const void *q,
+                                  int32_t dtype, int64_t token_stride, int64_t head_stride,
+                                  void *out, float *lse, void *workspace, uint32_t *counters,
+                                  moe_stream_t stream);
+
+/* Draws a token from each row of logits x.  With weights w_i = exp((x_i - max) / T)
+ * and tokens ordered by logit, the largest first, equal ones by index, a row keeps
+ *   the first top_k tokens (0, or at least the vocabulary: all);
+ *   of those the ones before which the weights' sum is below top_p times that of
+ *   all of them (1 or more: all), but always the first;
+ *   of those the ones with w_i >= min_p (0: all; more than 1 counts as 1);
+ * and draws the first token in order of index at which the sum of kept weights
+ * exceeds u times their sum.  logprob: the logarithm of the probability that it is
+ * drawn, w_i over that sum.  T = 0 (below 2^-100, or NaN) takes the first largest logit,
+ * logprob 0.  Logits of -inf and NaN are never drawn; a row of nothing else gives -1
+ * and -inf.  With a logit of +inf only those have weight, 1 each.  u below 0 or NaN
+ * counts as 0, from 1 on the last kept token is drawn.  Weights and their sums are in
+ * 64 bits (44 bits behind the point in rows with thousands of equal logits at a
+ * border).
+ * Each filter is a device array by row, or NULL: the value for all rows beside it. */
+typedef struct {
+    const float *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    float temperature_all, top_p_all, min_p_all;
+    int32_t top_k_all;
+} moe_sampling;
+
+/* Bytes of workspace and of counters (both 16-byte aligned; see moe_attn_workspace) of
+ * calls with up to `rows` rows. */
+moe_status moe_sample_workspace(int32_t rows, int32_t vocab, size_t *workspace, size_t *counters);
+
+/* x [rows][vocab] (dtype MOE_BF16, MOE_FP16 or MOE_F32) with rows row_stride elements
+ * apart, at the type's own alignment; u f32 [rows]; token i32 [rows]; logprob f32 [rows].
+ * vocab up to 2^19. */
+moe_status moe_sample(const void *x, int32_t dtype, int64_t row_stride, int32_t rows, int32_t vocab,
+                      const float *u, const moe_sampling *filters, int32_t *token, float *logprob,
+                      void *workspace, uint32_t *counters, moe_stream_t stream);
 
 /* y = x W^T with W[n][j] = (code[n][j] - zero[n][j / group]) * scale[n][j / group]:
  * codes u8 [n][k / 2] (column 2j in the low half of byte j), scales [n][k /

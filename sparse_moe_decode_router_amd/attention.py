@@ -5,14 +5,16 @@ sequences' page tables and lengths, the pages' reference counts) to the
 library's operators on them:
 
   append   new keys and values into their pages (converted to e4m3 where the
-           cache holds 8 bits)
+           cache holds 8 bits); append_rotated turns keys and queries by their
+           positions on the way
   extend   longer sequences, and pages for them
   fork     copies of sequences that share their full pages
   free     sequences given up
   compact  the pages in use moved together
 
 ``PagedAttention`` plans attention over such a cache: ``decode`` for one new
-token per sequence, ``prompt`` for many.  All of it runs on the cache's device,
+token per sequence, ``prompt`` for many, ``decode_shared`` for one per sequence
+where groups of them share a prefix.  All of it runs on the cache's device,
 on that device's current stream, reads lengths and tables on the device and
 never waits for it, so calls can be captured into a HIP graph.
 include/moe_serve.h states layouts and formulas.
@@ -20,13 +22,13 @@ include/moe_serve.h states layouts and formulas.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
 from .binding import MoEError
-from .serving import (DTYPES, AttnConfig, Cache, StreamSpace, check, current_device, lib,
-                      raw_stream, require, tensor)
+from .serving import (DTYPES, AttnConfig, Cache, SharedPlan, StreamSpace, check, current_device,
+                      lib, raw_stream, require, tensor)
 
 E4M3_MAX = 448.0
 MAX_TOKENS = 1 << 24  # of a prompt call
@@ -160,6 +162,53 @@ class PagedKV:
             None if cu is None else cu.data_ptr(), batch,
             self._granted_ptr if only_granted else None, raw_stream(self._index)), "append")
 
+    def append_rotated(self, layer: int, q, k, v, rotary, cu=None, only_granted: bool = False,
+                       out=None):
+        """append() of keys turned by their positions, with the queries q [tokens,
+        q_heads, head_dim] of the same tokens, which come back turned by the same
+        (in out, or a new tensor; out may be q where q is contiguous).  rotary: a
+        rotary.Rotary on the cache's device.  The queries of a sequence of length 0
+        come back as they are; rows that cu leaves out are not written."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.append_rotated(layer, q, k, v, rotary, cu, only_granted, out)
+        dim, dev = self.head_dim, self.device
+        ts, hs = _rows(k, "k", self.kv_heads, dim, self.compute_dtypes, dev)
+        if _rows(v, "v", self.kv_heads, dim, (k.dtype,), dev) != (ts, hs) or v.shape != k.shape:
+            raise MoEError("v: the shape and strides of k are needed")
+        if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[1] < 1:
+            raise MoEError(f"q: a tensor of shape (tokens, q_heads, {dim}) is needed")
+        q_heads, tokens = q.shape[1], k.shape[0]
+        qts, qhs = _rows(q, "q", q_heads, dim, (k.dtype,), dev)
+        if q.shape[0] != tokens:
+            raise MoEError(f"q: {q.shape[0]} tokens, and {tokens} keys")
+        if cu is None:
+            batch = tokens
+            if batch > self.seqs:
+                raise MoEError(f"k: {batch} tokens for {self.seqs} sequences")
+        else:
+            tensor(cu, "cu", torch.int32, device=dev)
+            batch = cu.numel() - 1
+            if cu.dim() != 1 or not 0 <= batch <= self.seqs:
+                raise MoEError(f"cu: 1 to {self.seqs + 1} entries are needed, got shape "
+                               f"{tuple(cu.shape)}")
+        if not 0 <= layer < self.layers:
+            raise MoEError(f"layer {layer} of {self.layers}")
+        if rotary.device != dev or rotary.last > dim:
+            raise MoEError(f"rotary: on {rotary.device}, up to dimension {rotary.last}; heads are "
+                           f"on {dev} and of {dim}")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            tensor(out, "out", q.dtype, q.shape, dev)
+            require(out.data_ptr() % 16 == 0, "out: 16-byte alignment is needed")
+        check(self._lib.moe_kv_append_rotated(
+            self._ref, layer, rotary._ref, q.data_ptr(), qts, qhs, q_heads, k.data_ptr(),
+            v.data_ptr(), DTYPES[k.dtype], ts, hs, tokens, None if cu is None else cu.data_ptr(),
+            batch, self._granted_ptr if only_granted else None, out.data_ptr(),
+            raw_stream(self._index)), "append_rotated")
+        return out
+
     def free(self, seqs) -> None:
         """Gives up the (distinct) sequences of an i32 list."""
         if current_device() != self._index:
@@ -265,6 +314,40 @@ class PagedAttention:
                                         stream), "decode")
         return out, lse
 
+    def share(self, groups: Sequence[Sequence[int]], prefix: Sequence[int],
+              batch: Optional[int] = None) -> "SharedPrefix":
+        """A plan for decode_shared of the sequences 0 .. batch - 1 (None: as many as
+        this one is for).  groups: lists of sequences, each sequence in one at
+        most; prefix: as many numbers of positions, from the first on, whose keys
+        and values are the same in all of a group.  After fork that is what the
+        parent had; its last page, if in part, may be counted in or not."""
+        return SharedPrefix(self, groups, prefix, self.batch if batch is None else batch)
+
+    def decode_shared(self, layer: int, q, shared: "SharedPrefix"):
+        """decode() of the plan's sequences: q [shared.batch, q_heads, head_dim]; the
+        keys and values of shared prefixes are read once for a group.  The results
+        are decode()'s up to rounding: of what a prefix adds, weights are held in q's
+        type, as prompt() does."""
+        if current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.decode_shared(layer, q, shared)
+        kv = self.kv
+        if not isinstance(shared, SharedPrefix) or shared.attention is not self:
+            raise MoEError("shared: a plan that share() of this object made is needed")
+        ts, hs = _rows(q, "q", self.q_heads, kv.head_dim, kv.compute_dtypes, kv.device)
+        if q.shape[0] != shared.batch:
+            raise MoEError(f"q: {q.shape[0]} sequences, planned for {shared.batch}")
+        if not 0 <= layer < kv.layers:
+            raise MoEError(f"layer {layer} of {kv.layers}")
+        out = torch.empty(q.shape, dtype=q.dtype, device=kv.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=kv.device)
+        stream = raw_stream(self._index)
+        w, c, _ = shared._space.get(stream)
+        check(self._lib.moe_attn_decode_shared(kv._ref, self._cfg, shared._ref, layer, q.data_ptr(),
+                                               DTYPES[q.dtype], ts, hs, out.data_ptr(),
+                                               lse.data_ptr(), w, c, stream), "decode_shared")
+        return out, lse
+
     def prompt(self, layer: int, q, cu, max_new: Optional[int] = None):
         """q [tokens, q_heads, head_dim]; cu [batch + 1] i32: rows cu[b] ..
         cu[b + 1] - 1 are the last positions of sequence b.  max_new: the most
@@ -299,3 +382,52 @@ class PagedAttention:
                                         ts, hs, tokens, cu.data_ptr(), batch, out.data_ptr(),
                                         lse.data_ptr(), w, c, stream), "prompt")
         return out, lse
+
+
+class SharedPrefix:
+    """Which of the sequences of a PagedAttention share which prefix, and how the
+    work on it is split (PagedAttention.share makes it).  It holds while members
+    share their prefix: they may grow, their pages may move (compact), and members
+    may be freed, which then see nothing.  A sequence of another content in a
+    member's place needs a new plan.  The plan is kept until its work on every
+    stream is done, and by graphs that captured it."""
+
+    def __init__(self, attention: PagedAttention, groups, prefix, batch: int):
+        groups, prefix = [list(g) for g in groups], list(prefix)
+        require(len(groups) == len(prefix),
+                f"{len(groups)} groups, and prefixes of {len(prefix)}")
+        require(isinstance(batch, int) and 1 <= batch <= attention.batch,
+                f"batch {batch!r}: 1 to {attention.batch} sequences are needed")
+        seen = set()
+        for g in groups:
+            for m in g:
+                require(isinstance(m, int) and 0 <= m < batch, f"sequence {m!r} of {batch}")
+                require(m not in seen, f"sequence {m} is named twice")
+                seen.add(m)
+        for p in prefix:
+            require(isinstance(p, int) and 0 <= p < 1 << 31,
+                    f"prefix: integers from 0 to 2^31 - 1 are needed, got {p!r}")
+        # (An empty group has no use, and there may be more of them than sequences.)
+        pairs = [(g, p) for g, p in zip(groups, prefix) if g]
+        cu, members = [0], []
+        for g, _ in pairs:
+            members += g
+            cu.append(len(members))
+        ints = lambda v: (ctypes.c_int32 * max(1, len(v)))(*v)  # noqa: E731
+        cu, members, prefix = ints(cu), ints(members), ints([p for _, p in pairs])
+        self.attention, self.batch, self.plan = attention, batch, SharedPlan()
+        kv, L = attention.kv, attention._lib
+        self._ref = ctypes.addressof(self.plan)
+
+        def make(data):
+            check(L.moe_attn_share(kv._ref, attention._cfg, batch, len(pairs), cu, members, prefix,
+                                   self._ref, data), "share")
+        make(None)
+        host = torch.empty(max(1, self.plan.ints), dtype=torch.int32)
+        make(host.data_ptr())
+        self._data = host.to(kv.device)
+        self.plan.data = self._data.data_ptr()
+        w, c = ctypes.c_size_t(), ctypes.c_size_t()
+        check(L.moe_attn_shared_workspace(kv._ref, attention._cfg, self._ref, ctypes.byref(w),
+                                          ctypes.byref(c)), "workspace")
+        self._space = StreamSpace(kv.device, w.value, c.value)

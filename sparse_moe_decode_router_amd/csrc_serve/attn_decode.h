@@ -181,24 +181,33 @@ __device__ __forceinline__ void sum_not_finite(Each each, Put put) {
 
 struct DecodeUnit {
     int b, n;        // sequence (-1: none), its length as far as its table goes
-    int first;       // of its window's positions (0: no window)
+    int first;       // of its window's positions (0: no window), behind a shared prefix
+    int sinks;       // 0 behind a shared prefix, which holds them
     Visible vis;
     int i0, i1;      // visible blocks of this unit
     int unit0, parts;  // the row's first unit (per kv head), and how many there are
 };
 
-// The unit of index `want` among all sequences' units (per kv head).
+// The unit of index `want` among all sequences' units (per kv head).  Shared: of what
+// is behind the sequences' shared prefixes.
+template <bool Shared>
 __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
     const int lane = lane_id();
     const int most = a.cols << a.page_log2;
     // The token's position is the length's, also where the table is too short for it.
-    auto first_of = [&](int n) { return a.window > 0 ? max(0, n - a.window) : 0; };
-    auto vis_of = [&](int n) { return visible<5>(min(n, most), first_of(n), a.sinks); };
-    int sum = 0, longest = 0, n0 = 0;
+    // p: a shared prefix.
+    auto first_of = [&](int n, int p) { return max(p, a.window > 0 ? max(0, n - a.window) : 0); };
+    auto sinks_of = [&](int p) { return Shared && p > 0 ? 0 : a.sinks; };
+    auto vis_of = [&](int n, int p) {
+        return visible<5>(min(n, most), first_of(n, p), sinks_of(p));
+    };
+    auto prefix_of = [&](int b) { return Shared && b < a.batch ? a.shared_rows[b].prefix : 0; };
+    int sum = 0, longest = 0, n0 = 0, p0 = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         const int b = b0 + lane;
         n0 = b < a.batch ? max(a.lengths[b], 0) : 0;
-        const int total = vis_of(n0).total;
+        p0 = prefix_of(b);
+        const int total = vis_of(n0, p0).total;
         sum += total;
         longest = max(longest, total);
     }
@@ -217,7 +226,8 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         const int b = b0 + lane;
         const int n = a.batch <= 64 ? n0 : b < a.batch ? max(a.lengths[b], 0) : 0;
-        const Visible vis = vis_of(n);
+        const int p = a.batch <= 64 ? p0 : prefix_of(b);
+        const Visible vis = vis_of(n, p);
         const int parts = b < a.batch ? max(1, (vis.total + c - 1) / c) : 0;
         int all;
         const int at = base + wave_excl_scan(parts, &all);
@@ -226,11 +236,13 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
             const int l = __builtin_ctzll(mine);
             u.b = b0 + l;
             const int length = __builtin_amdgcn_readlane(n, l);
+            const int prefix = Shared ? __builtin_amdgcn_readlane(p, l) : 0;
             u.n = min(length, most);
-            u.first = first_of(length);
+            u.first = first_of(length, prefix);
+            u.sinks = sinks_of(prefix);
             u.unit0 = __builtin_amdgcn_readlane(at, l);
             u.parts = __builtin_amdgcn_readlane(parts, l);
-            u.vis = vis_of(length);
+            u.vis = vis_of(length, prefix);
             u.i0 = (want - u.unit0) * c;
             u.i1 = min(u.vis.total, u.i0 + c);
             break;
@@ -240,7 +252,85 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
     return u;
 }
 
-template <class T, bool F8, int D>
+// Joins a row group's own parts, as join_parts does, with those of its shared prefix.
+// (The prefix's were written by a launch before this one, by lanes that held 32x32
+// tiles of them: 16-byte piece (d / 8, row % 32, d / 4 % 2) of a wave's 32 rows.)
+template <class T, int D, int Threads, class Row, class Lse>
+__device__ __forceinline__ void join_with_prefix(const float *part, int64_t stride, int n_parts,
+                                                 int rows, const float *pre, int64_t pre_stride,
+                                                 int n_pre, int row0, float *mx, float *den,
+                                                 Row write, Lse write_lse) {
+    const int tid = threadIdx.x;
+    constexpr int kRows = 128, kWave = 32 * (D + 2);
+    auto slot_of = [&](int row, int u) {    // row: of the group
+        return pre + ((int64_t)(row / kRows) * n_pre + u) * pre_stride + (row % kRows >> 5) * kWave;
+    };
+    for (int row = tid >> 4; row < rows; row += Threads / 16) {
+        float m = kNoMax, l = 0.f;
+        const int at = 32 * D + ((row0 + row) & 31);
+        for (int u = tid & 15; u < n_parts; u += 16)
+            m = fmaxf(m, load_agent(part + u * stride + 16 * D + row));
+        for (int u = tid & 15; u < n_pre; u += 16) m = fmaxf(m, slot_of(row0 + row, u)[at]);
+#pragma unroll
+        for (int s = 8; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
+        for (int u = tid & 15; u < n_parts; u += 16) {
+            const float *p = part + u * stride + 16 * D;
+            l += load_agent(p + 16 + row) * exp2_(load_agent(p + row) - m);
+        }
+        for (int u = tid & 15; u < n_pre; u += 16) {
+            const float *p = slot_of(row0 + row, u) + at;
+            l += p[32] * exp2_(p[0] - m);
+        }
+#pragma unroll
+        for (int s = 8; s >= 1; s >>= 1) l += __shfl_xor(l, s);
+        if ((tid & 15) == 0) {
+            mx[row] = m;
+            den[row] = l;
+            write_lse(row, l != 0.f ? (m + log2_(l) - T::kOff) * kLn2 : -__builtin_inff());
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * (D / 4); i += Threads) {
+        const int row = i / (D / 4), d = 4 * (i % (D / 4));
+        const float m = mx[row], l = den[row];
+        f32x4 sum = zero4();
+        for (int u = 0; u < n_parts; u += 8) {
+            f32x4 x[8];
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float *p = part + min(u + j, n_parts - 1) * stride;
+                x[j] = __builtin_bit_cast(f32x4, buf_ld16<true>(buf_rsrc(p), 4u * (row * D + d)));
+                f[j] = load_agent(p + 16 * D + row);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (u + j < n_parts) sum += x[j] * part_factor(f[j] - m);
+        }
+        const int at = 32 * D + ((row0 + row) & 31);
+        const int piece = 256 * (d >> 3) + 4 * (((row0 + row) & 31) + 8 * (d & 4));
+        for (int u = 0; u < n_pre; u += 8) {
+            f32x4 x[8];
+            float f[8], w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float *p = slot_of(row0 + row, min(u + j, n_pre - 1));
+                x[j] = ldf4(p + piece);
+                f[j] = p[at];
+                w[j] = p[at + 32];
+            }
+            // (A part that is empty for a row may have left no sums at all.)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (u + j < n_pre && w[j] != 0.f) sum += x[j] * part_factor(f[j] - m);
+        }
+        write(row, d, l != 0.f ? sum * (1.f / l) : zero4());
+    }
+}
+
+// Shared: of what is behind the sequences' shared prefixes, joined with the partial
+// results that a launch before this one left of those.
+template <class T, bool F8, int D, bool Shared = false>
 __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArgs a) {
     typedef DecodeTile<T, F8, D> Tile;
     constexpr int W = kDecodeWaves, KS = Tile::KS, E = Tile::E, ES = Tile::ES;
@@ -252,8 +342,11 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
     const int lane = lane_id(), wave = wave_index(), c = lane & 15, g = lane >> 4;
     const int heads = a.kv_heads * a.head_groups;
     const int hh = (int)blockIdx.x % heads, su = (int)blockIdx.x / heads;
-    const DecodeUnit u = find_unit(a, su);
+    const DecodeUnit u = find_unit<Shared>(a, su);
     if (u.b < 0) return;
+    SharedRow pre = {0, 0, 0, 0};
+    if constexpr (Shared) pre = a.shared_rows[u.b];
+    const bool whole_row = u.parts == 1 && (!Shared || pre.prefix == 0);
     const int h = hh / a.head_groups, hg = hh % a.head_groups;
     const int head0 = h * a.group + 16 * hg;             // first query head of the columns
     const int n_heads = min(16, a.group - 16 * hg);
@@ -300,7 +393,7 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
     // Whether key 16 (r / 4) + 4 g + r % 4 of a block is seen.
     auto sees_of = [&](const Ids &x, int r) {
         const int key = x.key + 16 * (r >> 2) + 4 * g + (r & 3);
-        return (key < u.n) & (x.p[r >> 2] < (uint32_t)a.pages) & ((key >= first) | (key < a.sinks));
+        return (key < u.n) & (x.p[r >> 2] < (uint32_t)a.pages) & ((key >= first) | (key < u.sinks));
     };
 
     int i = u.i0 + wave;
@@ -327,7 +420,7 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
             // and their values, which may be anything, are taken as zero.
             const bool whole = now.key + 32 <= u.n && now.p[0] < (uint32_t)a.pages &&
                                now.p[1] < (uint32_t)a.pages &&
-                               (now.key >= first || now.key + 32 <= a.sinks);
+                               (now.key >= first || now.key + 32 <= u.sinks);
             if (!whole) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
@@ -435,7 +528,7 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
             sum += ldf4(&s_o[w][head][d]) * f;
             den += s_l[w][head] * f;
         }
-        if (u.parts == 1) {
+        if (whole_row) {
             write(head, d, den != 0.f ? sum * (1.f / den) : zero4());
             if (d == 0)
                 write_lse(head, den != 0.f ? (top + log2_(den) - T::kOff) * kLn2
@@ -448,7 +541,7 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
             }
         }
     }
-    if (u.parts == 1) return;
+    if (whole_row) return;
 
     // Arrival: this unit's stores are complete before it is counted.
     wait_vm_all();
@@ -459,6 +552,17 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
     __syncthreads();
     if (s_last != (uint32_t)u.parts - 1) return;
     if (threadIdx.x == 0) store_agent(counter, 0u);
+    if constexpr (Shared) {
+        if (pre.prefix > 0) {
+            constexpr int64_t kPrefixSlot = 128 * (D + 2);
+            join_with_prefix<T, D, kDecodeThreads>(
+                a.part + ((int64_t)u.unit0 * heads + hh) * kSlot, kSlot * heads, u.parts, n_heads,
+                a.shared_part + ((int64_t)pre.slot * a.kv_heads + h) * kPrefixSlot,
+                kPrefixSlot * a.kv_heads, pre.parts, pre.member * a.group + 16 * hg, s_m[0], s_den,
+                write, write_lse);
+            return;
+        }
+    }
     join_parts<T, D, kDecodeThreads>(a.part + ((int64_t)u.unit0 * heads + hh) * kSlot,
                                      kSlot * heads, u.parts, n_heads, 16, s_m[0], s_den, write,
                                      write_lse);

@@ -137,7 +137,9 @@ __device__ __forceinline__ PromptArgs &prompt_args() {
     return *a;
 }
 
-template <class T, bool F8, int D>
+// Shared: the rows are the new tokens of a group of sequences, whose keys are their
+// shared prefix; only partial results are written.
+template <class T, bool F8, int D, bool Shared = false>
 __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_prompt(
     const AttnArgs) {
     typedef PromptTile<D> Tile;
@@ -188,7 +190,25 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
     int b = -1, tile = 0, index = 0;   // the row tile, and its place among all
     Seq seq = {};
     int64_t chunk = 0, at = 0, x0 = 0, x1 = 0;
-    if (a.units == 0) {
+    SharedUnit su = {};
+    if constexpr (Shared) {
+        su = a.shared_units[unit];
+        // The prefix is read from the member that has most of it.
+        int best = -1;
+        for (int i0 = 0; i0 < su.n_members; i0 += 64) {
+            const int i = i0 + lane;
+            const int bb = a.members[su.members + min(i, su.n_members - 1)];
+            const int have = i < su.n_members ? min(max(a.lengths[bb], 0), su.prefix) : -1;
+            int top = have;
+#pragma unroll
+            for (int y = 32; y >= 1; y >>= 1) top = max(top, __shfl_xor(top, y));
+            const int most_here = (int)uniform(top);
+            if (most_here > best) {
+                best = most_here;
+                b = __builtin_amdgcn_readlane(bb, __builtin_ctzll(__ballot(have == top)));
+            }
+        }
+    } else if (a.units == 0) {
         // One row tile, or a part of one: unit = tile * split + part.
         index = unit / a.split;
         int base = 0;
@@ -256,19 +276,53 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
     for (;;) {
         PromptArgs &a = prompt_args();
         // More than the tokens make up: a cu that decreases counts rows twice.
-        if (index >= a.row_tiles) return;
-        const int n_new = seq.n_new, tok0 = seq.tok0;
-        const int n_seen = min(seq.n, most);
-        const int row0 = tile * kPromptRows;
+        if (!Shared && index >= a.row_tiles) return;
+        const int n_new = Shared ? su.n_members : seq.n_new, tok0 = seq.tok0;
+        const int n_seen = min(Shared ? su.prefix : seq.n, most);
+        const int row0 = Shared ? su.row0 : tile * kPromptRows;
         const int rows = min(kPromptRows, n_new * a.group - row0);
         const int past = seq.n - n_new;
-        const int pos_lo = past + row0 / a.group, pos_hi = past + (row0 + rows - 1) / a.group;
-        const Visible vis = visible_of(seq, row0);
+        int pos_lo = past + row0 / a.group, pos_hi = past + (row0 + rows - 1) / a.group;
+        Visible vis;
+        if constexpr (Shared) {
+            // Every row has a position of its own; those of sequences that hold nothing
+            // see nothing, and widen no window.
+            int lo = 0x7FFFFFFF, lo_seen = 0x7FFFFFFF, hi = -1;
+#pragma unroll
+            for (int y = 0; y < kPromptRows; y += 64) {
+                const int r = row0 + min(y + lane, rows - 1);
+                const int p = max(a.lengths[a.members[su.members + r / a.group]], 0) - 1;
+                lo = min(lo, p);
+                lo_seen = p >= 0 ? min(lo_seen, p) : lo_seen;
+                hi = max(hi, p);
+            }
+#pragma unroll
+            for (int y = 32; y >= 1; y >>= 1) {
+                lo = min(lo, __shfl_xor(lo, y));
+                lo_seen = min(lo_seen, __shfl_xor(lo_seen, y));
+                hi = max(hi, __shfl_xor(hi, y));
+            }
+            pos_lo = (int)uniform(lo);
+            pos_hi = (int)uniform(hi);
+            lo_seen = (int)uniform(lo_seen);
+            vis = visible<6>(max(0, min(n_seen, pos_hi + 1)),
+                             a.window > 0 && pos_hi >= 0 ? max(0, lo_seen - a.window + 1) : 0,
+                             a.sinks);
+        } else {
+            vis = visible_of(seq, row0);
+        }
         // This workgroup's share of it, and where the parts of a split one go.
         constexpr int64_t kSlot = kPromptRows * (D + 2);
         int i0, i1, parts, part;
         int64_t slot0, weight = kPromptFixed + max(1, vis.total);
-        if (a.units == 0) {
+        if constexpr (Shared) {
+            const int c = (vis.total + su.parts - 1) / su.parts;
+            parts = 2;   // never the only one
+            part = su.part;
+            i0 = min(part * c, vis.total);
+            i1 = min(vis.total, i0 + c);
+            slot0 = ((int64_t)su.slot * a.kv_heads + h) * kSlot;
+        } else if (a.units == 0) {
             const int c = max(1, (vis.total + a.split - 1) / a.split);
             parts = max(1, (vis.total + c - 1) / c);
             part = unit % a.split;
@@ -290,13 +344,16 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         }
         // This lane's row.
         const int my = row0 + min(32 * wave + col, rows - 1);
-        const int my_tok = my / a.group, pos = past + my_tok;
+        const int my_tok = my / a.group;
+        const int my_seq = Shared ? a.members[su.members + my_tok] : 0;
+        const int pos = Shared ? max(a.lengths[my_seq], 0) - 1 : past + my_tok;
         const int from = a.window > 0 ? max(pos, -1) - a.window : -1;   // sees keys above it
         const int64_t out_row =
             (int64_t)(tok0 + my_tok) * a.kv_heads * a.group + h * a.group + (my - my_tok * a.group);
         u32x4 q[KS];
         {
-            const uint16_t *qp = (const uint16_t *)a.q + (tok0 + my_tok) * a.q_token +
+            const uint16_t *qp = (const uint16_t *)a.q +
+                                 (Shared ? my_seq : tok0 + my_tok) * a.q_token +
                                  (h * a.group + (my - my_tok * a.group)) * a.q_head + 8 * half;
 #pragma unroll
             for (int j = 0; j < KS; ++j) q[j] = ld16(qp + 16 * j);
@@ -645,6 +702,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         PromptArgs &z = prompt_args();
         // Part k's slot; of equal shares, part 0 has the second slot of its unit.
         auto slot_of = [&](int k) {
+            if constexpr (Shared) return z.shared_part + slot0;
             if (z.units == 0) return z.part + slot0 + (int64_t)k * z.kv_heads * kSlot;
             return z.part + slot0 + (int64_t)(k == 0 ? 1 : 2 * k) * z.kv_heads * kSlot;
         };
@@ -672,6 +730,8 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         const uint32_t at_part = 4u * (wave * 32 * (D + 2));
         if (parts > 1) {
             const rsrc_t to = buf_rsrc(slot_of(part));
+            // (An empty part of a shared prefix is known by its sum of weights.)
+            if (!Shared || i0 < i1)
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -753,6 +813,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
                 }
             }
         }
+        if constexpr (Shared) return;
         if (parts > 1) {
             const int64_t group = (int64_t)index * z.kv_heads + h;
             wait_vm_all();

@@ -27,30 +27,6 @@ struct AppendArgs {
     int32_t per_block;         // tokens a workgroup takes
 };
 
-// Eight values -> eight e4m3 codes of x / scale.  The division is the IEEE one
-// (a reciprocal could move a value over a rounding border); the clamp keeps NaN.
-template <class T>
-__device__ __forceinline__ u32x2 to_e4m3(u32x4 x, float scale) {
-    uint32_t r[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float f[4] = {T::lo(x[2 * i]), T::hi(x[2 * i]), T::lo(x[2 * i + 1]), T::hi(x[2 * i + 1])};
-        uint32_t nan = 0, sign = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[j] = f[j] / scale;
-            nan |= f[j] != f[j] ? 0xFFu << 8 * j : 0u;
-            sign |= __float_as_uint(f[j]) >> 31 << (8 * j + 7);
-            f[j] = fminf(fmaxf(f[j], -448.f), 448.f);
-        }
-        uint32_t w = 0;
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], w, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
-        r[i] = (w & ~nan) | (nan & (0x7F7F7F7Fu | sign));
-    }
-    return (u32x2){r[0], r[1]};
-}
-
 // A workgroup takes `per_block` consecutive tokens, a thread chunks of eight
 // elements of one head's row (keys and values).  The first token's sequence is
 // found by bisection with uniform loads, later ones from there.  Bound by memory:

@@ -1,91 +1,18 @@
-// serve.hip - host side of the serving operators: argument checks, launch
-// rules and the C ABI declared in include/moe_serve.h.
-#include <hip/hip_runtime.h>
-
-#include <algorithm>
-#include <atomic>
+// serve.hip - host side of attention, the cache's upkeep and the 4-bit products:
+// argument checks, launch rules and their part of the C ABI declared in
+// include/moe_serve.h.
+#include "serve_host.h"
 
 #include "attn_decode.h"
 #include "attn_prompt.h"
 #include "kv_pages.h"
-#include "moe_serve.h"
 #include "w4_linear.h"
 
 using namespace moe::serve;
 
 namespace {
 
-thread_local int32_t g_last_hip = 0;
-
-moe_status hip_error(hipError_t e) {
-    g_last_hip = (int32_t)e;
-    return MOE_ERR_HIP;
-}
-moe_status launched() {
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? MOE_OK : hip_error(e);
-}
-
-// Compute units of the current device (0: unknown yet, -1: not gfx950).
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_cus[kMaxDevices];
-
-moe_status compute_units(int *cus) {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return hip_error(e);
-    if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
-    int n = g_cus[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        hipDeviceProp_t p;
-        e = hipGetDeviceProperties(&p, dev);
-        if (e != hipSuccess) return hip_error(e);
-        const bool ours = p.gcnArchName[0] == 'g' && std::equal(p.gcnArchName, p.gcnArchName + 6, "gfx950");
-        n = ours ? p.multiProcessorCount : -1;
-        g_cus[dev].store(n, std::memory_order_relaxed);
-    }
-    if (n < 0) return MOE_ERR_UNSUPPORTED;
-    *cus = n;
-    return MOE_OK;
-}
-
-bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-int log2_of(int v) {
-    int r = 0;
-    while ((1 << r) < v) ++r;
-    return r;
-}
-int64_t plane_bytes(const moe_kv_cache &kv) {
-    return (int64_t)kv.pages * kv.kv_heads * kv.page * kv.head_dim * (kv.dtype == MOE_E4M3 ? 1 : 2);
-}
-char *plane(const moe_kv_cache &kv, int layer, int which) {
-    return (char *)kv.data + (2 * (int64_t)layer + which) * plane_bytes(kv);
-}
-
-constexpr int kMaxRows = 1 << 24;  // sequences, tokens of a call, pairs of a list
-// A grid's first axis has below 2^32 threads, its second up to 2^16 workgroups.
-constexpr int64_t kMaxGrid256 = (1ll << 24) - 1;   // of 256 threads each
 constexpr int kMaxW4Tokens = 1 << 21;              // of one launch: 2^15 times 64
-
-// Workgroups that one decode call aims at: with four waves each, three of them
-// share a compute unit.
-constexpr int kUnitsPerCu = 4;
-// What a plan is made for; the device a plan runs on has the same number.
-constexpr int kPlanCus = 256;
-
-int decode_split(const moe_kv_cache &kv, const moe_attn_config &c) {
-    const int group = c.q_heads / kv.kv_heads, hg = (group + 15) / 16;
-    const int heads = kv.kv_heads * hg;
-    // No unit is smaller than a block per wave.
-    int64_t keys = c.longest;
-    if (c.window > 0) keys = std::min<int64_t>(keys, (int64_t)c.window + c.sinks + 62);
-    const int64_t most = (int64_t)c.batch * ((keys + 127) / 128);
-    return (int)std::max<int64_t>(
-        1, std::min<int64_t>(most, std::max(1, kPlanCus * kUnitsPerCu / heads)));
-}
-
-// Workgroups of a prompt call that the chip holds at once.
-int prompt_slots(int head_dim) { return kPlanCus * (head_dim <= 128 ? 2 : 1); }
 
 // Row tiles as workgroups, split over the keys where there are few of them.
 // With more of them than fit at once, long and short ones would leave the chip
@@ -165,24 +92,6 @@ int64_t prompt_slots_up_to(const moe_kv_cache &kv, const moe_attn_config &c, int
 }
 
 template <class F>
-moe_status with_dim(int d, F f) {
-    switch (d) {
-        case 64: return f(std::integral_constant<int, 64>());
-        case 96: return f(std::integral_constant<int, 96>());
-        case 128: return f(std::integral_constant<int, 128>());
-        case 192: return f(std::integral_constant<int, 192>());
-        case 256: return f(std::integral_constant<int, 256>());
-    }
-    return MOE_ERR_UNSUPPORTED;
-}
-// Calls f with the compute type and whether the cache holds e4m3.
-template <class F>
-moe_status with_types(int dtype, bool f8, F f) {
-    if (dtype == MOE_BF16) return f8 ? f(Bf16(), std::true_type()) : f(Bf16(), std::false_type());
-    return f8 ? f(Fp16(), std::true_type()) : f(Fp16(), std::false_type());
-}
-
-template <class F>
 moe_status with_group(int group, bool z, F f) {
     auto g = [&](auto gl) { return z ? f(gl, std::true_type()) : f(gl, std::false_type()); };
     if (group == 32) return g(std::integral_constant<int, 5>());
@@ -234,51 +143,6 @@ moe_status w4_launch(const W4Args &a, int cus, hipStream_t stream) {
     return rt == 1   ? go(k_w4<T, 4, 16, 1, 8, 1, GL, Z>, 4, 1, 8)
            : rt == 2 ? go(k_w4<T, 4, 16, 2, 8, 1, GL, Z>, 4, 2, 8)
                      : go(k_w4<T, 4, 16, 4, 4, 1, GL, Z>, 4, 4, 4);
-}
-
-moe_status check_types(const moe_kv_cache &kv, int dtype) {
-    if (dtype != MOE_BF16 && dtype != MOE_FP16) return MOE_ERR_INVALID_ARG;
-    if (kv.dtype != MOE_E4M3 && kv.dtype != dtype) return MOE_ERR_INVALID_ARG;
-    return MOE_OK;
-}
-moe_status check_strides(int64_t token, int64_t head, int heads, int d) {
-    if (token < 0 || head < 0 || (token | head) % 8) return MOE_ERR_INVALID_ARG;
-    if (heads > 1 && head < d) return MOE_ERR_INVALID_ARG;
-    return MOE_OK;
-}
-
-AttnArgs attn_args(const moe_kv_cache &kv, const moe_attn_config &c, int layer) {
-    AttnArgs a = {};
-    a.k = plane(kv, layer, 0);
-    a.v = plane(kv, layer, 1);
-    a.tables = kv.tables;
-    a.lengths = kv.lengths;
-    a.k_scale = kv.k_scale;
-    a.v_scale = kv.v_scale;
-    a.scale = c.scale * moe::serve::kLog2e;
-    a.pages = kv.pages;
-    a.cols = kv.cols;
-    a.page_log2 = log2_of(kv.page);
-    a.kv_heads = kv.kv_heads;
-    a.group = c.q_heads / kv.kv_heads;
-    a.head_groups = (a.group + 15) / 16;
-    a.window = c.window;
-    a.sinks = c.window > 0 ? c.sinks : 0;
-    return a;
-}
-
-moe_status check_attn(const moe_kv_cache *kv, const moe_attn_config *c, int layer, const void *q,
-                      int dtype, int64_t token, int64_t head, int batch, const void *out,
-                      const void *lse, const void *ws, const void *counters) {
-    moe_status s = moe_attn_validate(kv, c);
-    if (s != MOE_OK) return s;
-    if (!q || !out || !lse || batch < 1 || batch > c->batch || layer < 0 || layer >= kv->layers)
-        return MOE_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return MOE_ERR_INVALID_ARG;
-    if ((s = check_types(*kv, dtype)) != MOE_OK) return s;
-    if ((s = check_strides(token, head, c->q_heads, kv->head_dim)) != MOE_OK) return s;
-    if (!aligned(ws, 16) || !aligned(counters, 16)) return MOE_ERR_WORKSPACE;
-    return MOE_OK;
 }
 
 PagesArgs pages_args(const moe_kv_cache &kv, int n, void *scratch) {
@@ -491,7 +355,7 @@ moe_status moe_attn_workspace(const moe_kv_cache *kv, const moe_attn_config *c, 
         const int hg = (c->q_heads / kv->kv_heads + 15) / 16;
         const size_t heads = (size_t)kv->kv_heads * hg;
         *workspace = sizeof(float) * 16 * (kv->head_dim + 2) * heads *
-                     ((size_t)decode_split(*kv, *c) + c->batch);
+                     ((size_t)decode_split(*kv, *c, c->longest) + c->batch);
         *counters = sizeof(uint32_t) * heads * c->batch;
     } else {
         const PromptPlan p = prompt_plan(*kv, *c, tokens, c->batch);
@@ -511,7 +375,7 @@ moe_status moe_attn_decode(const moe_kv_cache *kv, const moe_attn_config *c, int
     if (s != MOE_OK) return s;
     if (!workspace || !counters) return MOE_ERR_WORKSPACE;
     AttnArgs a = attn_args(*kv, *c, layer);
-    a.split = decode_split(*kv, *c);
+    a.split = decode_split(*kv, *c, c->longest);
     const int64_t grid = ((int64_t)a.split + batch) * a.kv_heads * a.head_groups;
     if (grid > kMaxGrid256) return MOE_ERR_UNSUPPORTED;
     int cus;

@@ -83,6 +83,18 @@ struct Fp16 {
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
 
+// Rows of queries that meet the keys of a shared prefix: a group's members, one after the
+// other, with the query heads of a kv head.  One workgroup (per kv head) takes 128 rows
+// from row0 on and part `part` of `parts` of the prefix, and writes slot `slot`.
+struct SharedUnit {
+    int32_t members, n_members, prefix, row0, part, parts, slot, pad;
+};
+// A sequence's own: the prefix (0: none), its group's first slot, the parts, and its
+// place among the members.
+struct SharedRow {
+    int32_t prefix, slot, parts, member;
+};
+
 // The arguments of both attention kernels.
 struct AttnArgs {
     const void *k, *v;         // the layer's [pages][kv_heads][page][head_dim]
@@ -101,6 +113,12 @@ struct AttnArgs {
     int32_t split;             // decode: units aimed at per kv head; prompt: most splits
     int32_t units;             // prompt: equal shares per kv head (0: row tiles)
     int32_t row_tiles;         // prompt: most of them that there are counters for
+    // Shared prefixes: what each workgroup (per kv head) takes, each sequence's part of
+    // it, the groups' members, and the partial results.
+    const SharedUnit *shared_units;
+    const SharedRow *shared_rows;
+    const int32_t *members;
+    float *shared_part;
 };
 
 // Blocks of 2^L keys that a row at the last position of n sees: the first
@@ -168,6 +186,30 @@ __device__ __forceinline__ uint32_t marks_of(uint32_t v, uint32_t sign) {
 // sign are among them (NaN counts as both).
 __device__ __forceinline__ float sum_of_marks(bool pos, bool neg) {
     return pos ? (neg ? __builtin_nanf("") : __builtin_inff()) : -__builtin_inff();
+}
+
+// Four values -> four e4m3 codes of x / scale, one rounding.  The division is the
+// IEEE one (a reciprocal could move a value over a rounding border); the clamp
+// keeps NaN.
+__device__ __forceinline__ uint32_t to_e4m3(f32x4 f, float scale) {
+    uint32_t nan = 0, sign = 0, w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[j] = f[j] / scale;
+        nan |= f[j] != f[j] ? 0xFFu << 8 * j : 0u;
+        sign |= __float_as_uint(f[j]) >> 31 << (8 * j + 7);
+        f[j] = fminf(fmaxf(f[j], -448.f), 448.f);
+    }
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+    return (w & ~nan) | (nan & (0x7F7F7F7Fu | sign));
+}
+// Eight values of 16 bits.
+template <class T>
+__device__ __forceinline__ u32x2 to_e4m3(u32x4 x, float scale) {
+    return (u32x2){
+        to_e4m3((f32x4){T::lo(x[0]), T::hi(x[0]), T::lo(x[1]), T::hi(x[1])}, scale),
+        to_e4m3((f32x4){T::lo(x[2]), T::hi(x[2]), T::lo(x[3]), T::hi(x[3])}, scale)};
 }
 
 // Joins the parts of a split row group.  Every part wrote `rows` rows of sums

@@ -1,5 +1,5 @@
 """Loading of ``libmoe_serve.so`` (the C ABI in include/moe_serve.h) and what
-the modules above it (``attention``, ``w4``) share: the argument structures,
+the modules above it (``attention``, ``rotary``, ``sampling``, ``w4``) share: the argument structures,
 dtype codes, checks of tensors and the status codes.
 
 Argument marshalling only, as in ``binding``: the operators run in the HIP
@@ -18,12 +18,15 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_serve.so")
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+LOGIT_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 3}
 STATUS = {-1: "invalid argument", -2: "unsupported shape or device", -3: "HIP error",
           -4: "workspace missing, too small or misaligned"}
 EXPORTED = ("moe_kv_validate", "moe_kv_append", "moe_kv_append_granted", "moe_kv_free",
             "moe_kv_scratch_size", "moe_kv_fork", "moe_kv_extend", "moe_kv_extend_granted",
             "moe_kv_compact", "moe_attn_validate", "moe_attn_workspace", "moe_attn_decode",
-            "moe_attn_prompt", "moe_w4_linear", "moe_serve_last_hip_error")
+            "moe_attn_prompt", "moe_w4_linear", "moe_serve_last_hip_error",
+            "moe_kv_append_rotated", "moe_attn_share", "moe_attn_shared_workspace",
+            "moe_attn_decode_shared", "moe_sample_workspace", "moe_sample")
 
 _lib = None
 
@@ -40,6 +43,28 @@ class AttnConfig(ctypes.Structure):
     """moe_attn_config"""
     _fields_ = [(n, ctypes.c_int32) for n in ("q_heads", "batch", "longest", "window", "sinks")] + \
                [("scale", ctypes.c_float)]
+
+
+class RotaryStruct(ctypes.Structure):
+    """moe_rotary"""
+    _fields_ = [("turns", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int32) for n in ("first", "rot", "interleaved")] + \
+               [("amplitude", ctypes.c_float)]
+
+
+class SharedPlan(ctypes.Structure):
+    """moe_attn_shared"""
+    _fields_ = [("data", ctypes.c_void_p), ("ints", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in
+                ("batch", "q_heads", "kv_heads", "head_dim", "units", "slots", "members", "window",
+                 "sinks", "tail")]
+
+
+class SamplingStruct(ctypes.Structure):
+    """moe_sampling"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("temperature", "top_p", "min_p", "top_k")] + \
+               [(n, ctypes.c_float) for n in ("temperature_all", "top_p_all", "min_p_all")] + \
+               [("top_k_all", ctypes.c_int32)]
 
 
 def lib() -> ctypes.CDLL:
@@ -69,6 +94,13 @@ def lib() -> ctypes.CDLL:
         "moe_attn_prompt": [vp, vp, i32, vp, i32, i64, i64, i32, vp, i32, vp, vp, vp, vp, vp],
         "moe_w4_linear": [vp, i64, i32, vp, vp, vp, i32, i32, i32, i32, vp, vp],
         "moe_serve_last_hip_error": [],
+        "moe_kv_append_rotated": [vp, i32, vp, vp, i64, i64, i32, vp, vp, i32, i64, i64, i32, vp,
+                                  i32, vp, vp, vp],
+        "moe_attn_share": [vp, vp, i32, i32, vp, vp, vp, vp, vp],
+        "moe_attn_shared_workspace": [vp, vp, vp] + sizes,
+        "moe_attn_decode_shared": [vp, vp, vp, i32, vp, i32, i64, i64, vp, vp, vp, vp, vp],
+        "moe_sample_workspace": [i32, i32] + sizes,
+        "moe_sample": [vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp],
     }
     for name in EXPORTED:
         f = getattr(L, name)

@@ -1,0 +1,490 @@
+"""Rotated append, decode over shared prefixes and sampling on the GPU against their
+definitions in 64 bits."""
+import math
+
+import pytest
+import torch
+
+import generate_util as gu
+import serve_util as su
+from sparse_moe_decode_router_amd import attention, rotary, sampling
+from sparse_moe_decode_router_amd.binding import MoEError
+
+pytestmark = pytest.mark.gpu
+
+BF, FP, F32, E4 = torch.bfloat16, torch.float16, torch.float32, su.E4M3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def randn(shape, dtype, seed, by=2.0):
+    return (by * torch.randn(shape, generator=torch.Generator().manual_seed(seed))).to(dtype)
+
+
+# ---- Rotated append --------------------------------------------------------
+
+# lengths, new (None: one each), q heads, kv heads, head_dim, page, dtype, cache, rot, first, pairs
+ROTARY = [
+    ([1], None, 1, 1, 64, 16, BF, BF, 64, 0, False),
+    ([33, 0, 16, 17, 100], None, 14, 2, 128, 16, BF, BF, 128, 0, False),
+    ([33, 0, 16, 17, 100], None, 14, 2, 128, 16, BF, E4, 128, 0, True),
+    ([70, 200], None, 3, 3, 96, 32, FP, FP, 48, 48, False),
+    ([70, 200], None, 3, 3, 96, 32, FP, E4, 32, 16, True),
+    ([40, 7, 0, 90], [40, 1, 0, 33], 8, 2, 192, 64, BF, BF, 64, 128, True),
+    ([40, 7, 0, 90], [40, 1, 0, 33], 4, 1, 256, 16, FP, FP, 256, 0, False),
+    ([130, 300], [130, 77], 5, 1, 64, 128, BF, E4, 16, 0, False),
+    ([9, 700], [9, 700], 2, 2, 128, 16, BF, BF, 96, 32, True),
+    ([5000, 4000], [5000, 4000], 1, 1, 64, 64, BF, BF, 64, 0, False),   # many tokens a workgroup
+    ([37], None, 70, 8, 256, 16, BF, BF, 128, 64, True),                # several workgroups a token
+]
+
+
+def rotary_case(case, seed=1):
+    lengths, new, qh, kvh, dim, page, dtype, cdtype, rot, first, pairs = case
+    cache = su.HostCache(lengths, kvh, page, dim, cdtype, seed=seed, clean=True)
+    new = new or [1] * len(lengths)
+    rows = randn((sum(new), qh + 2 * kvh, dim), dtype, seed + 1)
+    return cache, new, rows, rotary.frequencies(rot, 500000.0, factor=4.0, original=100)
+
+
+def check_append(cache, data, new, k, v, freq, first, pairs, amplitude, written=None):
+    """All of a cache's data after an append: the new positions, and the others as
+    they were."""
+    positions, at = [], []
+    for b, n in enumerate(new):
+        positions += [int(cache.lengths[b]) - n + i for i in range(n)]
+        at += [b] * n
+    turned, err = gu.rotate(k, positions, freq, first, pairs, amplitude)
+    want, tol = cache.data.double().clone(), torch.zeros(cache.data.shape, dtype=torch.float64)
+    touched = torch.zeros(cache.data.shape, dtype=torch.bool)
+    for t, (b, p) in enumerate(zip(at, positions)):
+        if p < 0 or (written is not None and not written[b]):
+            continue
+        page = int(cache.tables[b, p // cache.page])
+        want[0, 0, page, :, p % cache.page], want[0, 1, page, :, p % cache.page] = turned[t], v[t]
+        tol[0, 0, page, :, p % cache.page] = err[t]
+        touched[0, :, page, :, p % cache.page] = True
+    assert torch.equal(data.double()[~touched], cache.data.double()[~touched])
+    if cache.dtype == E4:
+        for which, scale in ((0, cache.k_scale), (1, cache.v_scale)):
+            hit = touched[0, which]
+            s = scale.double()[None, :, None, None].expand(hit.shape)[hit]
+            gu.check_codes(data[0, which][hit], want[0, which][hit], tol[0, which][hit], s)
+    else:
+        gu.check_rounded(data[touched], want[touched], tol[touched], cache.dtype)
+
+
+@pytest.mark.parametrize("case", ROTARY, ids=str)
+def test_append_rotated(case):
+    cache, new, rows, freq = rotary_case(case)
+    qh, kvh, first, pairs = case[2], case[3], case[9], case[10]
+    kv = cache.gpu()
+    cu = torch.tensor([0] + new).cumsum(0).to(torch.int32).cuda() if case[1] else None
+    turn = rotary.Rotary(freq, first, pairs, amplitude=1.25)
+    x = rows.cuda()
+    q, k, v = x[:, :qh], x[:, qh:qh + kvh], x[:, qh + kvh:]
+    got = kv.append_rotated(0, q, k, v, turn, cu)
+    torch.cuda.synchronize()
+    positions = [int(cache.lengths[b]) - n + i for b, n in enumerate(new) for i in range(n)]
+    want, err = gu.rotate(rows[:, :qh], positions, freq, first, pairs, 1.25)
+    gu.check_rounded(got.cpu(), want, err, rows.dtype)
+    check_append(cache, kv.data.cpu(), new, rows[:, qh:qh + kvh], rows[:, qh + kvh:], freq, first,
+                 pairs, 1.25)
+    # in place, and into a tensor whose other rows stay
+    own = q.contiguous()
+    assert kv.append_rotated(0, own, k, v, turn, cu, out=own) is own
+    assert torch.equal(own, got)
+
+
+def test_far_positions_keep_their_angle():
+    """A position near 2^31 / 16 turned by 32 bits would be off by many turns."""
+    page, cols = 1024, 1 << 17
+    n = cols * page - 1
+    kv = attention.PagedKV.empty(1, 2, 1, page, 64, 1, cols)
+    kv.tables[0, (n - 1) // page] = 1
+    kv.lengths.fill_(n)
+    freq = rotary.frequencies(64)
+    x = randn((1, 3, 64), BF, 5)
+    q = kv.append_rotated(0, x.cuda()[:, :1], x.cuda()[:, 1:2], x.cuda()[:, 2:], rotary.Rotary(freq))
+    want, err = gu.rotate(x[:, :2], [n - 1], freq, 0, False, 1.0)
+    # (the reference's own product is right to 2^-53 of 1.3e8 radians)
+    err += 1e-7
+    gu.check_rounded(q.cpu()[:, 0], want[:, 0], err[:, 0], BF)
+    gu.check_rounded(kv.data[0, 0, 1, :, (n - 1) % page].cpu(), want[0, 1:], err[0, 1:], BF)
+
+
+def test_rows_outside_of_cu_and_sequences_without_room_stay():
+    cache = su.HostCache([20, 30, 5], 1, 16, 64, BF, seed=7, clean=True)
+    kv = cache.gpu()
+    freq = rotary.frequencies(64)
+    x = randn((9, 4, 64), BF, 8)
+    xd = x.cuda()
+    out = torch.full((9, 2, 64), 7.0, dtype=BF, device="cuda")
+    cu = ints(2, 4, 4, 7)      # rows 0, 1, 7 and 8 belong to nobody
+    kv.granted.copy_(ints(1, 0, 3))   # the first sequence got one position for its two tokens
+    kv.append_rotated(0, xd[:, :2], xd[:, 2:3], xd[:, 3:], rotary.Rotary(freq), cu,
+                      only_granted=True, out=out)
+    got = out.cpu()
+    assert torch.all(got[[0, 1, 7, 8]] == 7)
+    want, err = gu.rotate(x[2:7, :2], [18, 19, 2, 3, 4], freq, 0, False, 1.0)
+    gu.check_rounded(got[2:7], want, err, BF)
+    check_append(cache, kv.data.cpu(), [2, 0, 3], x[2:7, 2:3], x[2:7, 3:], freq, 0, False, 1.0,
+                 written=[False, True, True])
+
+
+@pytest.mark.parametrize("lengths,table", [
+    ([33], [[0, 1, 9]]), ([33], [[0, 1, -1]]), ([49], [[0, 1, 2]]), ([-5], [[0, 1, 2]]),
+    ([2 ** 31 - 1], [[0, 1, 2]])])
+def test_positions_without_a_page_are_not_written(lengths, table):
+    kv = attention.PagedKV.empty(1, 4, 1, 16, 64, 1, 3)
+    kv.tables.copy_(torch.tensor(table))
+    kv.lengths.copy_(torch.tensor(lengths))
+    x = randn((1, 3, 64), BF, 9).cuda()
+    q = kv.append_rotated(0, x[:, :1], x[:, 1:2], x[:, 2:], rotary.Rotary(rotary.frequencies(64)))
+    torch.cuda.synchronize()
+    assert torch.all(kv.data == 0) and q.isfinite().all()
+    if lengths[0] < 0:
+        assert torch.equal(q, x[:, :1])
+
+
+def test_rotated_keys_that_are_not_finite():
+    kv = attention.PagedKV.empty(1, 2, 1, 16, 64, 1, 1, dtype=E4, k_scale=ints(1).float(),
+                                 v_scale=ints(1).float())
+    kv.tables.fill_(0)
+    kv.lengths.fill_(3)
+    x = randn((1, 3, 64), BF, 10)
+    x[0, 1, 0], x[0, 1, 5], x[0, 2, 1], x[0, 2, 2] = math.nan, 3e38, -math.inf, math.nan
+    xd = x.cuda()
+    kv.append_rotated(0, xd[:, :1], xd[:, 1:2], xd[:, 2:], rotary.Rotary(rotary.frequencies(32)))
+    k, v = (kv.data[0, i, 0, 0, 2].cpu().double() for i in (0, 1))
+    assert k[0].isnan() and k[16].isnan() and int(k.isnan().sum()) == 2
+    assert abs(k[5]) == 448 and v[1] == -448 and v[2].isnan() and int(v.isnan().sum()) == 1
+
+
+# ---- Decode over shared prefixes -------------------------------------------
+
+# groups, prefix, lengths, kv heads, heads per kv head, head_dim, page, dtype, cache, window, sinks
+SHARED = [
+    ([[0, 1]], [16], [17, 20], 1, 1, 64, 16, BF, BF, 0, 0),
+    ([[2, 0, 1]], [64], [70, 65, 100], 2, 7, 128, 16, BF, BF, 0, 0),
+    ([[0, 1], [3, 4, 2]], [50, 333], [90, 51, 340, 400, 334], 2, 3, 96, 32, FP, FP, 0, 0),
+    ([[0, 1], [3, 4, 2]], [50, 333], [90, 51, 340, 400, 334], 1, 5, 192, 16, BF, E4, 0, 0),
+    ([[0, 1]], [100], [100, 131], 2, 4, 256, 64, FP, FP, 0, 0),         # one without a tail
+    ([[0, 1]], [100], [100, 131], 1, 2, 256, 16, BF, E4, 0, 0),
+    ([[0, 1, 2]], [128], [0, 130, 50], 2, 2, 64, 128, BF, BF, 0, 0),    # freed, and shorter
+    ([[0, 1, 2]], [128], [0, 0, 0], 1, 2, 64, 16, BF, BF, 0, 0),
+    ([], [], [20, 33], 1, 3, 128, 16, BF, BF, 0, 0),
+    ([[1], [0]], [20, 16], [20, 33], 1, 3, 128, 16, BF, BF, 0, 0),      # alone
+    ([[0, 1], [2]], [0, 30], [20, 33, 31], 1, 3, 128, 16, BF, BF, 0, 0),
+    ([[0, 2]], [48], [60, 200, 49, 7], 1, 3, 128, 16, BF, BF, 0, 0),    # some in no group
+    ([list(range(30))], [200], [201 + i for i in range(30)], 1, 9, 64, 16, BF, BF, 0, 0),
+    ([list(range(70))], [64], [65 + i % 5 for i in range(70)], 1, 2, 64, 16, FP, FP, 0, 0),
+    ([[0, 1, 2]], [3000], [3001, 3100, 3777], 1, 7, 128, 16, BF, BF, 0, 0),      # many parts
+    ([[0, 1]], [5000], [5001, 5100], 2, 20, 128, 64, FP, E4, 0, 0),
+    ([[0, 1, 2]], [400], [401, 700, 450], 1, 3, 128, 16, BF, BF, 100, 4),        # windows
+    ([[0, 1, 2]], [400], [401, 420, 450], 2, 2, 64, 32, FP, FP, 64, 0),
+    ([[0, 1, 2]], [400], [401, 420, 450], 1, 2, 64, 32, BF, E4, 300, 16),
+    ([[0, 1]], [32], [60, 70], 1, 2, 64, 16, BF, BF, 8, 50),    # sinks behind the prefix
+    ([[0, 1]], [32], [40, 35], 1, 2, 64, 16, BF, BF, 500, 32),
+]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=str)
+def test_decode_shared(case):
+    groups, prefix, lengths, kvh, group, dim, page, dtype, cdtype, window, sinks = case
+    cache = gu.shared_cache(groups, prefix, lengths, kvh, page, dim, cdtype, seed=11)
+    b = len(lengths)
+    q = randn((b, kvh * group, dim), dtype, 12)
+    att = attention.PagedAttention(cache.gpu(), kvh * group, b, max(max(lengths), 1), window=window,
+                                   sinks=sinks)
+    plan = att.share(groups, prefix)
+    dense = su.attention_dense if max(lengths) > 400 else su.attention
+    want = dense(cache, 0, q, list(range(b + 1)), window, sinks)
+    qd = q.cuda()
+    for _ in range(2):  # the second call finds the counters as the first left them
+        got = att.decode_shared(0, qd, plan)
+        torch.cuda.synchronize()
+        su.check_attention(got, want, dtype, True)
+
+
+def test_members_grow_and_are_freed_under_one_plan():
+    """One plan through decoding, a freed first member, and pages moved together."""
+    cache = gu.shared_cache([[0, 1, 2]], [160], [170, 161, 200], 2, 16, 64, BF, seed=13, spare=12,
+                            spare_cols=6)
+    kv = cache.gpu()
+    att = attention.PagedAttention(kv, 6, 3, 300)
+    plan = att.share([[0, 1, 2]], [160])
+    q = randn((3, 6, 64), BF, 14).cuda()
+
+    def same():
+        got, want = att.decode_shared(0, q, plan), att.decode(0, q)
+        torch.cuda.synchronize()
+        assert not got[0].isnan().any()
+        # both are off by their rounding, and weights of the prefix by as much again
+        assert (got[0].float() - want[0].float()).abs().max() <= 4 * 2.0 ** -8 * \
+            kv.data.float().nan_to_num(0, 0, 0).abs().max()
+        assert torch.allclose(got[1], want[1], atol=1e-5, rtol=1e-6)
+        return got
+
+    same()
+    kv.extend(ints(3, 20, 1))
+    k = randn((24, 4, 64), BF, 15).cuda()
+    kv.append(0, k[:, :2], k[:, 2:], ints(0, 3, 23, 24))
+    same()
+    kv.free(ints(0))
+    got = same()
+    assert torch.all(got[0][0] == 0) and torch.all(got[1][0] == -math.inf)
+    kv.compact()
+    same()
+
+
+def test_visible_infinities_of_a_prefix():
+    cache = gu.shared_cache([[0, 1]], [96], [100, 130], 1, 16, 64, BF, seed=16)
+    page = int(cache.tables[0, 1])
+    cache.data[0, 1, page, 0, 3, 5], cache.data[0, 1, page, 0, 4, 7] = math.inf, -math.inf
+    cache.data[0, 1, page, 0, 5, 9], cache.data[0, 1, page, 0, 6, 9] = math.inf, -math.inf
+    att = attention.PagedAttention(cache.gpu(), 2, 2, 130)
+    q = randn((2, 2, 64), BF, 17).cuda()
+    out = att.decode_shared(0, q, att.share([[0, 1]], [96]))[0].cpu()
+    assert torch.all(out[..., 5] == math.inf) and torch.all(out[..., 7] == -math.inf)
+    assert out[..., 9].isnan().all()
+    out[..., [5, 7, 9]] = 0
+    assert out.isfinite().all()
+
+
+def test_shared_streams_and_graph():
+    """Two streams at once, and a captured call that follows the lengths."""
+    cache = gu.shared_cache([[0, 1, 2]], [2000], [2010, 2001, 2100], 2, 16, 128, BF, seed=18,
+                            spare=20, spare_cols=4)
+    kv = cache.gpu()
+    att = attention.PagedAttention(kv, 14, 3, 2200)
+    plan = att.share([[0, 1, 2]], [2000])
+    qs = [randn((3, 14, 128), BF, 19 + i).cuda() for i in range(2)]
+    want = [att.decode_shared(0, q, plan) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(5):
+        got = []
+        for s, q in zip(streams, qs):
+            with torch.cuda.stream(s):
+                got.append(att.decode_shared(0, q, plan))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = att.decode_shared(0, qs[0], plan)
+    for i in range(4):
+        if i:
+            kv.extend(ints(1, 17, 0))
+            k = randn((3, 4, 128), BF, 30 + i).cuda()
+            kv.append(0, k[:, :2], k[:, 2:])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), lse.clone()
+        eager = att.decode_shared(0, qs[0], plan)
+        torch.cuda.synchronize()
+        # (Of 17 new positions one is written: what is there else may be NaN, for both.)
+        for x, y in zip(got, eager):
+            assert torch.allclose(x, y, rtol=0, atol=0, equal_nan=True)
+
+
+# ---- Sampling --------------------------------------------------------------
+
+def logits(rows, vocab, dtype, seed, sharp=3.0, masked=0.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((rows, vocab), generator=g) * (sharp * (0.5 + torch.rand((rows, 1), generator=g)))
+    if masked:
+        x.masked_fill_(torch.rand((rows, vocab), generator=g) < masked, -math.inf)
+        x[:, vocab // 3] = 0.0
+    return x.to(dtype), torch.rand(rows, generator=g)
+
+
+def draw(x, u, **filters):
+    sampler = sampling.Sampler(*x.shape)
+    on = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in filters.items()}
+    xd, ud = x.cuda(), u.cuda()
+    for _ in range(2):  # the second call finds the counters as the first left them
+        got = sampler(xd, ud, **on)
+        torch.cuda.synchronize()
+        gu.check_sample(got, x, u, **filters)
+
+
+FILTERS = [
+    {}, dict(temperature=0.6), dict(temperature=0), dict(top_k=1), dict(top_k=20),
+    dict(top_p=0.9), dict(min_p=0.05), dict(temperature=1.5, top_k=300, top_p=0.7),
+    dict(top_k=50, top_p=0.95, min_p=0.02), dict(temperature=0.8, top_p=0.999),
+    dict(top_p=0.0), dict(min_p=1.0), dict(top_k=10 ** 9, top_p=1.0, min_p=0.0),
+    dict(temperature=3.0, top_p=0.99, min_p=1e-3), dict(temperature=0.01, top_p=0.5),
+]
+
+
+@pytest.mark.parametrize("filters", FILTERS, ids=str)
+@pytest.mark.parametrize("rows,vocab,dtype", [(3, 1000, F32), (5, 32003, BF), (2, 100001, FP)],
+                         ids=str)
+def test_sample(rows, vocab, dtype, filters):
+    x, u = logits(rows, vocab, dtype, 40)
+    draw(x, u, **filters)
+
+
+@pytest.mark.parametrize("rows,vocab,dtype,masked", [
+    (1, 163840, BF, 0.0), (64, 163840, F32, 0.0), (300, 20011, FP, 0.4), (40, 50021, BF, 0.99),
+    (2, 1 << 19, F32, 0.0), (1, 1 << 19, BF, 0.5), (9, 2, F32, 0.0), (7, 17, BF, 0.9)], ids=str)
+def test_sample_with_filters_of_each_row(rows, vocab, dtype, masked):
+    x, u = logits(rows, vocab, dtype, 41, masked=masked)
+    g = torch.Generator().manual_seed(42)
+    draw(x, u, temperature=0.3 + torch.rand(rows, generator=g) * (torch.arange(rows) % 5 > 0),
+         top_k=torch.randint(0, 100, (rows,), generator=g, dtype=torch.int32) *
+         (torch.arange(rows) % 3 > 0).int(),
+         top_p=1 - 0.5 * torch.rand(rows, generator=g) * (torch.arange(rows) % 4 > 0),
+         min_p=0.1 * torch.rand(rows, generator=g) * (torch.arange(rows) % 2 > 0))
+
+
+@pytest.mark.parametrize("filters", [{}, dict(top_k=7), dict(top_p=0.5), dict(top_k=6000, top_p=0.5),
+                                     dict(top_k=9000), dict(min_p=0.5), dict(temperature=0)], ids=str)
+@pytest.mark.parametrize("vocab", [1, 5, 10007, 120000])
+def test_sample_of_equal_logits(vocab, filters):
+    """All of one value, and all of two: whatever list of candidates there is does
+    not hold them."""
+    x = torch.zeros((3, vocab), dtype=BF)
+    x[1, ::2] = 1.0
+    x[2] = -5.0
+    draw(x, torch.tensor([0.0, 0.4999, 0.99999]), **filters)
+
+
+@pytest.mark.parametrize("filters", [{}, dict(top_p=0.9), dict(top_k=5000, top_p=0.9, min_p=1e-3),
+                                     dict(top_k=30000)], ids=str)
+def test_sample_with_many_at_the_border(filters):
+    """Logits of few values, so that thousands are equal at every border."""
+    g = torch.Generator().manual_seed(43)
+    x = torch.randint(-6, 3, (4, 90000), generator=g).to(FP) / 2
+    draw(x, torch.rand(4, generator=g), **filters)
+
+
+@pytest.mark.parametrize("filters", [{}, dict(top_k=3), dict(top_p=0.8), dict(temperature=0),
+                                     dict(top_k=2, top_p=0.3, min_p=0.5)], ids=str)
+def test_sample_of_logits_that_are_not_finite(filters):
+    x, u = logits(9, 5000, F32, 44)
+    x[0] = -math.inf
+    x[1] = math.nan
+    x[2, ::2] = math.nan
+    x[3, 77] = math.inf
+    x[4, [5, 1234, 4999]] = math.inf
+    x[5], x[5, 4999] = -math.inf, -3e38
+    x[6], x[6, :2] = -3.4e38, 3.4e38
+    x[7] = x[7] * 1e-40
+    x[8] = x[8] * 1e5
+    draw(x, u, **filters)
+
+
+def test_sample_of_numbers_at_the_ends():
+    x, _ = logits(6, 3001, F32, 45)
+    u = torch.tensor([0.0, 1.0, 1 - 2.0 ** -24, -1.0, math.nan, 7.0])
+    draw(x, u)
+    draw(x, u, top_p=0.9)
+    draw(x, u, top_k=40)
+    t = torch.tensor([0.0, -1.0, math.nan, 1e-30, 1e30, 1e-35])
+    draw(x, torch.rand(6, generator=torch.Generator().manual_seed(1)), temperature=t)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=str)
+def test_sample_of_rows_at_any_alignment(dtype):
+    x, u = logits(6, 4099, dtype, 46)
+    wide = torch.full((6, 4207), 50.0, dtype=dtype, device="cuda")   # what is beside would win
+    for at in range(9):
+        part = wide[:, at:at + 4099]
+        part.copy_(x)
+        got = sampling.Sampler(6, 4099)(part, u.cuda(), top_p=0.9)
+        torch.cuda.synchronize()
+        gu.check_sample(got, x, u, top_p=0.9)
+        wide.fill_(50.0)
+
+
+def test_sample_follows_its_probabilities():
+    """Even numbers u give each token its share of them, to one of them."""
+    x, _ = logits(1, 301, F32, 47, sharp=1.0)
+    n = 4096
+    u = (torch.arange(n) + 0.5) / n
+    tokens, drawn = sampling.Sampler(n, 301)(x.cuda().expand(n, 301).contiguous(), u.cuda())
+    share = torch.bincount(tokens.cpu().long(), minlength=301).double() / n
+    p = torch.softmax(x[0].double(), 0)
+    assert float((share - p).abs().max()) <= 1.0001 / n
+    assert torch.all(tokens[1:] >= tokens[:-1])
+    assert torch.allclose(drawn.cpu().double(), p.log()[tokens.cpu().long()], rtol=1e-6, atol=1e-9)
+
+
+def test_sample_streams_and_graph():
+    x, u = logits(5, 40000, F32, 48)
+    sampler = sampling.Sampler(8, 40000)
+    xs = [x.cuda(), x.flip(0).contiguous().cuda()]
+    ud = u.cuda()
+    want = [sampler(y, ud, top_p=0.9) for y in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        got = []
+        for s, y in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(sampler(y, ud, top_p=0.9))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = sampler(xs[0], ud, top_p=0.9)
+    for i in range(4):
+        y, v = logits(5, 40000, F32, 50 + i)
+        xs[0].copy_(y)
+        ud.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        eager = sampler(xs[0], ud, top_p=0.9)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], eager[0]) and torch.equal(got[1], eager[1])
+        gu.check_sample(got, y, v, top_p=0.9)
+
+
+def test_refusals_on_the_gpu():
+    kv = su.HostCache([20, 30], 2, 16, 64, BF, seed=23).gpu()
+    att = attention.PagedAttention(kv, 4, 2, 64)
+    plan, other = att.share([[0, 1]], [16]), attention.PagedAttention(kv, 4, 2, 64)
+    turn = rotary.Rotary(rotary.frequencies(64))
+    q = torch.zeros((2, 4, 64), dtype=BF, device="cuda")
+    k = q[:, :2]
+    x, u = torch.zeros((2, 100), device="cuda"), torch.zeros(2, device="cuda")
+    s = sampling.Sampler(2, 100)
+    for bad in (lambda: att.decode_shared(1, q, plan), lambda: att.decode_shared(0, q[:1], plan),
+                lambda: att.decode_shared(0, q.half(), plan), lambda: other.decode_shared(0, q, plan),
+                lambda: att.decode_shared(0, q, None), lambda: att.share([[0, 2]], [16]),
+                lambda: att.share([[0, 1], [1]], [16, 16]), lambda: att.share([[0, 1]], []),
+                lambda: att.share([[0, 1]], [-1]), lambda: att.share([[0]], [1], batch=3),
+                lambda: att.share([[0, 1]], [16.0]),
+                lambda: kv.append_rotated(0, q, k, k.half(), turn),
+                lambda: kv.append_rotated(0, q[:1], k, k, turn),
+                lambda: kv.append_rotated(0, q.half(), k, k, turn),
+                lambda: kv.append_rotated(1, q, k, k, turn),
+                lambda: kv.append_rotated(0, q, k, k, turn, ints(0, 1, 1, 2)),
+                lambda: kv.append_rotated(0, q, k, k, turn, out=q[:, :2]),
+                lambda: kv.append_rotated(0, q, k, k, rotary.Rotary(rotary.frequencies(64), 16)),
+                lambda: kv.append_rotated(0, q, k, k, rotary.Rotary(rotary.frequencies(64),
+                                                                    device="cpu")),
+                lambda: s(x[:, :99], u), lambda: s(x.double(), u), lambda: s(x.t(), u),
+                lambda: s(x.cpu(), u), lambda: s(x, u.double()), lambda: s(x, u[:1]),
+                lambda: s(torch.cat([x, x]), torch.cat([u, u])),
+                lambda: s(x[:1].expand(2, 100), u), lambda: s(x, u, temperature=-1.0),
+                lambda: s(x, u, temperature=u[:1]), lambda: s(x, u, top_k=u), lambda: s(x, u, top_k=1.5),
+                lambda: s(x, u, top_p=math.nan), lambda: sampling.Sampler(1, (1 << 19) + 1),
+                lambda: sampling.Sampler(0, 10)):
+        with pytest.raises(MoEError):
+            bad()
+    torch.cuda.synchronize()
