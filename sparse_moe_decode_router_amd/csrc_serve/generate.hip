@@ -10,42 +10,46 @@ using namespace moe::serve;
 namespace {
 
 constexpr int kMaxVocab = 1 << 19;     // counts of 20 bits, weights of 44 in one integer
-// Workgroups that one sampling call aims at.
-constexpr int kSampleGrid = 1024;
+// Workgroups that a sampling call aims at.
+constexpr int kSampleGrid = 512;
 
-int logits_per_chunk(int dtype) { return dtype == MOE_F32 ? 4 : 8; }
+constexpr int logits_per_chunk(int dtype) { return dtype == MOE_F32 ? 4 : 8; }
 // 16-byte chunks of a row, wherever it begins.
-int row_chunks(int vocab, int dtype) {
+constexpr int row_chunks(int vocab, int dtype) {
     const int per = logits_per_chunk(dtype);
     return (vocab + per - 1) / per + 1;
 }
-// The fewest slices whose workgroups hold theirs in registers.
-int least_slices(int vocab, int dtype) {
+// The fewest slices whose lanes have at most kSampleChunks chunks.
+constexpr int least_slices(int vocab, int dtype) {
     const int most = kSampleWaves * 64 * kSampleChunks;
     return (row_chunks(vocab, dtype) + most - 1) / most;
 }
-int sample_slices(int rows, int vocab, int dtype) {
+static_assert(least_slices(kMaxVocab, MOE_F32) <= kSampleMaxSlices, "slices of the largest row");
+// Slices of a row, at most `most`.
+int sample_slices(int rows, int vocab, int dtype, int most) {
     // No wave has less than one chunk a lane.
     const int useful = (row_chunks(vocab, dtype) + kSampleThreads - 1) / kSampleThreads;
     const int aimed = (kSampleGrid + rows - 1) / rows;
-    return std::max(least_slices(vocab, dtype), std::min({kSampleMaxSlices, useful, aimed}));
+    return std::max(least_slices(vocab, dtype), std::min({most, useful, aimed}));
 }
 // Slices of all rows that no call of up to `rows` rows goes beyond, whatever its type.
-int64_t most_slices(int rows, int vocab) {
+int64_t most_slices(int rows, int vocab, int most) {
     return std::max<int64_t>((int64_t)rows * least_slices(vocab, MOE_F32),
-                             std::min<int64_t>((int64_t)rows * kSampleMaxSlices,
-                                               (int64_t)kSampleGrid + rows));
+                             std::min<int64_t>((int64_t)rows * most, (int64_t)kSampleGrid + rows));
 }
 struct SampleSpace {
-    size_t hist, sums, list, slices, all;
+    size_t hist, sums, keys, list, slices, borders, listed, all;
 };
-SampleSpace sample_space(int64_t slices, int rows) {
+SampleSpace sample_space(int64_t slices, int64_t draws, int rows) {
     SampleSpace s;
     s.hist = 0;
     s.sums = s.hist + sizeof(uint64_t) * kSampleBins * slices;
-    s.list = s.sums + sizeof(double) * kSampleWaves * kSampleSlots * slices;
-    s.slices = s.list + sizeof(uint64_t) * kSampleList * rows;
-    s.all = s.slices + sizeof(SampleSlice) * slices;
+    s.keys = s.sums + sizeof(double) * kSampleWaves * kSampleSlots * draws;
+    s.list = s.keys + sizeof(uint64_t) * kSampleWaves * draws;
+    s.slices = s.list + sizeof(uint64_t) * kSampleList * draws;
+    s.borders = s.slices + sizeof(SampleSlice) * slices;
+    s.listed = s.borders + sizeof(SampleBorder) * rows;
+    s.all = s.listed + sizeof(int32_t) * draws;
     return s;
 }
 
@@ -130,9 +134,10 @@ moe_status moe_kv_append_rotated(const moe_kv_cache *kv, int32_t layer, const mo
 
 moe_status moe_sample_workspace(int32_t rows, int32_t vocab, size_t *workspace, size_t *counters) {
     if (rows < 1 || vocab < 1 || !workspace || !counters) return MOE_ERR_INVALID_ARG;
-    if (rows > kMaxRows / kSampleMaxSlices || vocab > kMaxVocab) return MOE_ERR_UNSUPPORTED;
-    *workspace = sample_space(most_slices(rows, vocab), rows).all;
-    *counters = 2 * sizeof(uint32_t) * (size_t)rows;
+    if (rows > kMaxRows / kSampleMaxDraws || vocab > kMaxVocab) return MOE_ERR_UNSUPPORTED;
+    *workspace = sample_space(most_slices(rows, vocab, kSampleMaxSlices),
+                              most_slices(rows, vocab, kSampleMaxDraws), rows).all;
+    *counters = sizeof(uint32_t) * (size_t)rows;
     return MOE_OK;
 }
 
@@ -142,7 +147,7 @@ moe_status moe_sample(const void *x, int32_t dtype, int64_t row_stride, int32_t 
     if ((dtype != MOE_BF16 && dtype != MOE_FP16 && dtype != MOE_F32) || rows < 0 || vocab < 1 ||
         !filters || (rows > 1 && row_stride < vocab))
         return MOE_ERR_INVALID_ARG;
-    if (rows > kMaxRows / kSampleMaxSlices || vocab > kMaxVocab || row_stride > 1ll << 40)
+    if (rows > kMaxRows / kSampleMaxDraws || vocab > kMaxVocab || row_stride > 1ll << 40)
         return MOE_ERR_UNSUPPORTED;
     if (rows == 0) return MOE_OK;
     if (!x || !u || !token || !logprob || !aligned(x, dtype == MOE_F32 ? 4 : 2) || !aligned(u, 4) ||
@@ -155,8 +160,10 @@ moe_status moe_sample(const void *x, int32_t dtype, int64_t row_stride, int32_t 
     moe_status s = compute_units(&cus);
     if (s != MOE_OK) return s;
     SampleArgs a = {};
-    a.slices_n = sample_slices(rows, vocab, dtype);
-    const SampleSpace space = sample_space((int64_t)a.slices_n * rows, rows);
+    a.slices_n = sample_slices(rows, vocab, dtype, kSampleMaxSlices);
+    a.draws = sample_slices(rows, vocab, dtype, kSampleMaxDraws);
+    const SampleSpace space =
+        sample_space((int64_t)a.slices_n * rows, (int64_t)a.draws * rows, rows);
     char *ws = (char *)workspace;
     a.x = x;
     a.u = u;
@@ -172,25 +179,38 @@ moe_status moe_sample(const void *x, int32_t dtype, int64_t row_stride, int32_t 
     a.logprob = logprob;
     a.hist = (uint64_t *)(ws + space.hist);
     a.sums = (double *)(ws + space.sums);
+    a.keys = (uint64_t *)(ws + space.keys);
     a.list = (uint64_t *)(ws + space.list);
+    a.borders = (SampleBorder *)(ws + space.borders);
     a.slices = (SampleSlice *)(ws + space.slices);
+    a.listed = (int32_t *)(ws + space.listed);
     a.counters = counters;
     a.stride = rows > 1 ? row_stride : 0;
     a.rows = rows;
     a.vocab = vocab;
-    const int segments = a.slices_n * kSampleWaves;
-    a.chunks = (row_chunks(vocab, dtype) + segments - 1) / segments;
-    const int grid = rows * a.slices_n;
-    auto go = [&](auto scan, auto draw) {
-        scan<<<grid, kSampleThreads, 0, stream>>>(a);
+    auto per_wave = [&](int slices) {
+        return (row_chunks(vocab, dtype) + slices * kSampleWaves - 1) / (slices * kSampleWaves);
+    };
+    a.chunks = per_wave(a.slices_n);
+    a.draw_chunks = per_wave(a.draws);
+    const int grid = rows * a.draws;
+    // Filters for all rows are known here; those by row are not.
+    const bool plain = !a.top_k && !a.top_p && !a.min_p && !(a.top_k_all > 0 && a.top_k_all < vocab) &&
+                       !(a.top_p_all < 1.f) && !(a.min_p_all > 0.f);
+    auto go = [&](auto plainly, auto scan, auto draw) {
+        if (plain) {
+            plainly<<<grid, kSampleThreads, 0, stream>>>(a);
+            return launched();
+        }
+        scan<<<rows * a.slices_n, kSampleThreads, 0, stream>>>(a);
         const moe_status r = launched();
         if (r != MOE_OK) return r;
         draw<<<grid, kSampleThreads, 0, stream>>>(a);
         return launched();
     };
-    if (dtype == MOE_F32) return go(k_sample_scan<kSampleF32>, k_sample_draw<kSampleF32>);
-    if (dtype == MOE_FP16) return go(k_sample_scan<1>, k_sample_draw<1>);
-    return go(k_sample_scan<0>, k_sample_draw<0>);
+    if (dtype == MOE_F32) return go(k_sample_plain<kSampleF32>, k_sample_scan<kSampleF32>, k_sample_draw<kSampleF32>);
+    if (dtype == MOE_FP16) return go(k_sample_plain<1>, k_sample_scan<1>, k_sample_draw<1>);
+    return go(k_sample_plain<0>, k_sample_scan<0>, k_sample_draw<0>);
 }
 
 }  // extern "C"
