@@ -10,7 +10,10 @@ using namespace moe::serve;
 namespace {
 
 constexpr int kMaxVocab = 1 << 19;     // counts of 20 bits, weights of 44 in one integer
-// Workgroups that a sampling call aims at.
+// Workgroups that a sampling call's launches aim at: two for each compute unit.  Every
+// one has a chain of latencies of its own (64 rows of 163840 in f32, 512 rows of 100003 in
+// bf16, us: 512 for both launches 66 and 152, 1024 for the second 79 and 160, for both
+// 76 and 182, 512 and 2048 100 and 187).
 constexpr int kSampleGrid = 512;
 
 constexpr int logits_per_chunk(int dtype) { return dtype == MOE_F32 ? 4 : 8; }
@@ -38,14 +41,13 @@ int64_t most_slices(int rows, int vocab, int most) {
                              std::min<int64_t>((int64_t)rows * most, (int64_t)kSampleGrid + rows));
 }
 struct SampleSpace {
-    size_t hist, sums, keys, list, slices, borders, listed, all;
+    size_t hist, sums, list, slices, borders, listed, all;
 };
 SampleSpace sample_space(int64_t slices, int64_t draws, int rows) {
     SampleSpace s;
     s.hist = 0;
     s.sums = s.hist + sizeof(uint64_t) * kSampleBins * slices;
-    s.keys = s.sums + sizeof(double) * kSampleWaves * kSampleSlots * draws;
-    s.list = s.keys + sizeof(uint64_t) * kSampleWaves * draws;
+    s.list = s.sums + sizeof(double) * kSampleWaves * kSampleSlots * draws;
     s.slices = s.list + sizeof(uint64_t) * kSampleList * draws;
     s.borders = s.slices + sizeof(SampleSlice) * slices;
     s.listed = s.borders + sizeof(SampleBorder) * rows;
@@ -179,7 +181,6 @@ moe_status moe_sample(const void *x, int32_t dtype, int64_t row_stride, int32_t 
     a.logprob = logprob;
     a.hist = (uint64_t *)(ws + space.hist);
     a.sums = (double *)(ws + space.sums);
-    a.keys = (uint64_t *)(ws + space.keys);
     a.list = (uint64_t *)(ws + space.list);
     a.borders = (SampleBorder *)(ws + space.borders);
     a.slices = (SampleSlice *)(ws + space.slices);

@@ -14,14 +14,14 @@
 //                   20 bits, both in one 64-bit integer addition.  The last slice of
 //                   a row finds the few bins in which the filters' borders are.
 //   k_sample_draw   every slice sums, in 64 bits, the weights above those bins, and lists
-//                   the values in them.  The last slice of a row to finish sorts
-//                   that list, finds the border, the segment (a wave's share of a
-//                   slice) that holds the token, and the token.
+//                   the values in them.  The last slice of a row to finish narrows
+//                   the list down, by histograms of 11 bits of (value, index) a pass,
+//                   to the last token that is kept; finds the segment (a wave's share
+//                   of a slice) that holds the drawn one; and that.
 // Bins are monotonic in the value and their counts exact, so that the list holds the
 // border whatever the weights' 20 bits missed (the margin of the search covers
 // that).  Where the list would be too long (thousands of equal logits at the border),
-// the last workgroup narrows the bins down by histograms of the values' bits instead,
-// 11 bits a pass over the row.
+// the passes go over the row instead.
 //   k_sample_plain  rows without filters: each segment's maximum and sum, and the last
 //                   slice draws.  One launch.
 #pragma once
@@ -40,14 +40,15 @@ constexpr int kSampleSegments = kSampleMaxDraws * kSampleWaves;
 constexpr int kSampleBins = 4096;       // the last one takes all that is below
 constexpr float kSamplePerOctave = 64.f;
 constexpr int kSampleList = 4096;       // values at the border of a row
-constexpr int kSampleKeyBins = 2048;    // of the values' bits
+constexpr int kSampleKeyBins = 2048;    // of a pass over the list
+constexpr int kSampleIndexBits = 19;
 constexpr int kSampleSlots = 3;         // sums of a segment: above, above and kept, all
 
 struct SampleSlice {
     float max;         // -inf: nothing to draw
     int32_t first;     // index of the first value that is the maximum
     int32_t bin;       // of the maximum
-    int32_t count;     // finite values, and +inf
+    int32_t pad;
 };
 
 // What the slices of a row agree on: values from `top` on are kept by the filters, those
@@ -70,7 +71,6 @@ struct SampleArgs {
     uint64_t *hist;           // [rows][slices][kSampleBins]: count << 44 | weights
     SampleBorder *borders;    // [rows]
     double *sums;             // [rows][draws][waves][kSampleSlots] (plain: the sum, the maximum)
-    uint64_t *keys;           // [rows][draws][waves]: smallest and largest key of listed ones
     uint64_t *list;           // [rows][draws][kSampleList]
     int32_t *listed;          // [rows][draws]
     uint32_t *counters;       // [rows]: arrivals
@@ -84,13 +84,19 @@ struct SampleArgs {
 enum { kSampleF32 = 3 };   // beside MOE_BF16 and MOE_FP16
 
 __device__ __forceinline__ int max_i(int a, int b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t min_u64(uint64_t a, uint64_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t xor_u64(uint64_t v, int lanes) {
+    const uint32_t lo = __shfl_xor((uint32_t)v, lanes);
+    return (uint64_t)(uint32_t)__shfl_xor((uint32_t)(v >> 32), lanes) << 32 | lo;
+}
 
 // The logits of a 16-byte chunk.
 template <int Type>
 struct Logits {
     static constexpr int kPer = Type == kSampleF32 ? 4 : 8;
     static constexpr int kBytes = 16 / kPer;
+    static constexpr int kDrop = Type == kSampleF32 ? 0 : Type == 0 ? 16 : 13;   // bits of f32 that say nothing
     static __device__ __forceinline__ float get(u32x4 c, int e) {
         if constexpr (Type == kSampleF32) return __uint_as_float(c[e]);
         if constexpr (Type == 0) return e & 1 ? Bf16::hi(c[e >> 1]) : Bf16::lo(c[e >> 1]);
@@ -145,10 +151,10 @@ __device__ __forceinline__ int sample_top(float place) {
     return max_i(sample_bin(place), -(1 << 29) + 2 * kSampleBins);
 }
 
-// 2^y for y <= 1 (NaN: 0), to 2^-44: with r = y less the nearest integer, 1 + r q(r),
+// 2^y for y <= 0 (above: 1, NaN: 0), to 2^-44: with r = y less the nearest integer, 1 + r q(r),
 // where q has the values of (2^r - 1) / r at nine Chebyshev nodes of [-1/2, 1/2].
 __device__ __forceinline__ double exp2_64(double y) {
-    y = fmax(y, -1100.0);
+    y = fmin(fmax(y, -1100.0), 0.0);
     const double n = __builtin_rint(y), r = y - n;
     double q = 1.0203121063391729e-07;
     q = fma(q, r, 1.3255224878668817e-06);
@@ -161,12 +167,19 @@ __device__ __forceinline__ double exp2_64(double y) {
     q = fma(q, r, 0.6931471805599453);
     return __builtin_ldexp(fma(q, r, 1.0), (int)n);
 }
-// c: log2(e) / T.  The maximum has weight 1, also where it is infinite; -inf and NaN
-// have none.
-__device__ __forceinline__ double sample_weight(float x, float max, double c) {
-    if (max == __builtin_inff()) return x == max ? 1.0 : 0.0;
-    return exp2_64(((double)x - (double)max) * c);
-}
+// The weight of a row's values: the maximum has 1, also where it is infinite (then all
+// finite ones have none); -inf and NaN have none.
+struct SampleWeight {
+    double max, c;      // c: log2(e) / T
+    __device__ __forceinline__ SampleWeight(float of_max, float temperature) {
+        const bool inf = of_max == __builtin_inff();
+        max = inf ? 0x1p128 : (double)of_max;
+        c = inf ? 0x1p900 : 1.44269504088896340736 / (double)temperature;
+    }
+    __device__ __forceinline__ double operator()(float x) const {
+        return exp2_64(((double)x - max) * c);
+    }
+};
 
 // Order of values as unsigned integers: larger x, smaller key.  NaN counts as -inf, and
 // the two zeros are equal.
@@ -176,6 +189,27 @@ __device__ __forceinline__ uint32_t sample_key(float x) {
 }
 __device__ __forceinline__ float sample_value(uint32_t key) {
     return __uint_as_float(key >> 31 ? key : ~key & 0x7FFFFFFFu);
+}
+// The order of tokens: by value, then by index.
+template <int Type>
+__device__ __forceinline__ uint64_t sample_order(float x, int index) {
+    return (uint64_t)(sample_key(x) >> Logits<Type>::kDrop) << kSampleIndexBits | (uint32_t)index;
+}
+template <int Type>
+__device__ __forceinline__ float sample_ordered(uint64_t order) {
+    constexpr int kDrop = Logits<Type>::kDrop;
+    const uint32_t key = (uint32_t)(order >> kSampleIndexBits) << kDrop;
+    return sample_value(key >> 31 ? key : key | ((1u << kDrop) - 1));   // (what is dropped is zero in x)
+}
+__device__ __forceinline__ int sample_index(uint64_t order) {
+    return (int)(order & ((1u << kSampleIndexBits) - 1));
+}
+// The natural logarithm of x >= 1, to 2^-40: a 32-bit one, corrected by what is left.
+__device__ __forceinline__ double log_64(double x) {
+    int e = __builtin_amdgcn_frexp_exp(x);
+    const double y = (double)e + (double)log2_((float)__builtin_ldexp(x, -e));
+    const double half = exp2_64(-0.5 * y), r = x * half * half - 1.0;   // (2^-y may be too small)
+    return y * 0.69314718055994530942 + (r - 0.5 * r * r);
 }
 
 // Adds the value that DPP control `C` brings in the rows of `Rows`, elsewhere zero.
@@ -195,6 +229,19 @@ __device__ __forceinline__ V wave_scan_d(V v) {
     v = add_dpp<0x118, 0xF>(v);
     v = add_dpp<0x142, 0xA>(v);     // rows 1 and 3: the last lane of the row before
     return add_dpp<0x143, 0xC>(v);  // rows 2 and 3: lane 31
+}
+// The same of 32 bits.
+template <int C, int Rows>
+__device__ __forceinline__ int add_dpp_i(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, C, Rows, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan_i(int v) {
+    v = add_dpp_i<0x111, 0xF>(v);
+    v = add_dpp_i<0x112, 0xF>(v);
+    v = add_dpp_i<0x114, 0xF>(v);
+    v = add_dpp_i<0x118, 0xF>(v);
+    v = add_dpp_i<0x142, 0xA>(v);
+    return add_dpp_i<0x143, 0xC>(v);
 }
 __device__ __forceinline__ double lane_d(double v, int lane) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
@@ -233,10 +280,9 @@ __device__ __forceinline__ V block_scan_d(V v, V *total, V *s_wave) {
     return before + (lane_id() ? __builtin_bit_cast(V, (uint64_t)hi << 32 | lo) : (V)0);
 }
 __device__ __forceinline__ int block_scan_i(int v, int *total, int *s_wave) {
-    int all;
-    const int at = wave_excl_scan(v, &all);
+    const int inc = wave_scan_i(v);
     __syncthreads();
-    if (lane_id() == 0) s_wave[wave_index()] = all;
+    if (lane_id() == 63) s_wave[wave_index()] = inc;
     __syncthreads();
     int before = 0, sum = 0;
 #pragma unroll
@@ -245,7 +291,7 @@ __device__ __forceinline__ int block_scan_i(int v, int *total, int *s_wave) {
         sum += s_wave[w];
     }
     *total = sum;
-    return before + at;
+    return before + inc - v;
 }
 __device__ __forceinline__ void store_agent_d(double *p, double v) {
     __hip_atomic_store((uint64_t *)p, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
@@ -262,51 +308,50 @@ __device__ __forceinline__ double load_agent_d(const double *p) {
 template <int Type>
 struct Segment {
     typedef Logits<Type> L;
-    const char *row;
+    rsrc_t memory;          // the row's chunks; behind them reads give zero
     int shift;              // values before the row's first in its first chunk
     int chunk0, chunks;
-    int total;              // chunks of the row
 
     __device__ __forceinline__ Segment(const SampleArgs &a, int r, int segment, int chunks)
         : chunks(chunks) {
         const uintptr_t at = (uintptr_t)a.x + (uint64_t)r * a.stride * L::kBytes;
-        row = (const char *)at;
         shift = (int)(at & 15) / L::kBytes;
         chunk0 = segment * chunks;
-        total = (shift + a.vocab + L::kPer - 1) / L::kPer;
+        const int total = (shift + a.vocab + L::kPer - 1) / L::kPer;
+        memory = __builtin_amdgcn_make_buffer_rsrc((void *)(at - shift * L::kBytes), (short)0,
+                                                   16 * total, 0x00020000);
     }
+    __device__ __forceinline__ u32x4 chunk(int i) const { return buf_ld16<false>(memory, 16u * (uint32_t)i); }
     // f(value, index) for every value of this lane (NaN too), as often in all lanes; what
-    // is beyond the row is -inf.  Four values to a round of the loop: more of them are more
+    // is beyond the row is -inf.  U values to a round of the loop: more of them are more
     // code than is fetched while a short segment's values are on their way (two thirds of
     // the time of one row went into that), and as many registers.
-    template <class F>
+    template <int U, class F>
     __device__ __forceinline__ void each(int vocab, F f) const {
-        const char *base = row - shift * L::kBytes;
         const int lane = lane_id();
-        auto load = [&](int i0) {
-            return ld16(base + 16 * (int64_t)min(chunk0 + min(i0 + lane, chunks - 1), total - 1));
-        };
         // Chunks that hold values of the row only, and all lanes have one.
         const int from = shift ? 1 : 0, to = min(chunk0 + chunks, (shift + vocab) / L::kPer);
-        u32x4 c0 = load(0), c1 = load(64), c2 = load(128), c3 = load(192);
+        const int first = chunk0 + lane;
+        u32x4 c0 = chunk(first), c1 = chunk(first + 64), c2 = chunk(first + 128), c3 = chunk(first + 192);
 #pragma unroll 1
         for (int i0 = 0; i0 < chunks; i0 += 64) {
             u32x4 c = c0;
             c0 = c1;
             c1 = c2;
             c2 = c3;
-            if (i0 + 256 < chunks) c3 = load(i0 + 256);
-            const int at = (chunk0 + i0 + lane) * L::kPer - shift;
+            c3 = chunk(first + i0 + 256);
+            const int at = (first + i0) * L::kPer - shift;
             if (chunk0 + i0 < from || chunk0 + i0 + 64 > to) {
 #pragma unroll
                 for (int e = 0; e < L::kPer; ++e)
                     if (i0 + lane >= chunks || (uint32_t)(at + e) >= (uint32_t)vocab) L::hide(c, e);
             }
+            constexpr int kRound = U < L::kPer ? U : L::kPer;
 #pragma unroll 1
-            for (int e = 0; e < L::kPer; e += 4) {
+            for (int e = 0; e < L::kPer; e += kRound) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f(L::get(c, j), at + e + j);
-                if constexpr (L::kPer == 8) c = (u32x4){c[2], c[3], 0u, 0u};
+                for (int j = 0; j < kRound; ++j) f(L::get(c, j), at + e + j);
+                if constexpr (kRound == 4 && L::kPer == 8) c = (u32x4){c[2], c[3], 0u, 0u};
             }
         }
     }
@@ -320,9 +365,10 @@ struct SampleBin {
 };
 
 // By the last slice of a row: the others' results are read where they are coherent.
+template <int Type>
 __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const SampleRow &f, int row,
                                                     float scale, const uint64_t *own_hist,
-                                                    int *s_wave_i, double *s_wave_d,
+                                                    int *s_wave_i, double *s_wave_d, double *s_far,
                                                     SampleBin *s_bin) {
     constexpr int kMine = kSampleBins / kSampleThreads;
     static_assert(kSamplePerOctave == 64.f, "an octave for a wave");
@@ -333,7 +379,6 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
     const uint64_t h0 = __hip_atomic_load(head, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const uint64_t h1 = __hip_atomic_load(head + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const float its_max = __uint_as_float((uint32_t)h0), max = wave_max(its_max);
-    const int values = wave_sum_i(lane < a.slices_n ? (int)(h1 >> 32) : 0);
     const float place = sample_place(max, scale);
     const int bin = sample_top(place);
     const int by = its_max > -__builtin_inff() ? min(bin - (int)(uint32_t)h1, kSampleBins) : kSampleBins;
@@ -377,31 +422,34 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
     }
     // Up to and with each bin; weights in units of the maximum's, up to a factor that
     // all share.
-    double unit = 0x1p-24 * __builtin_ldexp(exp2_64(fmin(((double)(bin + 1) - (double)place - lane) *
-                                                             (1.0 / kSamplePerOctave), 1.0)),
-                                            -kMine * wave_index());
+    double unit = 0x1p-24 *
+                  __builtin_ldexp(exp2_64(((double)bin - (double)place - lane) * (1.0 / kSamplePerOctave)),
+                                  -kMine * wave_index());
     int count[kMine], here = 0;
-    double mass[kMine], here_mass = 0.0;
+    double mass[kMine], here_mass = 0.0, far = 0.0;     // far: weights times bins
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
-        // The last bin has what is left; its weights, below 2^-63 each, do not show.
+        // The last bin has what is left: its weights, below 2^-63 each, do not show, and it is
+        // counted if need be.
         const bool is = r0 + 64 * j < kSampleBins - 1;
-        int all;
-        const int n = is ? (int)sum_count[j] : 0;
-        count[j] = here + wave_excl_scan(n, &all) + n;
-        here += all;
-        mass[j] = here_mass + wave_scan_d(is ? (double)sum_mass[j] * unit : 0.0);
+        count[j] = here + wave_scan_i(is ? (int)sum_count[j] : 0);
+        here = __builtin_amdgcn_readlane(count[j], 63);
+        const double m = is ? (double)sum_mass[j] * unit : 0.0;
+        far += m * (r0 + 64 * j);
+        mass[j] = here_mass + wave_scan_d(m);
         here_mass = lane_d(mass[j], 63);
         unit *= 0.5;
     }
+    far = wave_sum_d(far);
     __syncthreads();
     if (lane == 0) {
         s_wave_i[wave_index()] = here;
         s_wave_d[wave_index()] = here_mass;
+        s_far[wave_index()] = far;
     }
     __syncthreads();
     int all_count = 0, c0 = 0;
-    double all_mass = 0.0, m0 = 0.0;
+    double all_mass = 0.0, m0 = 0.0, all_far = 0.0;
 #pragma unroll
     for (int w = 0; w < kSampleWaves; ++w) {
         if (w == wave_index()) {
@@ -410,10 +458,11 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
         }
         all_count += s_wave_i[w];
         all_mass += s_wave_d[w];
+        all_far += s_far[w];
     }
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
-        count[j] = r0 + 64 * j < kSampleBins - 1 ? count[j] + c0 : values;
+        count[j] += c0;
         mass[j] += m0;
     }
     // s_bin[k]: the first bin that `reached` (the last one always is).
@@ -446,7 +495,7 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
         __syncthreads();
         return s_bin[k];
     };
-    int top = 0, bottom = kSampleBins - 1, above = 0, upto = values;
+    int top = 0, bottom = kSampleBins - 1, above = 0, upto = 0;
     double lo = all_mass, hi = all_mass;
     if (f.top_k) {
         const SampleBin k = first_bin(0, [&](int j) { return count[j] >= f.top_k; });
@@ -461,23 +510,38 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
         top = 0;
         above = 0;
     } else if (f.by_p) {
-        // What the sums of weights may be off by: 2^-23 each for the power and for the
-        // 24 bits, and for places and their scale, rounded to 24 bits both (ln 2 / 64 a
+        // What any sum of weights may be off by: each by 2^-23 for its power and for its 24
+        // bits, and for its place and the scale, rounded to 24 bits both (ln 2 / 64 a
         // place; more, where they are off by many).
-        const double off = 0x1p-20 + (fabs((double)place) + kSampleBins) * 0x1p-24 * 0.035;
-        const double least = f.top_p * lo * (1.0 - off), most = f.top_p * hi * (1.0 + off);
+        const double off = all_mass * (0x1p-21 + fabs((double)place) * 0x1p-24 * 0.035) +
+                           all_far * 0x1p-24 * 0.035;
+        const double least = f.top_p * (lo - off) - off, most = f.top_p * (hi + off) + off;
         const SampleBin p =
-            first_bin(1, [&](int j) { return mass[j] * (1.0 + off) >= least; });
+            first_bin(1, [&](int j) { return mass[j] >= least; });
         if (!f.top_k || p.bin < top) {
             top = p.bin;
             above = p.count_before;
         }
         if (!f.top_k) {
             const SampleBin q =
-                first_bin(2, [&](int j) { return mass[j] * (1.0 - off) >= most; });
+                first_bin(2, [&](int j) { return mass[j] >= most; });
             bottom = q.bin;
             upto = q.count;
         }
+    }
+    if (bottom == kSampleBins - 1) {
+        // All finite values, then.
+        int n = 0;
+        for (int i = wave_index(); i < a.slices_n * kSampleWaves; i += kSampleWaves)
+            Segment<Type>(a, row, i, a.chunks)
+                .template each<4>(a.vocab, [&](float x, int) { n += x > -__builtin_inff(); });
+        n = wave_sum_i(n);
+        __syncthreads();
+        if (lane == 0) s_wave_i[wave_index()] = n;
+        __syncthreads();
+        upto = 0;
+#pragma unroll
+        for (int w = 0; w < kSampleWaves; ++w) upto += s_wave_i[w];
     }
     // The smallest values in bins above `top`, and in `bottom`: of the keys from +inf's to
     // that of the lowest finite value the last for which that holds, 64 tried at once.
@@ -505,12 +569,12 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
 template <int Type>
 __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_scan(const SampleArgs a) {
     __shared__ uint64_t s_hist[kSampleBins];
-    __shared__ double s_wave_d[kSampleWaves];
+    __shared__ double s_wave_d[kSampleWaves], s_far[kSampleWaves];
     __shared__ int s_wave_i[kSampleWaves];
     __shared__ SampleBin s_bin[3];
     __shared__ uint32_t s_last;
     __shared__ float s_max[kSampleWaves];
-    __shared__ int s_first[kSampleWaves], s_count[kSampleWaves];
+    __shared__ int s_first[kSampleWaves];
     const int row = (int)blockIdx.x / a.slices_n, slice = (int)blockIdx.x % a.slices_n;
     const int lane = lane_id(), wave = wave_index();
     const SampleRow f = sample_row(a, row);
@@ -519,11 +583,11 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_scan(const SampleA
     if (binned)
         for (int i = threadIdx.x; i < kSampleBins; i += kSampleThreads) s_hist[i] = 0;
     float max = -__builtin_inff();
-    seg.each(a.vocab, [&](float x, int) { max = fmaxf(max, x); });
+    seg.template each<8>(a.vocab, [&](float x, int) { max = fmaxf(max, x); });
     max = wave_max(max);
     int first = 0x7FFFFFFF;
     if (f.greedy) {
-        seg.each(a.vocab, [&](float x, int i) { first = x == max ? min(first, i) : first; });
+        seg.template each<8>(a.vocab, [&](float x, int i) { first = x == max ? min(first, i) : first; });
         first = wave_min_i(first);
     }
     if (lane == 0) {
@@ -544,9 +608,11 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_scan(const SampleA
         __hip_atomic_store(mine, (uint64_t)(uint32_t)first << 32 | __float_as_uint(max),
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (!binned) return;
-    int low = 0;
+    if (threadIdx.x == 0)
+        __hip_atomic_store(mine + 1, (uint64_t)(uint32_t)top, __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
     if (max > -__builtin_inff())
-        seg.each(a.vocab, [&](float x, int) {
+        seg.template each<8>(a.vocab, [&](float x, int) {
             const float place = sample_place(x, scale);
             const int r = top - sample_bin(place);
             // 2^24 times the weight in units of that of the bin's upper end
@@ -555,31 +621,12 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_scan(const SampleA
             if (r < kSampleBins - 1)
                 __hip_atomic_fetch_add(&s_hist[r], 1ull << 44 | (uint32_t)w, __ATOMIC_RELAXED,
                                        __HIP_MEMORY_SCOPE_WORKGROUP);
-            else
-                low += x > -__builtin_inff();
         });
     __syncthreads();
-    // All of its values: those that are not in the last bin of this slice may be in the
-    // row's.
-    int count = low;
-    uint64_t *hist = a.hist + (int64_t)blockIdx.x * kSampleBins;
-#pragma unroll
-    for (int j = 0; j < kSampleBins / kSampleThreads; ++j) {
-        const int i = threadIdx.x + kSampleThreads * j;
-        const uint64_t v = s_hist[i];
-        count += (int)(v >> 44);
-        if (a.slices_n > 1)
-            __hip_atomic_store(hist + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    count = wave_sum_i(count);
-    if (lane == 0) s_count[wave] = count;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        count = 0;
-#pragma unroll
-        for (int w = 0; w < kSampleWaves; ++w) count += s_count[w];
-        __hip_atomic_store(mine + 1, (uint64_t)(uint32_t)count << 32 | (uint32_t)top,
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (a.slices_n > 1) {
+        uint64_t *hist = a.hist + (int64_t)blockIdx.x * kSampleBins;
+        for (int i = threadIdx.x; i < kSampleBins; i += kSampleThreads)
+            __hip_atomic_store(hist + i, s_hist[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     wait_vm_all();
     __syncthreads();
@@ -588,80 +635,19 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_scan(const SampleA
                                         __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (s_last != (uint32_t)a.slices_n - 1) return;
-    const SampleBorder b = find_border(a, f, row, scale, s_hist, s_wave_i, s_wave_d, s_bin);
+    const SampleBorder b = find_border<Type>(a, f, row, scale, s_hist, s_wave_i, s_wave_d, s_far,
+                                             s_bin);
     if (threadIdx.x == 0) {
         a.borders[row] = b;
         store_agent(a.counters + row, 0u);
     }
 }
 
-// Sorts n different 64-bit keys in LDS, K a thread: in registers among a thread's own, by
-// lane exchanges within a wave, and through LDS between waves only (a stage through LDS
-// takes 0.2 us, most of it the barriers).
-template <int K>
-__device__ __forceinline__ void sort_keys(uint64_t *s, int n) {
-    const int own = threadIdx.x;
-    uint64_t v[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = K * own + k < n ? s[K * own + k] : ~0ull;
-    int n2 = K;
-    while (n2 < n) n2 <<= 1;
-#pragma unroll 1
-    for (int size = 2; size <= n2; size <<= 1)
-#pragma unroll 1
-        for (int by = size >> 1; by > 0; by >>= 1) {
-            if (by < K) {
-#pragma unroll
-                for (int b = 1; b < K; b <<= 1) {
-                    if (b != by) continue;
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        if (k & b) continue;
-                        const bool up = ((K * own + k) & size) == 0;
-                        const uint64_t x = v[k], y = v[k | b];
-                        const bool swap = (x > y) == up;
-                        v[k] = swap ? y : x;
-                        v[k | b] = swap ? x : y;
-                    }
-                }
-                continue;
-            }
-            const int lanes = by / K;
-            const bool keep_min = ((K * own & by) == 0) == ((K * own & size) == 0);
-            if (lanes >= 64) {
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < K; ++k) s[kSampleThreads * k + own] = v[k];
-                __syncthreads();
-            }
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                uint64_t o;
-                if (lanes >= 64) {
-                    o = s[kSampleThreads * k + (own ^ lanes)];
-                } else {
-                    const uint32_t lo = __shfl_xor((uint32_t)v[k], lanes);
-                    o = (uint64_t)(uint32_t)__shfl_xor((uint32_t)(v[k] >> 32), lanes) << 32 | lo;
-                }
-                v[k] = (o < v[k]) == keep_min ? o : v[k];
-            }
-        }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (K * own + k < n) s[K * own + k] = v[k];
-    __syncthreads();
-}
-
 template <int Type>
 struct SampleLds {
-    union {
-        uint64_t list[kSampleList];
-        struct {
-            uint32_t count[kSampleKeyBins];
-            unsigned long long mass[kSampleKeyBins];
-        } bins;
-    };
+    uint64_t list[kSampleList];
+    uint32_t count_of[kSampleKeyBins];
+    unsigned long long mass_of[kSampleKeyBins];
     union {
         double wave_d[kSampleWaves];
         uint64_t wave_u[kSampleWaves];
@@ -671,12 +657,11 @@ struct SampleLds {
     union {
         double upto[kSampleSegments];          // of a segment's kept ones at the border
         unsigned long long quanta[kSampleSegments];
-        int equal[kSampleSegments];            // values like the border's in a segment
     };
     int n, found;
     uint32_t last;
-    int token, count, before, bin;
-    uint64_t mass_before;
+    int count, before, bin;
+    uint64_t mass_before, border, list_end[kSampleWaves];
 };
 // Of k_sample_plain.
 struct SamplePlainLds {
@@ -727,8 +712,7 @@ __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const S
 #pragma unroll 1
         for (int j = 0; j < per; ++j) {
             const int in = first + j, at = (seg.chunk0 + in) * L::kPer - seg.shift;
-            u32x4 c = ld16(seg.row - seg.shift * L::kBytes +
-                           16 * (int64_t)min(seg.chunk0 + in, seg.total - 1));
+            u32x4 c = seg.chunk(seg.chunk0 + in);
 #pragma unroll 1
             for (int e = 0; e < L::kPer; e += 4) {
 #pragma unroll
@@ -743,26 +727,37 @@ __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const S
             }
         }
     };
-    double sum = 0.0, all;
-    each_kept([&](int, double w) { sum += w; });
-    const double before = s.seg[who] + block_scan_d(sum, &all, s.wave_d);
-    // (Where rounding leaves nobody beyond the target, the last that is kept.)
-    const int by = first_place(s, kSampleThreads, [&](int) { return sum > 0.0 && before + sum > target; },
-                               [&](int) { return sum > 0.0; });
-    if (own == by) {
+    // Twice: the threads' sums, then the token by the thread that has it.
+    double sum = 0.0, before = 0.0;
+    int by = own;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
         double at = before, of = 1.0;
         int token = 0;
         bool found = false;
-        each_kept([&](int i, double w) {
-            at += w;
-            if (!found && w > 0.0) {
-                token = i;
-                of = w;
-                found = at > target;
+        if (own == by)
+            each_kept([&](int i, double w) {
+                at += w;
+                if (!found && w > 0.0) {
+                    token = i;
+                    of = w;
+                    found = at > target;
+                }
+            });
+        if (pass) {
+            if (own == by) {
+                a.token[row] = token;
+                a.logprob[row] = (float)-log_64(total / of);
             }
-        });
-        a.token[row] = token;
-        a.logprob[row] = (float)log(of / total);
+            return;
+        }
+        double all;
+        sum = at;
+        before = s.seg[who] + block_scan_d(sum, &all, s.wave_d);
+        // (Where rounding leaves nobody beyond the target, the last that is kept.)
+        by = first_place(s, kSampleThreads,
+                         [&](int) { return sum > 0.0 && before + sum > target; },
+                         [&](int) { return sum > 0.0; });
     }
 }
 
@@ -775,43 +770,31 @@ __device__ __forceinline__ void each_segment(const SampleArgs &a, int row, F f) 
     }
 }
 
-// Of the listed values with keys from lo to hi: the key at which a sum reaches `target`,
-// by count or by weight (in 2^-44), with what is before it in s.before and s.mass_before
-// (if weights are summed) and how often it is there in s.count.  base: the sum before the
-// first of them.
-template <int Type, class Listed, class Weight>
-__device__ __forceinline__ uint32_t border_key(const SampleArgs &a, int row, SampleLds<Type> &s,
-                                               bool by_mass, bool summed, double base,
-                                               double target, uint32_t lo, uint32_t hi,
-                                               Listed listed, Weight weight_of) {
+// Among values in the order of tokens, from lo to hi: the one at which a sum reaches
+// `target`, by count or by weight (in units), else the last one, as s.border; what is
+// before it in s.before and (if weights are summed) s.mass_before.  base: the sum before
+// the first of them.  visit(f) calls f(order, weight()) for all there are.
+template <class Lds, class Visit>
+__device__ __forceinline__ void find_border_token(Lds &s, bool by_mass, bool summed, double base,
+                                                  double unit, double target, uint64_t lo,
+                                                  uint64_t hi, Visit visit) {
+    const double per = 1.0 / unit;
     int before = 0;
     uint64_t mass_before = 0;
     for (;;) {
-        int shift = 0;
-        while ((hi - lo) >> shift >= kSampleKeyBins) ++shift;
+        const uint64_t range = hi - lo;
+        const int shift = range < kSampleKeyBins ? 0 : 64 - 11 - __builtin_clzll(range);
         __syncthreads();
         for (int i = threadIdx.x; i < kSampleKeyBins; i += kSampleThreads) {
-            s.bins.count[i] = 0;
-            s.bins.mass[i] = 0;
+            s.count_of[i] = 0;
+            s.mass_of[i] = 0;
         }
         __syncthreads();
-        each_segment<Type>(a, row, [&](const Segment<Type> &seg, int) {
-            seg.each(a.vocab, [&](float x, int) {
-                const uint32_t key = sample_key(x);
-                const bool in = listed(x) && key >= lo && key <= hi;
-                const uint64_t here = __ballot(in);
-                if (!here) return;
-                const uint64_t m = summed ? (uint64_t)(weight_of(x) * 0x1p44) : 0;
-                // (All of one value, as equal logits are: one addition for the wave.)
-                const int first = __builtin_ctzll(here);
-                const uint32_t value = __builtin_amdgcn_readlane(key, first);
-                const bool one = __ballot(in && key == value) == here;
-                const int n = one ? __builtin_popcountll(here) : 1;
-                if (one ? lane_id() == first : in) {
-                    atomicAdd(&s.bins.count[(key - lo) >> shift], (uint32_t)n);
-                    if (summed) atomicAdd(&s.bins.mass[(key - lo) >> shift], (unsigned long long)m * n);
-                }
-            });
+        visit([&](uint64_t order, auto weight) {
+            if (order < lo || order > hi) return;
+            const int bin = (int)((order - lo) >> shift);
+            atomicAdd(&s.count_of[bin], 1u);
+            if (summed) atomicAdd(&s.mass_of[bin], (unsigned long long)__builtin_rint(weight() * per));
         });
         __syncthreads();
         // The bin at which the sum reaches the target, or the last that holds any.
@@ -821,13 +804,14 @@ __device__ __forceinline__ uint32_t border_key(const SampleArgs &a, int row, Sam
         uint64_t here_mass = 0, all_mass;
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
-            here += (int)s.bins.count[r0 + j];
-            here_mass += s.bins.mass[r0 + j];
+            here += (int)s.count_of[r0 + j];
+            here_mass += s.mass_of[r0 + j];
         }
         const int c0 = before + block_scan_i(here, &all_count, s.wave_i);
-        const uint64_t m0 = mass_before + block_scan_d(here_mass, &all_mass, s.wave_u);
+        uint64_t m0 = 0;
+        if (summed) m0 = mass_before + block_scan_d(here_mass, &all_mass, s.wave_u);
         auto reached = [&](int c, uint64_t m) {
-            return by_mass ? base + (double)m * 0x1p-44 >= target : base + (double)c >= target;
+            return by_mass ? base + (double)m * unit >= target : base + (double)c >= target;
         };
         const int who = first_place(
             s, kSampleThreads, [&](int) { return here && reached(c0 + here, m0 + here_mass); },
@@ -835,25 +819,33 @@ __device__ __forceinline__ uint32_t border_key(const SampleArgs &a, int row, Sam
         if ((int)threadIdx.x == who) {
             int c = c0;
             uint64_t m = m0;
+#pragma unroll 1
             for (int j = 0; j < kMine; ++j) {
-                const int n = (int)s.bins.count[r0 + j];
+                const int n = (int)s.count_of[r0 + j];
                 if (!n) continue;
                 s.bin = r0 + j;
                 s.count = n;
                 s.before = c;
                 s.mass_before = m;
                 c += n;
-                m += s.bins.mass[r0 + j];
+                m += s.mass_of[r0 + j];
                 if (reached(c, m)) break;
             }
         }
         __syncthreads();
         before = s.before;
         mass_before = s.mass_before;
-        lo += (uint32_t)s.bin << shift;
-        hi = min(hi, lo + ((1u << shift) - 1));
-        if (shift == 0 || lo == hi) return lo;
+        lo += (uint64_t)s.bin << shift;
+        hi = min(hi, lo + ((1ull << shift) - 1));
+        if (s.count == 1 || shift == 0) break;
     }
+    if (threadIdx.x == 0) s.border = lo;
+    __syncthreads();
+    if (lo < hi)     // the only one in its bin
+        visit([&](uint64_t order, auto) {
+            if (order >= lo && order <= hi) s.border = order;
+        });
+    __syncthreads();
 }
 
 template <int Type>
@@ -877,9 +869,9 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
         }
         return;
     }
-    const double c = 1.44269504088896340736 / (double)f.temperature, min_p = f.min_p;
+    const SampleWeight weight_of(max, f.temperature);
+    const double min_p = f.min_p;
     if (!f.top_k && !f.by_p) b = {-3.402823466e38f, -3.402823466e38f, a.vocab, 0};   // all are above
-    auto weight_of = [&](float x) { return sample_weight(x, max, c); };
     auto kept_weight = [&](float x) {
         const double w = weight_of(x);
         return w >= min_p ? w : 0.0;
@@ -888,25 +880,16 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
     const bool wide = b.listed > kSampleList;
     const bool rest = f.by_p && !f.top_k;     // the sum of all weights is needed
     uint32_t *arrived = a.counters + row;
-    uint64_t *list = a.list + (int64_t)blockIdx.x * kSampleList;
     if (threadIdx.x == 0) s.n = 0;
     __syncthreads();
     double above = 0.0, kept = 0.0, total = 0.0;
-    uint32_t key_lo = ~0u, key_hi = 0;
     auto list_it = [&](float x, int i) {
-        const uint32_t key = sample_key(x);
-        if (wide) {
-            key_lo = min(key_lo, key);
-            key_hi = max_u(key_hi, key);
-        } else {
-            const int at = atomicAdd(&s.n, 1);
-            if (at < kSampleList)
-                __hip_atomic_store(list + at, (uint64_t)key << 32 | (uint32_t)i, __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
-        }
+        if (wide) return;
+        const int at = atomicAdd(&s.n, 1);
+        if (at < kSampleList) s.list[at] = sample_order<Type>(x, i);
     };
     if (rest)
-        seg.each(a.vocab, [&](float x, int i) {
+        seg.template each<4>(a.vocab, [&](float x, int i) {
             const double w = weight_of(x);
             total += w;
             const double is = x >= b.top ? w : 0.0;
@@ -915,7 +898,7 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
             if (is_listed(x)) list_it(x, i);
         });
     else
-        seg.each(a.vocab, [&](float x, int i) {
+        seg.template each<4>(a.vocab, [&](float x, int i) {
             if (x >= b.top) {
                 const double w = weight_of(x);
                 above += w;
@@ -927,26 +910,22 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
     above = wave_sum_d(above);
     kept = min_p > 0.0 ? wave_sum_d(kept) : above;
     if (rest) total = wave_sum_d(total);
-    if (wide)
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) {
-            key_lo = min(key_lo, (uint32_t)__shfl_xor((int)key_lo, m));
-            key_hi = max_u(key_hi, (uint32_t)__shfl_xor((int)key_hi, m));
-        }
     if (lane == 0) {
         const int64_t at = (int64_t)blockIdx.x * kSampleWaves + wave;
         double *to = a.sums + at * kSampleSlots;
         store_agent_d(to, above);
         store_agent_d(to + 1, kept);
         store_agent_d(to + 2, total);
-        if (wide)
-            __hip_atomic_store(a.keys + at, (uint64_t)key_hi << 32 | key_lo, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
-    if (threadIdx.x == 0)
-        __hip_atomic_store(a.listed + blockIdx.x, min(s.n, kSampleList), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+    int n = min(s.n, kSampleList);
+    if (a.draws > 1) {
+        uint64_t *list = a.list + (int64_t)blockIdx.x * kSampleList;
+        for (int i = threadIdx.x; i < n; i += kSampleThreads)
+            __hip_atomic_store(list + i, s.list[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (threadIdx.x == 0)
+            __hip_atomic_store(a.listed + blockIdx.x, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     wait_vm_all();
     __syncthreads();
     if (threadIdx.x == 0)
@@ -970,153 +949,122 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
     if (f.by_p) block_scan_d(above, &all_above, s.wave_d);
     if (rest) block_scan_d(total, &all_weights, s.wave_d);
 
-    // The border: values up to this one, by key and index, are kept, and those above.
+    // The border: in the order of tokens those up to this one are kept.
     uint64_t border = 0;
-    bool some = false;          // any of the listed ones are
-    const int per_segment = a.draw_chunks * L::kPer;
-    const int own = (int)threadIdx.x;
-    if (b.listed && !wide) {
-        // All slices' shares of the list: the n-th of all is the share's whose first is the
-        // last one up to n.
-        int n;
-        const int first = wave_excl_scan(lane < a.draws ? listed : 0, &n);
-        for (int j0 = 64 * wave; j0 < n; j0 += kSampleThreads) {
-            const int j = j0 + lane;
-            int share = 0;
-            for (int i = 1; i < a.draws; ++i) {
-                const int at = __builtin_amdgcn_readlane(first, i);
-                share = j >= at ? i : share;
-            }
-            const int at = __shfl(first, share);
-            if (j < n)
-                s.list[j] = __hip_atomic_load(
-                    a.list + ((int64_t)row * a.draws + share) * kSampleList + j - at,
-                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        for (int i = own; i < segments; i += kSampleThreads) s.quanta[i] = 0;
-        __syncthreads();
-        if (n <= kSampleThreads) sort_keys<1>(s.list, n);
-        else if (n <= 2 * kSampleThreads) sort_keys<2>(s.list, n);
-        else sort_keys<8>(s.list, n);
-        int take = f.top_k ? min(n, f.top_k - b.above) : n;
-        if (f.by_p) {
-            const int per = (n + kSampleThreads - 1) / kSampleThreads, j0 = own * per;
-            auto weight_at = [&](int j) { return weight_of(sample_value((uint32_t)(s.list[j] >> 32))); };
-            double sum = 0.0, all;
-            for (int j = j0; j < min(j0 + per, take); ++j) sum += weight_at(j);
-            double before = all_above + block_scan_d(sum, &all, s.wave_d);
-            const double target = (double)f.top_p * (rest ? all_weights : all_above + all);
-            int count = 0, in;
-            for (int j = j0; j < min(j0 + per, take); ++j) {
-                count += before < target;
-                before += weight_at(j);
-            }
-            block_scan_i(count, &in, s.wave_i);
-            take = max_i(in, b.above ? 0 : 1);
-        }
-        some = take > 0;
-        border = some ? s.list[take - 1] : 0;
-        // What is kept of it, by segment: as integers, whose sums have no order.
-        for (int j = own; j < take; j += kSampleThreads) {
-            const double w = kept_weight(sample_value((uint32_t)(s.list[j] >> 32)));
-            const int at = (int)(uint32_t)s.list[j] + seg.shift;
-            atomicAdd(&s.quanta[at / (a.draw_chunks * L::kPer)],
-                      (unsigned long long)__builtin_rint(w * 0x1p44));
-        }
-        __syncthreads();
-        const double mine = own < segments ? (double)s.quanta[own] * 0x1p-44 : 0.0;
-        double all;
-        const double before = block_scan_d(mine, &all, s.wave_d);
-        if (own <= segments)
-            s.seg[own] = own < segments ? kept_before + before : all_kept + all;
-        __syncthreads();
-    } else if (wide) {
-        uint32_t lo = ~0u, hi = 0;
-        for (int i = 0; i < segments; ++i) {
-            const uint64_t k = __hip_atomic_load(a.keys + (int64_t)row * segments + i,
-                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            lo = min(lo, (uint32_t)k);
-            hi = max_u(hi, (uint32_t)(k >> 32));
-        }
-        auto quantum = [&](uint32_t key) { return (uint64_t)(weight_of(sample_value(key)) * 0x1p44); };
-        uint32_t key = hi;
-        int equal = 0x7FFFFFFF, count = 0;      // kept of those with this key, and all
-        double mass = all_weights;
-        if (f.top_k) {
-            key = border_key<Type>(a, row, s, false, f.by_p, b.above, f.top_k, lo, hi, is_listed,
-                                   weight_of);
-            count = s.count;
-            equal = min(count, f.top_k - b.above - s.before);
-            mass = all_above + (double)(s.mass_before + equal * quantum(key)) * 0x1p-44;
-        }
-        if (f.by_p) {
-            const double target = (double)f.top_p * mass;
-            const uint32_t its = border_key<Type>(a, row, s, true, true, all_above, target, lo, key,
-                                                  is_listed, weight_of);
-            const double w = (double)quantum(its) * 0x1p-44;
-            const double left = target - (all_above + (double)s.mass_before * 0x1p-44);
-            const double more = w > 0.0 ? __builtin_ceil(left / w) : 0x1p31;
-            count = s.count;
-            const int n = (int)fmin(fmax(more, 1.0), (double)count);
-            equal = its == key ? min(equal, n) : n;
-            key = its;
-        }
-        some = equal > 0;
-        border = (uint64_t)key << 32 | 0xFFFFFFFFu;
-        __syncthreads();
-        if (equal < count) {
-            // Equal ones are kept by index: the index of the last that is.
-            each_segment<Type>(a, row, [&](const Segment<Type> &seg, int i) {
-                int n = 0;
-                seg.each(a.vocab, [&](float x, int) { n += x > -__builtin_inff() && sample_key(x) == key; });
-                n = wave_sum_i(n);
-                if (lane == 0) s.equal[i] = n;
-            });
-            __syncthreads();
-            int at = 0, before = 0;
-            while (before + s.equal[at] < equal) before += s.equal[at++];
-            if (wave == 0) {
-                Segment<Type> seg(a, row, at, a.draw_chunks);
-                        int from = at * per_segment - seg.shift - 1, to = from + per_segment;
-                while (to - from > 1) {       // (as many as are needed are up to `to`)
-                    const int mid = (from + to) >> 1;
-                    int n = 0;
-                    seg.each(a.vocab, [&](float x, int i) {
-                        n += x > -__builtin_inff() && sample_key(x) == key && i <= mid;
-                    });
-                    if (wave_sum_i(n) >= equal - before) to = mid;
-                    else from = mid;
+    const int own = (int)threadIdx.x, per_segment = a.draw_chunks * L::kPer;
+    double listed_kept = 0.0;       // of the listed ones those in segment `own`
+    if (b.listed) {
+        if (!wide && a.draws > 1) {
+            // All slices' shares of the list: the n-th of all is in the share whose first is
+            // the last one up to n.
+            const int upto = wave_scan_i(lane < a.draws ? listed : 0);
+            n = __builtin_amdgcn_readlane(upto, 63);
+            for (int j0 = 64 * wave; j0 < n; j0 += kSampleThreads) {
+                const int j = j0 + lane;
+                int share = 0, at = 0;
+                for (int i = 0; i < a.draws - 1; ++i) {
+                    const int end = __builtin_amdgcn_readlane(upto, i);
+                    share = j >= end ? i + 1 : share;
+                    at = j >= end ? end : at;
                 }
-                if (lane == 0) s.token = to;
+                if (j < n)
+                    s.list[j] = __hip_atomic_load(
+                        a.list + ((int64_t)row * a.draws + share) * kSampleList + j - at,
+                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+        if (!wide)
+            for (int i = own; i < segments; i += kSampleThreads) s.quanta[i] = 0;
+        auto visit = [&](auto f) {
+            if (wide) {
+                each_segment<Type>(a, row, [&](const Segment<Type> &seg, int) {
+                    seg.template each<4>(a.vocab, [&](float x, int i) {
+                        if (is_listed(x)) f(sample_order<Type>(x, i), [&] { return weight_of(x); });
+                    });
+                });
+            } else {
+                for (int j = own; j < n; j += kSampleThreads) {
+                    const uint64_t v = s.list[j];
+                    f(v, [&] { return weight_of(sample_ordered<Type>(v)); });
+                }
+            }
+        };
+        // Weights as integers, whose sums have no order: in 2^-44 of a power of two that
+        // none of these reaches.
+        const float largest = b.top == b.top ? b.top : max;
+        const int e = max_i(__builtin_amdgcn_frexp_exp(weight_of(largest)), -900) - 44;
+        const double unit = __builtin_ldexp(1.0, e);
+        uint64_t lo = sample_order<Type>(largest, 0);
+        border = sample_order<Type>(b.bottom, (1 << kSampleIndexBits) - 1);
+        if (!wide) {
+            // From the first to the last of the list: fewer passes, and fewer in one bin,
+            // whose additions wait for each other.
+            uint64_t first = ~0ull, last = 0;
+            for (int j = own; j < n; j += kSampleThreads) {
+                first = min_u64(first, s.list[j]);
+                last = max_u64(last, s.list[j]);
+            }
+#pragma unroll 1
+            for (int m = 32; m >= 1; m >>= 1) {
+                first = min_u64(first, xor_u64(first, m));
+                last = max_u64(last, xor_u64(last, m));
+            }
+            if (lane == 0) {
+                s.wave_u[wave] = first;
+                s.list_end[wave] = last;
             }
             __syncthreads();
-            border = (uint64_t)key << 32 | (uint32_t)s.token;
-            __syncthreads();
+            lo = s.wave_u[0];
+            border = s.list_end[0];
+#pragma unroll
+            for (int w = 1; w < kSampleWaves; ++w) {
+                lo = min_u64(lo, s.wave_u[w]);
+                border = max_u64(border, s.list_end[w]);
+            }
         }
-        each_segment<Type>(a, row, [&](const Segment<Type> &seg, int i) {
-            double sum = 0.0;
-            seg.each(a.vocab, [&](float x, int at) {
-                const bool is = some && is_listed(x) &&
-                                ((uint64_t)sample_key(x) << 32 | (uint32_t)at) <= border;
-                if (is) sum += kept_weight(x);
+        double mass = all_weights;
+        if (f.top_k || f.by_p) {
+#pragma unroll 1
+            for (int by_p = f.top_k ? 0 : 1; by_p <= (f.by_p ? 1 : 0); ++by_p) {
+                find_border_token(s, by_p, f.by_p, by_p ? all_above : (double)b.above, unit,
+                                  by_p ? (double)f.top_p * mass : (double)f.top_k, lo, border, visit);
+                border = s.border;
+                // (The first kept ones' weights: up to and with this one.)
+                mass = all_above + (double)s.mass_before * unit +
+                       weight_of(sample_ordered<Type>(border));
+            }
+        }
+        if (wide) {
+            each_segment<Type>(a, row, [&](const Segment<Type> &seg, int i) {
+                double sum = 0.0;
+                seg.template each<4>(a.vocab, [&](float x, int at) {
+                    if (is_listed(x) && sample_order<Type>(x, at) <= border) sum += kept_weight(x);
+                });
+                sum = wave_sum_d(sum);
+                if (lane == 0) s.upto[i] = sum;
             });
-            sum = wave_sum_d(sum);
-            if (lane == 0) s.upto[i] = sum;
-        });
-        __syncthreads();
-        double all;
-        const double before = block_scan_d(own < segments ? s.upto[own] : 0.0, &all, s.wave_d);
-        if (own <= segments)
-            s.seg[own] = own < segments ? kept_before + before : all_kept + all;
-        __syncthreads();
-    } else {
-        if (own <= segments) s.seg[own] = own < segments ? kept_before : all_kept;
-        __syncthreads();
+            __syncthreads();
+            listed_kept = own < segments ? s.upto[own] : 0.0;
+        } else {
+            const double per = 1.0 / unit;
+            for (int j = own; j < n; j += kSampleThreads) {
+                const uint64_t v = s.list[j];
+                if (v > border) continue;
+                atomicAdd(&s.quanta[(sample_index(v) + seg.shift) / per_segment],
+                          (unsigned long long)__builtin_rint(
+                              kept_weight(sample_ordered<Type>(v)) * per));
+            }
+            __syncthreads();
+            listed_kept = own < segments ? (double)s.quanta[own] * unit : 0.0;
+        }
     }
-
+    double all_listed = 0.0, listed_before = 0.0;
+    if (b.listed) listed_before = block_scan_d(listed_kept, &all_listed, s.wave_d);
+    if (own <= segments)
+        s.seg[own] = own < segments ? kept_before + listed_before : all_kept + all_listed;
+    __syncthreads();
     draw_token<Type>(a, row, f, s, kept_weight, [&](float x, int i) {
-        return x >= b.top ||
-               (some && ((uint64_t)sample_key(x) << 32 | (uint32_t)i) <= border);
+        return x >= b.top || sample_order<Type>(x, i) <= border;
     });
 }
 
@@ -1127,22 +1075,20 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_plain(const Sample
     const int row = (int)blockIdx.x / a.draws, slice = (int)blockIdx.x % a.draws;
     const int lane = lane_id(), wave = wave_index(), own = threadIdx.x;
     const SampleRow f = sample_row(a, row);
-    const double c = 1.44269504088896340736 / (double)f.temperature;
     // The segment's maximum, where it is first, and the weights in units of its own.
     {
         const Segment<Type> seg(a, row, slice * kSampleWaves + wave, a.draw_chunks);
         float max = -__builtin_inff();
-        seg.each(a.vocab, [&](float x, int) { max = fmaxf(max, x); });
+        seg.template each<4>(a.vocab, [&](float x, int) { max = fmaxf(max, x); });
         max = wave_max(max);
         double sum = 0.0;
         int first = 0x7FFFFFFF;
         if (f.greedy) {
-            seg.each(a.vocab, [&](float x, int i) { first = x == max ? min(first, i) : first; });
+            seg.template each<4>(a.vocab, [&](float x, int i) { first = x == max ? min(first, i) : first; });
             first = wave_min_i(first);
         } else if (max > -__builtin_inff()) {
-            seg.each(a.vocab, [&](float x, int) {
-                if (x > -__builtin_inff()) sum += sample_weight(x, max, c);
-            });
+            const SampleWeight weight_of(max, f.temperature);
+            seg.template each<4>(a.vocab, [&](float x, int) { sum += weight_of(x); });
             sum = wave_sum_d(sum);
         }
         if (lane == 0) {
@@ -1189,18 +1135,19 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_plain(const Sample
         }
         return;
     }
+    const SampleWeight weight_of(max, f.temperature);
     double before = 0.0;
 #pragma unroll 1
     for (int j = 0; j < kEach && 64 * j < segments; ++j) {
         const int i = 64 * j + lane;
         const bool is = i < segments && its[j] > -__builtin_inff();
-        const double inc = before + wave_scan_d(is ? part[j] * sample_weight(its[j], max, c) : 0.0);
+        const double inc = before + wave_scan_d(is ? part[j] * weight_of(its[j]) : 0.0);
         if (wave == 0 && i < segments) s.seg[i + 1] = inc;
         before = lane_d(inc, 63);
     }
     if (own == 0) s.seg[0] = 0.0;
     __syncthreads();
-    draw_token<Type>(a, row, f, s, [&](float x) { return sample_weight(x, max, c); },
+    draw_token<Type>(a, row, f, s, weight_of,
                      [](float, int) { return true; });
 }
 
