@@ -204,6 +204,9 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *cfg, i
  * call runs, so a plan holds while the members share their prefix: they may grow, pages
  * may move, and a member may be freed (it then sees nothing), but not become another
  * sequence.
+ * least: bytes of keys and values of one layer that reading prefixes once for each group has
+ * to spare; with less, sequences are decoded one by one, which then takes no longer (below
+ * 0: 200 MB, where that was measured to end; 0: prefixes are always read apart).
  * Host only: cu [groups + 1], members and prefix are host memory.  data NULL: only the
  * sizes; else it receives plan->ints integers, which the caller copies to the device and
  * puts the address of into plan->data. */
@@ -211,15 +214,18 @@ typedef struct {
     const int32_t *data;  /* device memory, 16-byte aligned */
     int64_t ints;         /* its size */
     int32_t batch, q_heads, kv_heads, head_dim;
-    int32_t units;        /* workgroups per kv head that read prefixes */
-    int32_t slots;        /* their partial results per kv head */
+    int32_t units;        /* workgroups that read prefixes */
+    int32_t tiles;        /* rows of a group, 128 at a time */
+    int32_t slots;        /* partial results per kv head */
+    int32_t parts;        /* most of a prefix */
     int32_t members;
     int32_t window, sinks;
     int32_t tail;         /* most positions that a sequence has by itself */
 } moe_attn_shared;
 moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *cfg, int32_t batch,
                           int32_t groups, const int32_t *cu, const int32_t *members,
-                          const int32_t *prefix, moe_attn_shared *plan, int32_t *data);
+                          const int32_t *prefix, int64_t least, moe_attn_shared *plan,
+                          int32_t *data);
 /* As moe_attn_workspace, of moe_attn_decode_shared. */
 moe_status moe_attn_shared_workspace(const moe_kv_cache *kv, const moe_attn_config *cfg,
                                      const moe_attn_shared *plan, size_t *workspace,

@@ -315,19 +315,21 @@ class PagedAttention:
         return out, lse
 
     def share(self, groups: Sequence[Sequence[int]], prefix: Sequence[int],
-              batch: Optional[int] = None) -> "SharedPrefix":
+              batch: Optional[int] = None, least: Optional[int] = None) -> "SharedPrefix":
         """A plan for decode_shared of the sequences 0 .. batch - 1 (None: as many as
         this one is for).  groups: lists of sequences, each sequence in one at
         most; prefix: as many numbers of positions, from the first on, whose keys
         and values are the same in all of a group.  After fork that is what the
-        parent had; its last page, if in part, may be counted in or not."""
-        return SharedPrefix(self, groups, prefix, self.batch if batch is None else batch)
+        parent had; its last page, if in part, may be counted in or not.  least:
+        bytes of keys and values of a layer that sharing has to spare, else
+        sequences are decoded one by one (None: what it takes to be faster)."""
+        return SharedPrefix(self, groups, prefix, self.batch if batch is None else batch, least)
 
     def decode_shared(self, layer: int, q, shared: "SharedPrefix"):
         """decode() of the plan's sequences: q [shared.batch, q_heads, head_dim]; the
-        keys and values of shared prefixes are read once for a group.  The results
-        are decode()'s up to rounding: of what a prefix adds, weights are held in q's
-        type, as prompt() does."""
+        keys and values of shared prefixes are read once for a group, where the plan
+        finds that worth while.  The results are decode()'s up to rounding: of what a
+        prefix adds, weights are held in q's type, as prompt() does."""
         if current_device() != self._index:
             with torch.cuda.device(self.device):
                 return self.decode_shared(layer, q, shared)
@@ -392,7 +394,7 @@ class SharedPrefix:
     member's place needs a new plan.  The plan is kept until its work on every
     stream is done, and by graphs that captured it."""
 
-    def __init__(self, attention: PagedAttention, groups, prefix, batch: int):
+    def __init__(self, attention: PagedAttention, groups, prefix, batch: int, least=None):
         groups, prefix = [list(g) for g in groups], list(prefix)
         require(len(groups) == len(prefix),
                 f"{len(groups)} groups, and prefixes of {len(prefix)}")
@@ -407,6 +409,8 @@ class SharedPrefix:
         for p in prefix:
             require(isinstance(p, int) and 0 <= p < 1 << 31,
                     f"prefix: integers from 0 to 2^31 - 1 are needed, got {p!r}")
+        require(least is None or isinstance(least, int) and 0 <= least < 1 << 63,
+                f"least: a number of bytes is needed, got {least!r}")
         # (An empty group has no use, and there may be more of them than sequences.)
         pairs = [(g, p) for g, p in zip(groups, prefix) if g]
         cu, members = [0], []
@@ -421,7 +425,7 @@ class SharedPrefix:
 
         def make(data):
             check(L.moe_attn_share(kv._ref, attention._cfg, batch, len(pairs), cu, members, prefix,
-                                   self._ref, data), "share")
+                                   -1 if least is None else least, self._ref, data), "share")
         make(None)
         host = torch.empty(max(1, self.plan.ints), dtype=torch.int32)
         make(host.data_ptr())

@@ -201,7 +201,7 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
     auto vis_of = [&](int n, int p) {
         return visible<5>(min(n, most), first_of(n, p), sinks_of(p));
     };
-    auto prefix_of = [&](int b) { return Shared && b < a.batch ? a.shared_rows[b].prefix : 0; };
+    auto prefix_of = [&](int b) { return Shared && b < a.batch ? a.prefixes[b] : 0; };
     int sum = 0, longest = 0, n0 = 0, p0 = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
         const int b = b0 + lane;
@@ -252,84 +252,8 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
     return u;
 }
 
-// Joins a row group's own parts, as join_parts does, with those of its shared prefix.
-// (The prefix's were written by a launch before this one, by lanes that held 32x32
-// tiles of them: 16-byte piece (d / 8, row % 32, d / 4 % 2) of a wave's 32 rows.)
-template <class T, int D, int Threads, class Row, class Lse>
-__device__ __forceinline__ void join_with_prefix(const float *part, int64_t stride, int n_parts,
-                                                 int rows, const float *pre, int64_t pre_stride,
-                                                 int n_pre, int row0, float *mx, float *den,
-                                                 Row write, Lse write_lse) {
-    const int tid = threadIdx.x;
-    constexpr int kRows = 128, kWave = 32 * (D + 2);
-    auto slot_of = [&](int row, int u) {    // row: of the group
-        return pre + ((int64_t)(row / kRows) * n_pre + u) * pre_stride + (row % kRows >> 5) * kWave;
-    };
-    for (int row = tid >> 4; row < rows; row += Threads / 16) {
-        float m = kNoMax, l = 0.f;
-        const int at = 32 * D + ((row0 + row) & 31);
-        for (int u = tid & 15; u < n_parts; u += 16)
-            m = fmaxf(m, load_agent(part + u * stride + 16 * D + row));
-        for (int u = tid & 15; u < n_pre; u += 16) m = fmaxf(m, slot_of(row0 + row, u)[at]);
-#pragma unroll
-        for (int s = 8; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
-        for (int u = tid & 15; u < n_parts; u += 16) {
-            const float *p = part + u * stride + 16 * D;
-            l += load_agent(p + 16 + row) * exp2_(load_agent(p + row) - m);
-        }
-        for (int u = tid & 15; u < n_pre; u += 16) {
-            const float *p = slot_of(row0 + row, u) + at;
-            l += p[32] * exp2_(p[0] - m);
-        }
-#pragma unroll
-        for (int s = 8; s >= 1; s >>= 1) l += __shfl_xor(l, s);
-        if ((tid & 15) == 0) {
-            mx[row] = m;
-            den[row] = l;
-            write_lse(row, l != 0.f ? (m + log2_(l) - T::kOff) * kLn2 : -__builtin_inff());
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < rows * (D / 4); i += Threads) {
-        const int row = i / (D / 4), d = 4 * (i % (D / 4));
-        const float m = mx[row], l = den[row];
-        f32x4 sum = zero4();
-        for (int u = 0; u < n_parts; u += 8) {
-            f32x4 x[8];
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float *p = part + min(u + j, n_parts - 1) * stride;
-                x[j] = __builtin_bit_cast(f32x4, buf_ld16<true>(buf_rsrc(p), 4u * (row * D + d)));
-                f[j] = load_agent(p + 16 * D + row);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (u + j < n_parts) sum += x[j] * part_factor(f[j] - m);
-        }
-        const int at = 32 * D + ((row0 + row) & 31);
-        const int piece = 256 * (d >> 3) + 4 * (((row0 + row) & 31) + 8 * (d & 4));
-        for (int u = 0; u < n_pre; u += 8) {
-            f32x4 x[8];
-            float f[8], w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float *p = slot_of(row0 + row, min(u + j, n_pre - 1));
-                x[j] = ldf4(p + piece);
-                f[j] = p[at];
-                w[j] = p[at + 32];
-            }
-            // (A part that is empty for a row may have left no sums at all.)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (u + j < n_pre && w[j] != 0.f) sum += x[j] * part_factor(f[j] - m);
-        }
-        write(row, d, l != 0.f ? sum * (1.f / l) : zero4());
-    }
-}
-
-// Shared: of what is behind the sequences' shared prefixes, joined with the partial
-// results that a launch before this one left of those.
+// Shared: of what is behind the sequences' shared prefixes; those that have one are left
+// as partial results, for attn_shared.h to join.
 template <class T, bool F8, int D, bool Shared = false>
 __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArgs a) {
     typedef DecodeTile<T, F8, D> Tile;
@@ -344,9 +268,8 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
     const int hh = (int)blockIdx.x % heads, su = (int)blockIdx.x / heads;
     const DecodeUnit u = find_unit<Shared>(a, su);
     if (u.b < 0) return;
-    SharedRow pre = {0, 0, 0, 0};
-    if constexpr (Shared) pre = a.shared_rows[u.b];
-    const bool whole_row = u.parts == 1 && (!Shared || pre.prefix == 0);
+    const bool left = Shared && a.prefixes[u.b] > 0;
+    const bool whole_row = u.parts == 1 && !left;
     const int h = hh / a.head_groups, hg = hh % a.head_groups;
     const int head0 = h * a.group + 16 * hg;             // first query head of the columns
     const int n_heads = min(16, a.group - 16 * hg);
@@ -542,6 +465,11 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
         }
     }
     if (whole_row) return;
+    if (left) {
+        if (su == u.unit0 && threadIdx.x == 0)
+            a.shared_tails[(int64_t)u.b * heads + hh] = {u.unit0, u.parts};
+        return;
+    }
 
     // Arrival: this unit's stores are complete before it is counted.
     wait_vm_all();
@@ -552,17 +480,6 @@ __global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArg
     __syncthreads();
     if (s_last != (uint32_t)u.parts - 1) return;
     if (threadIdx.x == 0) store_agent(counter, 0u);
-    if constexpr (Shared) {
-        if (pre.prefix > 0) {
-            constexpr int64_t kPrefixSlot = 128 * (D + 2);
-            join_with_prefix<T, D, kDecodeThreads>(
-                a.part + ((int64_t)u.unit0 * heads + hh) * kSlot, kSlot * heads, u.parts, n_heads,
-                a.shared_part + ((int64_t)pre.slot * a.kv_heads + h) * kPrefixSlot,
-                kPrefixSlot * a.kv_heads, pre.parts, pre.member * a.group + 16 * hg, s_m[0], s_den,
-                write, write_lse);
-            return;
-        }
-    }
     join_parts<T, D, kDecodeThreads>(a.part + ((int64_t)u.unit0 * heads + hh) * kSlot,
                                      kSlot * heads, u.parts, n_heads, 16, s_m[0], s_den, write,
                                      write_lse);

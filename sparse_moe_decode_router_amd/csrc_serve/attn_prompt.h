@@ -191,22 +191,38 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
     Seq seq = {};
     int64_t chunk = 0, at = 0, x0 = 0, x1 = 0;
     SharedUnit su = {};
+    int rows_lo = 0x7FFFFFFF, rows_hi = -1, rows_seen = 0x7FFFFFFF;   // positions; of those that see any
     if constexpr (Shared) {
-        su = a.shared_units[unit];
-        // The prefix is read from the member that has most of it.
+        su = a.shared_units[blockIdx.x];
+        h = su.head;
+        // The prefix is read from the member that has most of it.  Every row has a position of
+        // its own; those of sequences that hold nothing see nothing, and widen no window.
+        const int first = su.row0 / a.group;
+        const int last = min(su.n_members, (su.row0 + kPromptRows - 1) / a.group + 1) - 1;
         int best = -1;
         for (int i0 = 0; i0 < su.n_members; i0 += 64) {
             const int i = i0 + lane;
             const int bb = a.members[su.members + min(i, su.n_members - 1)];
-            const int have = i < su.n_members ? min(max(a.lengths[bb], 0), su.prefix) : -1;
-            int top = have;
+            const int n = max(a.lengths[bb], 0);
+            const bool mine = i >= first && i <= last;
+            const int have = i < su.n_members ? min(n, su.prefix) : -1;
+            int top = have, lo = mine ? n - 1 : 0x7FFFFFFF, hi = mine ? n - 1 : -1;
+            int seen = mine && n > 0 ? n - 1 : 0x7FFFFFFF;
 #pragma unroll
-            for (int y = 32; y >= 1; y >>= 1) top = max(top, __shfl_xor(top, y));
+            for (int y = 32; y >= 1; y >>= 1) {
+                top = max(top, __shfl_xor(top, y));
+                lo = min(lo, __shfl_xor(lo, y));
+                hi = max(hi, __shfl_xor(hi, y));
+                seen = min(seen, __shfl_xor(seen, y));
+            }
             const int most_here = (int)uniform(top);
             if (most_here > best) {
                 best = most_here;
                 b = __builtin_amdgcn_readlane(bb, __builtin_ctzll(__ballot(have == top)));
             }
+            rows_lo = min(rows_lo, (int)uniform(lo));
+            rows_hi = max(rows_hi, (int)uniform(hi));
+            rows_seen = min(rows_seen, (int)uniform(seen));
         }
     } else if (a.units == 0) {
         // One row tile, or a part of one: unit = tile * split + part.
@@ -285,28 +301,10 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
         int pos_lo = past + row0 / a.group, pos_hi = past + (row0 + rows - 1) / a.group;
         Visible vis;
         if constexpr (Shared) {
-            // Every row has a position of its own; those of sequences that hold nothing
-            // see nothing, and widen no window.
-            int lo = 0x7FFFFFFF, lo_seen = 0x7FFFFFFF, hi = -1;
-#pragma unroll
-            for (int y = 0; y < kPromptRows; y += 64) {
-                const int r = row0 + min(y + lane, rows - 1);
-                const int p = max(a.lengths[a.members[su.members + r / a.group]], 0) - 1;
-                lo = min(lo, p);
-                lo_seen = p >= 0 ? min(lo_seen, p) : lo_seen;
-                hi = max(hi, p);
-            }
-#pragma unroll
-            for (int y = 32; y >= 1; y >>= 1) {
-                lo = min(lo, __shfl_xor(lo, y));
-                lo_seen = min(lo_seen, __shfl_xor(lo_seen, y));
-                hi = max(hi, __shfl_xor(hi, y));
-            }
-            pos_lo = (int)uniform(lo);
-            pos_hi = (int)uniform(hi);
-            lo_seen = (int)uniform(lo_seen);
+            pos_lo = rows_lo;
+            pos_hi = rows_hi;
             vis = visible<6>(max(0, min(n_seen, pos_hi + 1)),
-                             a.window > 0 && pos_hi >= 0 ? max(0, lo_seen - a.window + 1) : 0,
+                             a.window > 0 && pos_hi >= 0 ? max(0, rows_seen - a.window + 1) : 0,
                              a.sinks);
         } else {
             vis = visible_of(seq, row0);

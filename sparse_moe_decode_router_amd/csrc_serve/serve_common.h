@@ -84,15 +84,14 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 __device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
 
 // Rows of queries that meet the keys of a shared prefix: a group's members, one after the
-// other, with the query heads of a kv head.  One workgroup (per kv head) takes 128 rows
-// from row0 on and part `part` of `parts` of the prefix, and writes slot `slot`.
+// other, with the query heads of kv head `head`.  One workgroup takes 128 rows from row0
+// on and part `part` of `parts` of the prefix, and writes slot `slot` of that head.
 struct SharedUnit {
-    int32_t members, n_members, prefix, row0, part, parts, slot, pad;
+    int32_t members, n_members, prefix, row0, part, parts, slot, head;
 };
-// A sequence's own: the prefix (0: none), its group's first slot, the parts, and its
-// place among the members.
-struct SharedRow {
-    int32_t prefix, slot, parts, member;
+// A sequence's own: its first unit behind the prefix, and how many there are.
+struct SharedTail {
+    int32_t unit0, parts;
 };
 
 // The arguments of both attention kernels.
@@ -115,10 +114,11 @@ struct AttnArgs {
     int32_t row_tiles;         // prompt: most of them that there are counters for
     // Shared prefixes: what each workgroup (per kv head) takes, each sequence's part of
     // it, the groups' members, and the partial results.
-    const SharedUnit *shared_units;
-    const SharedRow *shared_rows;
+    const SharedUnit *shared_units, *shared_tiles;   // (tiles: those of part 0)
+    const int32_t *prefixes;       // by sequence, 0: none
     const int32_t *members;
     float *shared_part;
+    SharedTail *shared_tails;      // [batch][kv_heads * head_groups], of those with a prefix
 };
 
 // Blocks of 2^L keys that a row at the last position of n sees: the first

@@ -1,16 +1,17 @@
 // shared.hip - host side of decode over shared prefixes: the plan, argument checks, and
 // their part of the C ABI declared in include/moe_serve.h.
 //
-// Two launches.  The first multiplies the queries of all members of a group with the
+// Three launches.  The first multiplies the queries of all members of a group with the
 // keys of their prefix, as prompts do: the rows (member, query head) of a kv head are
 // taken 128 at a time, and the prefix in as many parts as fill the chip once.  The
-// second is decode over what each sequence has behind the prefix, and joins its
-// partial results with the first one's.  Prefix keys are read once for 128 rows instead
-// of once for each member.
+// second is decode over what each sequence has behind the prefix.  The third joins the
+// partial results of both.  Prefix keys are read once for 128 rows instead of once for
+// each member.
 #include "serve_host.h"
 
 #include "attn_decode.h"
 #include "attn_prompt.h"
+#include "attn_shared.h"
 
 using namespace moe::serve;
 
@@ -18,10 +19,23 @@ namespace {
 
 // The fewest tiles of 64 keys that a workgroup takes, and the most parts of a prefix: every
 // part is read again by the join.
-constexpr int kSharedTiles = 4, kSharedParts = 64;
+constexpr int kSharedTiles = 4, kSharedParts = 128;
+// Bytes of keys and values that reading prefixes apart has to spare: three launches instead of
+// one cost some 12 us, in which a prefix that is read again comes from the caches.  Decode of
+// each sequence by itself, and shared, us, 7 heads on each kv head: 59 MB (8 of 8192, 2 kv
+// heads) 16 and 25; 117 MB (8 of 16384, 2) 21 and 26; 126 MB (16 of 4096, 8, e4m3) 23 and
+// 24; 132 MB (64 of 512, 8) 17 and 25; 264 MB (64 of 1024, 8) 26 and 25; 235 MB (8 of 8192, 4
+// heads of 256 on 4 each) 39 and 35.
+constexpr int64_t kSharedLeast = 200000000;
+// Units behind the prefixes that a call aims at, for each compute unit: tails are short, and
+// a sequence's is best taken by one workgroup (64 tails of up to 512, 56 heads on 8: 1, 2
+// and 4 a compute unit 63.0, 63.6 and 64.7 us; up to 1000 in e4m3: 100, 104, 107).
 
 size_t prefix_floats(const moe_attn_shared &p) {
     return (size_t)kPromptRows * (p.head_dim + 2) * p.slots * p.kv_heads;
+}
+int head_groups(const moe_kv_cache &kv, const moe_attn_config &c) {
+    return (c.q_heads / kv.kv_heads + 15) / 16;
 }
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
@@ -31,7 +45,8 @@ extern "C" {
 
 moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *c, int32_t batch,
                           int32_t groups, const int32_t *cu, const int32_t *members,
-                          const int32_t *prefix, moe_attn_shared *plan, int32_t *data) {
+                          const int32_t *prefix, int64_t least, moe_attn_shared *plan,
+                          int32_t *data) {
     const moe_status s = moe_attn_validate(kv, c);
     if (s != MOE_OK) return s;
     if (!plan || batch < 1 || batch > c->batch || groups < 0 || groups > batch ||
@@ -50,9 +65,17 @@ moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *c, int3
         if (members[i] < 0 || members[i] >= batch) return MOE_ERR_INVALID_ARG;
     // A prefix that is read apart: one that several share, and that holds all sinks (those
     // behind it would be seen beside a window that is behind them).
+    bool worth = true;
     auto apart = [&](int g) {
-        return cu[g + 1] - cu[g] > 1 && prefix[g] > 0 && (c->window == 0 || c->sinks <= prefix[g]);
+        return worth && cu[g + 1] - cu[g] > 1 && prefix[g] > 0 &&
+               (c->window == 0 || c->sinks <= prefix[g]);
     };
+    double spared = 0.0;
+    for (int g = 0; g < groups; ++g)
+        if (apart(g))
+            spared += (double)(cu[g + 1] - cu[g] - 1) * std::min<int64_t>(prefix[g], most) *
+                      (plane_bytes(*kv) / kv->pages / kv->page) * 2;
+    worth = spared >= (double)(least < 0 ? kSharedLeast : least);
     auto tiles_of = [&](int g) { return ((cu[g + 1] - cu[g]) * group + kPromptRows - 1) / kPromptRows; };
     auto keys_of = [&](int g) {
         return (std::min<int64_t>(prefix[g], most) + kPromptKeys - 1) / kPromptKeys;
@@ -78,48 +101,64 @@ moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *c, int3
         else lo = mid;
     }
     const int64_t share = hi, units = units_with(share);
-    if (units * kv->kv_heads > kMaxGrid256) return MOE_ERR_UNSUPPORTED;
-    // The longest that is left for each sequence by itself.
-    int64_t least = total == batch && groups ? most : 0;
+    int64_t tiles = 0;
+    int parts = 0;       // most of a group's
     for (int g = 0; g < groups; ++g)
-        if (cu[g + 1] > cu[g]) least = std::min<int64_t>(least, apart(g) ? prefix[g] : 0);
+        if (apart(g)) {
+            tiles += tiles_of(g);
+            parts = std::max(parts, (int)parts_of(g, share));
+        }
+    if (units * kv->kv_heads > kMaxGrid256 ||
+        tiles * (kv->head_dim / 8) * kv->kv_heads > kMaxGrid256)
+        return MOE_ERR_UNSUPPORTED;
+    // The longest that is left for each sequence by itself.
+    int64_t shortest = total == batch && groups ? most : 0;
+    for (int g = 0; g < groups; ++g)
+        if (cu[g + 1] > cu[g]) shortest = std::min<int64_t>(shortest, apart(g) ? prefix[g] : 0);
     *plan = {};
     plan->batch = batch;
     plan->q_heads = c->q_heads;
     plan->kv_heads = kv->kv_heads;
     plan->head_dim = kv->head_dim;
-    plan->units = (int32_t)units;
+    plan->units = (int32_t)(units * kv->kv_heads);
     plan->slots = (int32_t)units;
     plan->members = (int32_t)total;
     plan->window = c->window;
     plan->sinks = c->sinks;
-    plan->tail = (int32_t)std::max<int64_t>(1, c->longest - least);
-    plan->ints = 8 * units + 4 * (int64_t)batch + total;
+    plan->tiles = (int32_t)tiles;
+    plan->parts = parts;
+    plan->tail = (int32_t)std::max<int64_t>(1, c->longest - shortest);
+    plan->ints = 8 * (plan->units + tiles) + batch + total;
     if (!data) return MOE_OK;
-    SharedUnit *unit = (SharedUnit *)data;
-    SharedRow *rows = (SharedRow *)(data + 8 * units);
-    for (int b = 0; b < batch; ++b) rows[b] = {0, 0, 0, -1};
+    SharedUnit *unit = (SharedUnit *)data, *tile = unit + plan->units;
+    int32_t *prefixes = (int32_t *)(tile + tiles);
+    std::fill(prefixes, prefixes + batch, -1);
     int64_t at = 0;
     for (int g = 0; g < groups; ++g) {
         const int n = cu[g + 1] - cu[g];
-        const bool is = apart(g);
-        const int parts = (int)parts_of(g, share);
-        for (int i = 0; i < n; ++i) {
-            SharedRow &r = rows[members[cu[g] + i]];
-            if (r.member >= 0) return MOE_ERR_INVALID_ARG;   // named twice
-            r = is ? SharedRow{prefix[g], (int32_t)at, parts, i} : SharedRow{0, 0, 0, i};
+        for (int i = cu[g]; i < cu[g + 1]; ++i) {
+            int32_t &p = prefixes[members[i]];
+            if (p >= 0) return MOE_ERR_INVALID_ARG;   // named twice
+            p = apart(g) ? prefix[g] : 0;
         }
-        if (!is) continue;
-        // All row tiles of a part are neighbours: they read the same keys.
-        const int tiles = (int)tiles_of(g);
-        for (int part = 0; part < parts; ++part)
-            for (int t = 0; t < tiles; ++t)
-                unit[at + part * tiles + t] = {cu[g], n, prefix[g], t * kPromptRows, part, parts,
-                                               (int32_t)at + t * parts + part, 0};
-        at += (int64_t)tiles * parts;
+        if (!apart(g)) continue;
+        // All row tiles of a part and head read the same keys: workgroups go round the eight
+        // XCDs, so they are eight apart, on one of them.
+        const int its = (int)tiles_of(g), parts = (int)parts_of(g, share);
+        const int streams = parts * kv->kv_heads;
+        auto make = [&](int t, int part, int head) {
+            return SharedUnit{cu[g], n, prefix[g], t * kPromptRows, part, parts,
+                              (int32_t)at + t * parts + part, head};
+        };
+        for (int s0 = 0; s0 < streams; s0 += 8)
+            for (int t = 0; t < its; ++t)
+                for (int y = s0; y < std::min(s0 + 8, streams); ++y)
+                    *unit++ = make(t, y / kv->kv_heads, y % kv->kv_heads);
+        for (int t = 0; t < its; ++t) *tile++ = make(t, 0, 0);
+        at += (int64_t)its * parts;
     }
-    for (int b = 0; b < batch; ++b) rows[b].member = std::max(rows[b].member, 0);
-    std::copy(members, members + total, data + 8 * units + 4 * (int64_t)batch);
+    for (int b = 0; b < batch; ++b) prefixes[b] = std::max(prefixes[b], 0);
+    std::copy(members, members + total, prefixes + batch);
     return MOE_OK;
 }
 
@@ -129,9 +168,10 @@ moe_status moe_attn_shared_workspace(const moe_kv_cache *kv, const moe_attn_conf
     const moe_status s = moe_attn_workspace(kv, c, 0, workspace, counters);
     if (s != MOE_OK) return s;
     if (!plan || plan->q_heads != c->q_heads || plan->kv_heads != kv->kv_heads ||
-        plan->head_dim != kv->head_dim || plan->slots < 0)
+        plan->head_dim != kv->head_dim || plan->slots < 0 || plan->batch < 1)
         return MOE_ERR_INVALID_ARG;
-    *workspace = round16(*workspace) + sizeof(float) * prefix_floats(*plan);
+    *workspace = round16(*workspace) + sizeof(float) * prefix_floats(*plan) +
+                 sizeof(SharedTail) * plan->batch * kv->kv_heads * head_groups(*kv, *c);
     return MOE_OK;
 }
 
@@ -146,15 +186,19 @@ moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config 
     if (s != MOE_OK) return s;
     if (!plan->data || !aligned(plan->data, 16) || plan->q_heads != c->q_heads ||
         plan->kv_heads != kv->kv_heads || plan->head_dim != kv->head_dim ||
-        plan->window != c->window || plan->sinks != c->sinks || plan->units < 0)
+        plan->window != c->window || plan->sinks != c->sinks || plan->units < 0 || plan->tiles < 0)
         return MOE_ERR_INVALID_ARG;
+    // Nothing is read apart: as any decode.
+    if (plan->units == 0)
+        return moe_attn_decode(kv, c, layer, q, dtype, token_stride, head_stride, plan->batch, out,
+                               lse, workspace, counters, stream);
     size_t decode_bytes, counter_bytes;
     if ((s = moe_attn_workspace(kv, c, 0, &decode_bytes, &counter_bytes)) != MOE_OK) return s;
     if (!workspace || !counters) return MOE_ERR_WORKSPACE;
     AttnArgs a = attn_args(*kv, *c, layer);
-    a.split = decode_split(*kv, *c, plan->tail);
+    a.split = std::max(1, std::min(decode_split(*kv, *c, plan->tail), kPlanCus / (a.kv_heads * a.head_groups)));
     const int64_t grid = ((int64_t)a.split + plan->batch) * a.kv_heads * a.head_groups;
-    const int64_t first = (int64_t)plan->units * kv->kv_heads;
+    const int64_t first = plan->units;
     if (grid > kMaxGrid256 || first > kMaxGrid256) return MOE_ERR_UNSUPPORTED;
     int cus;
     if ((s = compute_units(&cus)) != MOE_OK) return s;
@@ -167,20 +211,27 @@ moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config 
     a.shared_part = (float *)((char *)workspace + round16(decode_bytes));
     a.counters = counters;
     a.batch = plan->batch;
+    a.shared_tails = (SharedTail *)(a.shared_part + prefix_floats(*plan));
     a.shared_units = (const SharedUnit *)plan->data;
-    a.shared_rows = (const SharedRow *)(plan->data + 8 * (int64_t)plan->units);
-    a.members = plan->data + 8 * (int64_t)plan->units + 4 * (int64_t)plan->batch;
+    a.shared_tiles = a.shared_units + plan->units;
+    a.prefixes = (const int32_t *)(a.shared_tiles + plan->tiles);
+    a.members = a.prefixes + plan->batch;
     return with_types(dtype, kv->dtype == MOE_E4M3, [&](auto t, auto f8) {
         return with_dim(kv->head_dim, [&](auto d) {
             typedef decltype(t) T;
             constexpr bool kF8 = decltype(f8)::value;
             constexpr int D = decltype(d)::value;
-            if (first) {
-                k_attn_prompt<T, kF8, D, true><<<(int)first, kPromptThreads, 0, stream>>>(a);
-                const moe_status r = launched();
-                if (r != MOE_OK) return r;
-            }
+            k_attn_prompt<T, kF8, D, true><<<(int)first, kPromptThreads, 0, stream>>>(a);
+            moe_status r = launched();
+            if (r != MOE_OK) return r;
             k_attn_decode<T, kF8, D, true><<<(int)grid, kDecodeThreads, 0, stream>>>(a);
+            if ((r = launched()) != MOE_OK) return r;
+            const int64_t join = (int64_t)plan->tiles * 4 * (D / 32) * kv->kv_heads;
+            // Up to 32 parts are two rounds of loads; more are taken by four times the waves.
+            if (plan->parts <= 32)
+                k_attn_join<T, kF8, D, 1><<<(int)join, kJoinThreads, 0, stream>>>(a);
+            else
+                k_attn_join<T, kF8, D, 4><<<(int)join, 4 * kJoinThreads, 0, stream>>>(a);
             return launched();
         });
     });

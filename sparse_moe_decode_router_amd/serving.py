@@ -56,8 +56,8 @@ class SharedPlan(ctypes.Structure):
     """moe_attn_shared"""
     _fields_ = [("data", ctypes.c_void_p), ("ints", ctypes.c_int64)] + \
                [(n, ctypes.c_int32) for n in
-                ("batch", "q_heads", "kv_heads", "head_dim", "units", "slots", "members", "window",
-                 "sinks", "tail")]
+                ("batch", "q_heads", "kv_heads", "head_dim", "units", "tiles", "slots", "parts",
+                 "members", "window", "sinks", "tail")]
 
 
 class SamplingStruct(ctypes.Structure):
@@ -96,7 +96,7 @@ def lib() -> ctypes.CDLL:
         "moe_serve_last_hip_error": [],
         "moe_kv_append_rotated": [vp, i32, vp, vp, i64, i64, i32, vp, vp, i32, i64, i64, i32, vp,
                                   i32, vp, vp, vp],
-        "moe_attn_share": [vp, vp, i32, i32, vp, vp, vp, vp, vp],
+        "moe_attn_share": [vp, vp, i32, i32, vp, vp, vp, i64, vp, vp],
         "moe_attn_shared_workspace": [vp, vp, vp] + sizes,
         "moe_attn_decode_shared": [vp, vp, vp, i32, vp, i32, i64, i64, vp, vp, vp, vp, vp],
         "moe_sample_workspace": [i32, i32] + sizes,

@@ -44,7 +44,7 @@ def test_rotated_append_refuses_arguments(kw, want):
     assert status("moe_kv_append_rotated", *{**args, **kw}.values()) == want
 
 
-def plan(c, cfg, groups, prefix, batch):
+def plan(c, cfg, groups, prefix, batch, least=0):
     """(status, plan, its data as an array)"""
     cu = [0]
     for g in groups:
@@ -52,7 +52,7 @@ def plan(c, cfg, groups, prefix, batch):
     arr = lambda v: (ctypes.c_int32 * max(1, len(v)))(*v)  # noqa: E731
     p = serving.SharedPlan()
     args = (ctypes.addressof(c), ctypes.addressof(cfg), batch, len(groups), arr(cu),
-            arr([m for g in groups for m in g]), arr(prefix), ctypes.addressof(p))
+            arr([m for g in groups for m in g]), arr(prefix), least, ctypes.addressof(p))
     s = status("moe_attn_share", *args, None)
     if s:
         return s, p, None
@@ -85,34 +85,33 @@ def test_a_plan_takes_every_row_and_key_once(heads, kv_heads, dim, groups, membe
     lists = [order[g * members:(g + 1) * members] for g in range(groups)]
     prefixes = [prefix - g for g in range(groups)] if prefix > groups else [prefix] * groups
     s, p, data = plan(c, cfg, lists, prefixes, n)
-    assert s == 0 and p.ints == len(data) and p.slots == p.units
-    units, rows = data[:8 * p.units].reshape(-1, 8), data[8 * p.units:8 * p.units + 4 * n].reshape(n, 4)
-    flat = data[8 * p.units + 4 * n:]
+    assert s == 0 and p.ints == len(data) and p.slots * kv_heads == p.units
+    units, tiles = (data[8 * i:8 * j].reshape(-1, 8) for i, j in
+                    ((0, p.units), (p.units, p.units + p.tiles)))
+    own, flat = data[8 * (p.units + p.tiles):][:n], data[8 * (p.units + p.tiles) + n:]
     assert flat.tolist() == order
-    assert sorted(units[:, 6].tolist()) == list(range(p.units))      # slots
+    assert sorted(units[:, [6, 7]].tolist()) == [[i, h] for i in range(p.slots) for h in range(kv_heads)]
     group = heads // kv_heads
     slots = {}
-    for first, count, pre, row0, part, parts, slot, _ in units.tolist():
-        assert 0 <= part < parts <= 64 and row0 % 128 == 0 and row0 < count * group
-        slots[(first, row0, part)] = slot
-    used = 0
+    for first, count, pre, row0, part, parts, slot, head in units.tolist():
+        assert 0 <= part < parts <= 128 and row0 % 128 == 0 and row0 < count * group
+        assert slots.setdefault((first, row0, part), slot) == slot
+    used, tile = 0, 0
     for g, members_of in enumerate(lists):
         apart = len(members_of) > 1 and prefixes[g] > 0 and (window == 0 or sinks <= prefixes[g])
-        for i, m in enumerate(members_of):
-            pre, slot, parts, member = rows[m].tolist()
-            assert member == i and pre == (prefixes[g] if apart else 0)
-            for row in range(i * group, (i + 1) * group) if apart else ():
-                for part in range(parts):
-                    assert slots[(g * members, row // 128 * 128, part)] == \
-                        slot + row // 128 * parts + part
-        if apart:
-            used += -(-len(members_of) * group // 128) * rows[members_of[0]][2]
-    assert used == p.units
+        assert all(own[m] == (prefixes[g] if apart else 0) for m in members_of)
+        for row0 in range(0, len(members_of) * group, 128) if apart else ():
+            first, count, pre, at, part, parts, slot, _ = tiles[tile].tolist()
+            assert (first, count, pre, at, part) == (g * members, members, prefixes[g], row0, 0)
+            assert [slots[(first, row0, i)] for i in range(parts)] == list(range(slot, slot + parts))
+            tile, used = tile + 1, used + parts
+    assert tile == p.tiles
+    assert used == p.slots
     assert 1 <= p.tail <= 40000
     # one round of workgroups where that is possible, never more than four
     at_once = 512 if dim <= 128 else 256
     least = sum(-(-len(g) * group // 128) for g in lists)
-    assert p.units * kv_heads <= max(4 * at_once, least * kv_heads)
+    assert p.units <= max(4 * at_once, least * kv_heads)
 
 
 def test_shared_calls_refuse():

@@ -206,7 +206,7 @@ def test_decode_shared(case):
     q = randn((b, kvh * group, dim), dtype, 12)
     att = attention.PagedAttention(cache.gpu(), kvh * group, b, max(max(lengths), 1), window=window,
                                    sinks=sinks)
-    plan = att.share(groups, prefix)
+    plan = att.share(groups, prefix, least=0)
     dense = su.attention_dense if max(lengths) > 400 else su.attention
     want = dense(cache, 0, q, list(range(b + 1)), window, sinks)
     qd = q.cuda()
@@ -222,7 +222,7 @@ def test_members_grow_and_are_freed_under_one_plan():
                             spare_cols=6)
     kv = cache.gpu()
     att = attention.PagedAttention(kv, 6, 3, 300)
-    plan = att.share([[0, 1, 2]], [160])
+    plan = att.share([[0, 1, 2]], [160], least=0)
     q = randn((3, 6, 64), BF, 14).cuda()
 
     def same():
@@ -247,6 +247,20 @@ def test_members_grow_and_are_freed_under_one_plan():
     same()
 
 
+def test_little_to_spare_is_decoded_one_by_one():
+    """Below 200 MB the plan is decode() itself; with `least` the prefix is read apart."""
+    cache = gu.shared_cache([[0, 1, 2]], [160], [170, 161, 200], 2, 16, 64, BF, seed=13)
+    att = attention.PagedAttention(cache.gpu(), 6, 3, 300)
+    q = randn((3, 6, 64), BF, 14).cuda()
+    plan = att.share([[0, 1, 2]], [160])
+    spared = 2 * 160 * 2 * 2 * 64 * 2
+    assert plan.plan.units == 0 and att.share([[0, 1, 2]], [160], least=spared + 1).plan.units == 0
+    assert att.share([[0, 1, 2]], [160], least=spared).plan.units > 0
+    got, want = att.decode_shared(0, q, plan), att.decode(0, q)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_visible_infinities_of_a_prefix():
     cache = gu.shared_cache([[0, 1]], [96], [100, 130], 1, 16, 64, BF, seed=16)
     page = int(cache.tables[0, 1])
@@ -254,7 +268,7 @@ def test_visible_infinities_of_a_prefix():
     cache.data[0, 1, page, 0, 5, 9], cache.data[0, 1, page, 0, 6, 9] = math.inf, -math.inf
     att = attention.PagedAttention(cache.gpu(), 2, 2, 130)
     q = randn((2, 2, 64), BF, 17).cuda()
-    out = att.decode_shared(0, q, att.share([[0, 1]], [96]))[0].cpu()
+    out = att.decode_shared(0, q, att.share([[0, 1]], [96], least=0))[0].cpu()
     assert torch.all(out[..., 5] == math.inf) and torch.all(out[..., 7] == -math.inf)
     assert out[..., 9].isnan().all()
     out[..., [5, 7, 9]] = 0
@@ -267,7 +281,7 @@ def test_shared_streams_and_graph():
                             spare=20, spare_cols=4)
     kv = cache.gpu()
     att = attention.PagedAttention(kv, 14, 3, 2200)
-    plan = att.share([[0, 1, 2]], [2000])
+    plan = att.share([[0, 1, 2]], [2000], least=0)
     qs = [randn((3, 14, 128), BF, 19 + i).cuda() for i in range(2)]
     want = [att.decode_shared(0, q, plan) for q in qs]
     torch.cuda.synchronize()
@@ -468,7 +482,8 @@ def test_refusals_on_the_gpu():
                 lambda: att.decode_shared(0, q, None), lambda: att.share([[0, 2]], [16]),
                 lambda: att.share([[0, 1], [1]], [16, 16]), lambda: att.share([[0, 1]], []),
                 lambda: att.share([[0, 1]], [-1]), lambda: att.share([[0]], [1], batch=3),
-                lambda: att.share([[0, 1]], [16.0]),
+                lambda: att.share([[0, 1]], [16.0]), lambda: att.share([[0, 1]], [16], least=-1),
+                lambda: att.share([[0, 1]], [16], least=1.5),
                 lambda: kv.append_rotated(0, q, k, k.half(), turn),
                 lambda: kv.append_rotated(0, q[:1], k, k, turn),
                 lambda: kv.append_rotated(0, q.half(), k, k, turn),
