@@ -468,6 +468,92 @@ def test_sample_streams_and_graph():
         gu.check_sample(got, y, v, top_p=0.9)
 
 
+def test_a_captured_step_of_all():
+    """Rotated append, shared decode and sampling in one graph; replays follow lengths,
+    tokens and uniform numbers, with eager calls of the same plans in between."""
+    cache = gu.shared_cache([[0, 1, 2]], [320], [330, 321, 340], 2, 16, 64, BF, seed=60, spare=20,
+                            spare_cols=4, clean=True)
+    kv = cache.gpu()
+    kv.extend(ints(1, 1, 1))
+    att = attention.PagedAttention(kv, 8, 3, 400)
+    plan = att.share([[0, 1, 2]], [320], least=0)
+    turn = rotary.Rotary(rotary.frequencies(64))
+    sampler = sampling.Sampler(3, 512)
+    g = torch.Generator().manual_seed(61)
+    y = torch.randn((3, 12, 64), generator=g).to(BF).cuda()
+    u = torch.rand(3, generator=g).cuda()
+
+    def step():
+        q = kv.append_rotated(0, y[:, :8], y[:, 8:10], y[:, 10:], turn)
+        out, lse = att.decode_shared(0, q, plan)
+        return (q, out, lse) + sampler(out.flatten(1).float(), u, top_k=40, top_p=0.9)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for i in range(4):
+        y.copy_(torch.randn((3, 12, 64), generator=g).to(BF))
+        u.copy_(torch.rand(3, generator=g))
+        if i:
+            kv.extend(ints(1, 1, 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in held]
+        eager = step()
+        torch.cuda.synchronize()
+        for a, b in zip(got, eager):
+            assert torch.equal(a, b) and not a.isnan().any()
+
+
+@pytest.mark.parametrize("cdtype", [BF, E4], ids=str)
+def test_continuations_of_prompts(cdtype):
+    """From prompts to sampled continuations through all the operators: without a
+    temperature all continuations of a prompt are the same one; with one they differ,
+    and sharing the prompts or not makes no difference but rounding."""
+    from sparse_moe_decode_router_amd import binding, serve_layer, synth
+    moe = binding.DeviceLayer(synth.make_layer(synth.TINY, 0), device="cuda:0")
+
+    def layer():
+        one = serve_layer.ServeLayer(moe, cache=cdtype, seqs=6, vocab=500,
+                                     rotary=rotary.Rotary(rotary.frequencies(128)))
+        one.moe.set_mode(binding.MODE_ORDERED)   # (rows of equal tokens give equal sums)
+        return one
+
+    kw = dict(steps=4, prompts=(70, 33), continuations=3, vocab=500)
+    made, tokens, drawn, us = serve_layer.generate(layer=layer(), least=0, temperature=0, **kw)
+    assert tokens.shape == drawn.shape == (2, 3, 4) and us > 0
+    assert torch.equal(tokens, tokens[:, :1].expand_as(tokens)) and torch.all(drawn == 0)
+    assert made.kv.lengths.tolist() == [73, 36, 73, 73, 36, 36]
+    made.close()
+    made, tokens, drawn, _ = serve_layer.generate(layer=layer(), least=0, temperature=1.5, **kw)
+    assert torch.all((tokens >= 0) & (tokens < 500)) and torch.all(drawn <= 0)
+    assert not torch.equal(tokens, tokens[:, :1].expand_as(tokens))
+    # one more step, shared and not: the same but for the weights' rounding
+    kv = made.kv
+    kv.extend(ints(*[1] * 6))
+    x = torch.randn((6, moe.dims.hidden), generator=torch.Generator().manual_seed(62)).to(BF).cuda()
+    plan = made.attention.share([[0, 2, 3], [1, 4, 5]], [70, 33], least=0)
+    y = made.qkv(x).unflatten(1, (-1, 128))
+    q = kv.append_rotated(0, y[:, :14], y[:, 14:16], y[:, 16:], made.rotary)
+    a, b = made.attention.decode_shared(0, q, plan), made.attention.decode(0, q)
+    scale = 1.0 if kv.v_scale is None else float(kv.v_scale.max())
+    # twice the outputs' own rounding, and half a step of every weight
+    assert float((a[0].float() - b[0].float()).abs().max()) <= \
+        3 * 2.0 ** -8 * scale * float(kv.data[0, 1].float().abs().max())
+    assert torch.allclose(a[1], b[1], rtol=1e-5, atol=1e-4)
+    made.close()
+
+
+def test_the_example_samples():
+    from sparse_moe_decode_router_amd import serve_layer
+    layer, tokens, drawn, us = serve_layer.generate(steps=3, continuations=2, temperature=0.8,
+                                                    top_p=0.95)
+    assert tokens.shape == (4, 2, 3) and drawn.isfinite().all() and us > 0
+    layer.close()
+
+
 def test_refusals_on_the_gpu():
     kv = su.HostCache([20, 30], 2, 16, 64, BF, seed=23).gpu()
     att = attention.PagedAttention(kv, 4, 2, 64)
