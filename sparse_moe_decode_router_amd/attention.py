@@ -174,14 +174,18 @@ class PagedKV:
                 return self.append_rotated(layer, q, k, v, rotary, cu, only_granted, out)
         dim, dev = self.head_dim, self.device
         ts, hs = _rows(k, "k", self.kv_heads, dim, self.compute_dtypes, dev)
-        if _rows(v, "v", self.kv_heads, dim, (k.dtype,), dev) != (ts, hs) or v.shape != k.shape:
-            raise MoEError("v: the shape and strides of k are needed")
+        dtype, v_at = k.dtype, v.data_ptr() if isinstance(v, torch.Tensor) else 1
+        # (What is as k is needs no checks of its own.)
+        if v_at % 16 or v.dtype != dtype or v.shape != k.shape or v.stride() != k.stride() or \
+                v.device != dev:
+            if _rows(v, "v", self.kv_heads, dim, (dtype,), dev) != (ts, hs) or v.shape != k.shape:
+                raise MoEError("v: the shape and strides of k are needed")
         if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[1] < 1:
             raise MoEError(f"q: a tensor of shape (tokens, q_heads, {dim}) is needed")
-        q_heads, tokens = q.shape[1], k.shape[0]
-        qts, qhs = _rows(q, "q", q_heads, dim, (k.dtype,), dev)
-        if q.shape[0] != tokens:
-            raise MoEError(f"q: {q.shape[0]} tokens, and {tokens} keys")
+        tokens, q_heads, _ = q.shape
+        qts, qhs = _rows(q, "q", q_heads, dim, (dtype,), dev)
+        if k.shape[0] != tokens:
+            raise MoEError(f"q: {tokens} tokens, and {k.shape[0]} keys")
         if cu is None:
             batch = tokens
             if batch > self.seqs:
@@ -198,13 +202,13 @@ class PagedKV:
             raise MoEError(f"rotary: on {rotary.device}, up to dimension {rotary.last}; heads are "
                            f"on {dev} and of {dim}")
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            out = torch.empty(q.shape, dtype=dtype, device=dev)
         else:
-            tensor(out, "out", q.dtype, q.shape, dev)
+            tensor(out, "out", dtype, q.shape, dev)
             require(out.data_ptr() % 16 == 0, "out: 16-byte alignment is needed")
         check(self._lib.moe_kv_append_rotated(
-            self._ref, layer, rotary._ref, q.data_ptr(), qts, qhs, q_heads, k.data_ptr(),
-            v.data_ptr(), DTYPES[k.dtype], ts, hs, tokens, None if cu is None else cu.data_ptr(),
+            self._ref, layer, rotary._ref, q.data_ptr(), qts, qhs, q_heads, k.data_ptr(), v_at,
+            DTYPES[dtype], ts, hs, tokens, None if cu is None else cu.data_ptr(),
             batch, self._granted_ptr if only_granted else None, out.data_ptr(),
             raw_stream(self._index)), "append_rotated")
         return out
