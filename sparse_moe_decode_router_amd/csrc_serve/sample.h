@@ -243,6 +243,24 @@ __device__ __forceinline__ int wave_scan_i(int v) {
     v = add_dpp_i<0x142, 0xA>(v);
     return add_dpp_i<0x143, 0xC>(v);
 }
+// Scans of K values side by side: each step waits for the one before it.
+template <int C, int Rows, int K>
+__device__ __forceinline__ void add_dpp_all(int *n, double *v) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        n[k] = add_dpp_i<C, Rows>(n[k]);
+        v[k] = add_dpp<C, Rows>(v[k]);
+    }
+}
+template <int K>
+__device__ __forceinline__ void wave_scan_all(int *n, double *v) {
+    add_dpp_all<0x111, 0xF, K>(n, v);
+    add_dpp_all<0x112, 0xF, K>(n, v);
+    add_dpp_all<0x114, 0xF, K>(n, v);
+    add_dpp_all<0x118, 0xF, K>(n, v);
+    add_dpp_all<0x142, 0xA, K>(n, v);
+    add_dpp_all<0x143, 0xC, K>(n, v);
+}
 __device__ __forceinline__ double lane_d(double v, int lane) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane);
@@ -385,39 +403,33 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
     // A wave has bins next to each other, an octave at a time.
     const int r0 = kMine * 64 * wave_index() + lane;
     if (own < 3) s_bin[own].bin = kSampleBins - 1;
-    uint64_t sum_count[kMine] = {}, sum_mass[kMine] = {};
-    // Several slices' loads on their way at once: each takes more than a microsecond.
-    constexpr int kAtOnce = 3;
+    // Counts and weights of all slices fit into such integers too: a row has 2^19 values.
+    uint64_t sum[kMine] = {};
     if (a.slices_n == 1) {
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-            const uint64_t v = own_hist[r0 + 64 * j];
-            sum_count[j] = v >> 44;
-            sum_mass[j] = v & ((1ull << 44) - 1);
-        }
+        for (int j = 0; j < kMine; ++j) sum[j] = own_hist[r0 + 64 * j];
     } else {
+        // Several slices' loads on their way at once: each takes more than a microsecond.
+        constexpr int kAtOnce = 5;
+#pragma unroll 1
         for (int s0 = 0; s0 < a.slices_n; s0 += kAtOnce) {
             uint64_t v[kAtOnce][kMine];
+            int off[kAtOnce];
 #pragma unroll
             for (int y = 0; y < kAtOnce; ++y) {
-                const int sl = min(s0 + y, a.slices_n - 1), off = __builtin_amdgcn_readlane(by, sl);
+                // (Behind the last slice the last one again, for nothing.)
+                const int sl = min(s0 + y, a.slices_n - 1);
+                off[y] = s0 + y < a.slices_n ? __builtin_amdgcn_readlane(by, sl) : kSampleBins;
                 const uint64_t *hist = a.hist + ((int64_t)row * a.slices_n + sl) * kSampleBins;
 #pragma unroll
                 for (int j = 0; j < kMine; ++j)
-                    v[y][j] = __hip_atomic_load(hist + max_i(r0 + 64 * j - off, 0),
+                    v[y][j] = __hip_atomic_load(hist + max_i(r0 + 64 * j - off[y], 0),
                                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
 #pragma unroll
-            for (int y = 0; y < kAtOnce; ++y) {
-                const int off =
-                    s0 + y < a.slices_n ? __builtin_amdgcn_readlane(by, s0 + y) : kSampleBins;
+            for (int y = 0; y < kAtOnce; ++y)
 #pragma unroll
-                for (int j = 0; j < kMine; ++j) {
-                    if (r0 + 64 * j < off) v[y][j] = 0;
-                    sum_count[j] += v[y][j] >> 44;
-                    sum_mass[j] += v[y][j] & ((1ull << 44) - 1);
-                }
-            }
+                for (int j = 0; j < kMine; ++j) sum[j] += r0 + 64 * j >= off[y] ? v[y][j] : 0;
         }
     }
     // Up to and with each bin; weights in units of the maximum's, up to a factor that
@@ -432,13 +444,18 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
         // The last bin has what is left: its weights, below 2^-63 each, do not show, and it is
         // counted if need be.
         const bool is = r0 + 64 * j < kSampleBins - 1;
-        count[j] = here + wave_scan_i(is ? (int)sum_count[j] : 0);
-        here = __builtin_amdgcn_readlane(count[j], 63);
-        const double m = is ? (double)sum_mass[j] * unit : 0.0;
-        far += m * (r0 + 64 * j);
-        mass[j] = here_mass + wave_scan_d(m);
-        here_mass = lane_d(mass[j], 63);
+        count[j] = is ? (int)(sum[j] >> 44) : 0;
+        mass[j] = is ? (double)(sum[j] & ((1ull << 44) - 1)) * unit : 0.0;
+        far += mass[j] * (r0 + 64 * j);
         unit *= 0.5;
+    }
+    wave_scan_all<kMine>(count, mass);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        count[j] += here;
+        mass[j] += here_mass;
+        here = __builtin_amdgcn_readlane(count[j], 63);
+        here_mass = lane_d(mass[j], 63);
     }
     far = wave_sum_d(far);
     __syncthreads();
@@ -465,8 +482,9 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
         count[j] += c0;
         mass[j] += m0;
     }
-    // s_bin[k]: the first bin that `reached` (the last one always is).
-    auto first_bin = [&](int k, auto reached) {
+    // s_bin[k]: the first bin that `reached` (the last one always is): find, a barrier, tell, a
+    // barrier.
+    auto find = [&](int k, auto reached) {
         int r = kSampleBins - 1;
 #pragma unroll
         for (int j = kMine - 1; j >= 0; --j) {
@@ -474,9 +492,10 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
             if (are) r = kMine * 64 * wave_index() + 64 * j + __builtin_ctzll(are);
         }
         if (lane == 0) atomicMin(&s_bin[k].bin, r);
-        __syncthreads();
-        r = s_bin[k].bin;
+    };
+    auto tell = [&](int k) {
         // Its lane tells what is there, and the one before it.
+        const int r = s_bin[k].bin;
 #pragma unroll
         for (int j = 0; j < kMine; ++j) {
             if (r0 + 64 * j == r) {
@@ -487,18 +506,20 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
                 s_bin[k].count_before = count[j];
                 s_bin[k].mass_before = mass[j];
             }
-            if (r == 0 && own == 0 && j == 0) {
-                s_bin[k].count_before = 0;
-                s_bin[k].mass_before = 0.0;
-            }
         }
-        __syncthreads();
-        return s_bin[k];
+        if (r == 0 && own == 0) {
+            s_bin[k].count_before = 0;
+            s_bin[k].mass_before = 0.0;
+        }
     };
     int top = 0, bottom = kSampleBins - 1, above = 0, upto = 0;
     double lo = all_mass, hi = all_mass;
     if (f.top_k) {
-        const SampleBin k = first_bin(0, [&](int j) { return count[j] >= f.top_k; });
+        find(0, [&](int j) { return count[j] >= f.top_k; });
+        __syncthreads();
+        tell(0);
+        __syncthreads();
+        const SampleBin k = s_bin[0];
         top = bottom = k.bin;
         above = k.count_before;
         upto = k.count;
@@ -516,17 +537,20 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
         const double off = all_mass * (0x1p-21 + fabs((double)place) * 0x1p-24 * 0.035) +
                            all_far * 0x1p-24 * 0.035;
         const double least = f.top_p * (lo - off) - off, most = f.top_p * (hi + off) + off;
-        const SampleBin p =
-            first_bin(1, [&](int j) { return mass[j] >= least; });
+        find(1, [&](int j) { return mass[j] >= least; });
+        if (!f.top_k) find(2, [&](int j) { return mass[j] >= most; });
+        __syncthreads();
+        tell(1);
+        if (!f.top_k) tell(2);
+        __syncthreads();
+        const SampleBin p = s_bin[1];
         if (!f.top_k || p.bin < top) {
             top = p.bin;
             above = p.count_before;
         }
         if (!f.top_k) {
-            const SampleBin q =
-                first_bin(2, [&](int j) { return mass[j] >= most; });
-            bottom = q.bin;
-            upto = q.count;
+            bottom = s_bin[2].bin;
+            upto = s_bin[2].count;
         }
     }
     if (bottom == kSampleBins - 1) {
@@ -658,7 +682,7 @@ struct SampleLds {
         double upto[kSampleSegments];          // of a segment's kept ones at the border
         unsigned long long quanta[kSampleSegments];
     };
-    int n, found;
+    int n, place[2 * kSampleWaves];
     uint32_t last;
     int count, before, bin;
     uint64_t mass_before, border, list_end[kSampleWaves];
@@ -667,31 +691,29 @@ struct SampleLds {
 struct SamplePlainLds {
     double wave_d[kSampleWaves];
     double seg[kSampleSegments + 1];
-    int found;
+    int place[2 * kSampleWaves];
     uint32_t last;
 };
 
-// The first of n places that `holds`; where none does, the last that `some`, or 0.
-template <class Lds, class Holds, class Some>
-__device__ __forceinline__ int first_place(Lds &s, int n, Holds holds, Some some) {
+// The first thread whose place `holds`; where none does, the last that has `some`, or 0.
+// One barrier after the places are known (s.place: two for each wave).
+template <class Lds>
+__device__ __forceinline__ int first_place(Lds &s, bool holds, bool some) {
+    const uint64_t h = __ballot(holds), any = __ballot(some);
+    const int base = 64 * wave_index();
     __syncthreads();
-    if (threadIdx.x == 0) s.found = 0x7FFFFFFF;
+    if (lane_id() == 0) {
+        s.place[wave_index()] = h ? base + (int)__builtin_ctzll(h) : 0x7FFFFFFF;
+        s.place[kSampleWaves + wave_index()] = any ? base + 63 - (int)__builtin_clzll(any) : 0;
+    }
     __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kSampleThreads)
-        if (holds(j)) {
-            atomicMin(&s.found, j);
-            break;
-        }
-    __syncthreads();
-    int who = s.found;
-    if (who != 0x7FFFFFFF) return who;
-    __syncthreads();
-    if (threadIdx.x == 0) s.found = 0;
-    __syncthreads();
-    for (int j = threadIdx.x; j < n; j += kSampleThreads)
-        if (some(j)) atomicMax(&s.found, j);
-    __syncthreads();
-    return s.found;
+    int first = 0x7FFFFFFF, last = 0;
+#pragma unroll
+    for (int w = 0; w < kSampleWaves; ++w) {
+        first = min(first, s.place[w]);
+        last = max_i(last, s.place[kSampleWaves + w]);
+    }
+    return first != 0x7FFFFFFF ? first : last;
 }
 
 // The token of a row whose sums up to each segment are in s.seg: the segment, then the
@@ -703,9 +725,12 @@ __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const S
     typedef Logits<Type> L;
     const int own = threadIdx.x, segments = a.draws * kSampleWaves;
     const double total = s.seg[segments], target = (double)f.u * total;
-    const int who = first_place(
-        s, segments, [&](int j) { return s.seg[j + 1] > target && s.seg[j + 1] > s.seg[j]; },
-        [&](int j) { return s.seg[j + 1] > s.seg[j]; });
+    bool holds = false, some = false;
+    if (own < segments) {
+        some = s.seg[own + 1] > s.seg[own];
+        holds = some && s.seg[own + 1] > target;
+    }
+    const int who = first_place(s, holds, some);
     const Segment<Type> seg(a, row, who, a.draw_chunks);
     const int per = (a.draw_chunks + kSampleThreads - 1) / kSampleThreads, first = own * per;
     auto each_kept = [&](auto take) {
@@ -755,9 +780,7 @@ __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const S
         sum = at;
         before = s.seg[who] + block_scan_d(sum, &all, s.wave_d);
         // (Where rounding leaves nobody beyond the target, the last that is kept.)
-        by = first_place(s, kSampleThreads,
-                         [&](int) { return sum > 0.0 && before + sum > target; },
-                         [&](int) { return sum > 0.0; });
+        by = first_place(s, sum > 0.0 && before + sum > target, sum > 0.0);
     }
 }
 
@@ -813,9 +836,7 @@ __device__ __forceinline__ void find_border_token(Lds &s, bool by_mass, bool sum
         auto reached = [&](int c, uint64_t m) {
             return by_mass ? base + (double)m * unit >= target : base + (double)c >= target;
         };
-        const int who = first_place(
-            s, kSampleThreads, [&](int) { return here && reached(c0 + here, m0 + here_mass); },
-            [&](int) { return here != 0; });
+        const int who = first_place(s, here && reached(c0 + here, m0 + here_mass), here != 0);
         if ((int)threadIdx.x == who) {
             int c = c0;
             uint64_t m = m0;
