@@ -395,8 +395,8 @@ class SharedPrefix:
     work on it is split (PagedAttention.share makes it).  It holds while members
     share their prefix: they may grow, their pages may move (compact), and members
     may be freed, which then see nothing.  A sequence of another content in a
-    member's place needs a new plan.  The plan is kept until its work on every
-    stream is done, and by graphs that captured it."""
+    member's place needs a new plan.  Keep the plan until its work on every stream is
+    done, and as long as graphs that captured it."""
 
     def __init__(self, attention: PagedAttention, groups, prefix, batch: int, least=None):
         groups, prefix = [list(g) for g in groups], list(prefix)

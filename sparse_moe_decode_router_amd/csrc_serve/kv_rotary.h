@@ -13,6 +13,13 @@
 // halves r / 2 apart), elsewhere two chunks as far apart.  Lanes next to each other
 // take chunks next to each other.  An item reads both of its chunks before it
 // writes them, so queries may be turned in place.
+//
+// Memory bounds it: 20750 tokens, 56 heads on 8 of 128, bf16, are 765 MB read and
+// written in 154 us, 4.98 TB/s, where a copy reaches 5.07.  A workgroup has up to eight
+// tokens there, so that finding a sequence and the cosines are waited for once in eight.
+// Where tokens are few a token is cut into parts, since the chain of loads (length,
+// page, row) and not the bytes is what takes the time: 64 tokens of 56 heads on 8
+// into e4m3 pages 4.6 us, one of 7 heads on 1 2.9.
 #pragma once
 
 #include "serve_common.h"

@@ -36,7 +36,8 @@ class Rotary:
     """frequencies [rot / 2]: radians a position of each pair.  The dimensions
     first .. first + rot - 1 of a head are turned (both multiples of 16), pair j
     of them being (2j, 2j + 1) if interleaved, else (j, j + rot / 2).  amplitude:
-    what turned queries and keys are multiplied by."""
+    what turned queries and keys are multiplied by.  Keep it as long as graphs that
+    captured calls with it."""
 
     def __init__(self, frequencies, first: int = 0, interleaved: bool = False,
                  amplitude: float = 1.0, device="cuda"):

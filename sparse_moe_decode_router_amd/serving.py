@@ -1,6 +1,6 @@
 """Loading of ``libmoe_serve.so`` (the C ABI in include/moe_serve.h) and what
-the modules above it (``attention``, ``rotary``, ``sampling``, ``w4``) share: the argument structures,
-dtype codes, checks of tensors and the status codes.
+the modules above it (``attention``, ``rotary``, ``sampling``, ``w4``) share: the
+argument structures, dtype codes, checks of tensors and the status codes.
 
 Argument marshalling only, as in ``binding``: the operators run in the HIP
 kernels of the library, and there is nothing to fall back to.
