@@ -35,7 +35,7 @@
 // are spilled but at head_dim 256 on a 16-bit cache (17).
 #pragma once
 
-#include "serve_common.h"
+#include "attn_prompt.h"
 
 namespace moe {
 namespace serve {
@@ -252,20 +252,46 @@ __device__ __forceinline__ DecodeUnit find_unit(const AttnArgs &a, int want) {
     return u;
 }
 
-// Shared: of what is behind the sequences' shared prefixes; those that have one are left
-// as partial results, for attn_shared.h to join.
+template <int D>
+struct DecodeLds {
+    __attribute__((aligned(16))) float o[kDecodeWaves][16][D + 4];
+    float m[kDecodeWaves][16], l[kDecodeWaves][16], den[16];
+    uint32_t last;
+};
+
+// Shared: the first workgroups multiply shared prefixes, as prompts do, and the others take
+// what is behind them: the one multiplies, the other reads memory, so they go side by side,
+// the longer work first.  Sequences that have a prefix are left as partial results, for
+// attn_shared.h to join.
+template <int D>
+union SharedLds {
+    PromptLds<D> prefix;
+    DecodeLds<D> own;
+};
 template <class T, bool F8, int D, bool Shared = false>
-__global__ __launch_bounds__(kDecodeThreads, 2) void k_attn_decode(const AttnArgs a) {
+__global__ __launch_bounds__(kDecodeThreads, Shared && D > 128 ? 1 : 2) void k_attn_decode(
+    const AttnArgs a) {
     typedef DecodeTile<T, F8, D> Tile;
     constexpr int W = kDecodeWaves, KS = Tile::KS, E = Tile::E, ES = Tile::ES;
-    constexpr int kRow = D + 4;
-    __shared__ __attribute__((aligned(16))) float s_o[W][16][kRow];
-    __shared__ float s_m[W][16], s_l[W][16], s_den[16];
-    __shared__ uint32_t s_last;
+    __shared__ std::conditional_t<Shared, SharedLds<D>, DecodeLds<D>> lds;
+    int block = blockIdx.x;
+    if constexpr (Shared) {
+        static_assert(kPromptThreads == kDecodeThreads, "one launch of both");
+        if (block < a.prefix_units) return attn_prompt<T, F8, D, true>(lds.prefix, block);
+        block -= a.prefix_units;
+    }
+    auto &s = [&]() -> DecodeLds<D> & {
+        if constexpr (Shared) return lds.own;
+        else return lds;
+    }();
+    auto &s_o = s.o;
+    auto &s_m = s.m, &s_l = s.l;
+    auto &s_den = s.den;
+    uint32_t &s_last = s.last;
 
     const int lane = lane_id(), wave = wave_index(), c = lane & 15, g = lane >> 4;
     const int heads = a.kv_heads * a.head_groups;
-    const int hh = (int)blockIdx.x % heads, su = (int)blockIdx.x / heads;
+    const int hh = block % heads, su = block / heads;
     const DecodeUnit u = find_unit<Shared>(a, su);
     if (u.b < 0) return;
     const bool left = Shared && a.prefixes[u.b] > 0;

@@ -137,17 +137,23 @@ __device__ __forceinline__ PromptArgs &prompt_args() {
     return *a;
 }
 
-// Shared: the rows are the new tokens of a group of sequences, whose keys are their
-// shared prefix; only partial results are written.
-template <class T, bool F8, int D, bool Shared = false>
-__global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_prompt(
-    const AttnArgs) {
+template <int D>
+struct PromptLds {
+    __attribute__((aligned(1024))) char k[2][PromptTile<D>::kBytes];
+    __attribute__((aligned(1024))) char v[2][PromptTile<D>::kBytes];
+    uint32_t last;
+    int odd;
+};
+
+// The work of a workgroup.  Shared: the rows are the new tokens of a group of sequences,
+// whose keys are their shared prefix; only partial results are written.
+template <class T, bool F8, int D, bool Shared>
+__device__ __forceinline__ void attn_prompt(PromptLds<D> &s, int block) {
     typedef PromptTile<D> Tile;
     constexpr int KS = D / 16, DT = D / 32;
-    __shared__ __attribute__((aligned(1024))) char s_k[2][Tile::kBytes];
-    __shared__ __attribute__((aligned(1024))) char s_v[2][Tile::kBytes];
-    __shared__ uint32_t s_last;
-    __shared__ int s_odd;
+    auto &s_k = s.k, &s_v = s.v;
+    uint32_t &s_last = s.last;
+    int &s_odd = s.odd;
 
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_index();
     const int col = lane & 31, half = lane >> 5;
@@ -180,10 +186,10 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
 
     // Equal shares: workgroups go round the XCDs, so neighbours in the sequence,
     // which read the same keys, are given to the workgroups of one of them.
-    int h = (int)blockIdx.x % a.kv_heads, unit = (int)blockIdx.x / a.kv_heads;
+    int h = block % a.kv_heads, unit = block / a.kv_heads;
     if (a.units) {
-        const int xcd = (int)blockIdx.x & 7, per = (int)gridDim.x >> 3, more = (int)gridDim.x & 7;
-        const int id = xcd * per + min(xcd, more) + ((int)blockIdx.x >> 3);
+        const int xcd = block & 7, per = (int)gridDim.x >> 3, more = (int)gridDim.x & 7;
+        const int id = xcd * per + min(xcd, more) + (block >> 3);
         h = id / a.units;
         unit = id - h * a.units;
     }
@@ -193,7 +199,7 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
     SharedUnit su = {};
     int rows_lo = 0x7FFFFFFF, rows_hi = -1, rows_seen = 0x7FFFFFFF;   // positions; of those that see any
     if constexpr (Shared) {
-        su = a.shared_units[blockIdx.x];
+        su = a.shared_units[block];
         h = su.head;
         // The prefix is read from the member that has most of it.  Every row has a position of
         // its own; those of sequences that hold nothing see nothing, and widen no window.
@@ -882,6 +888,13 @@ __global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_promp
             } while (seq.tiles == 0);
         }
     }
+}
+
+template <class T, bool F8, int D>
+__global__ __launch_bounds__(kPromptThreads, D <= 128 ? 2 : 1) void k_attn_prompt(
+    const AttnArgs) {
+    __shared__ PromptLds<D> s;
+    attn_prompt<T, F8, D, false>(s, blockIdx.x);
 }
 
 }  // namespace serve

@@ -7,10 +7,10 @@
 // a part is a whole block, and sixteen parts of each share are on their way at once.  A
 // sequence's own parts are row by row (attn_decode.h).
 //
-// Loads of what other XCDs wrote bound it: 448 rows of 8 heads 9 us, four groups of 112
-// rows of 8 heads 10, 224 rows of 2 heads in 64 parts each 12.  In the decode launch, by the
-// last arrival of a row, a wave joined its own rows one part after another, and a long
-// prefix's 128 parts took 40 us.
+// Loads of what other XCDs wrote bound it: 448 rows of 8 heads 7 us, four groups of 112
+// rows of 8 heads 8, 224 rows of 2 heads in 64 parts or so each 12.  In the decode launch,
+// by the last arrival of a row, a wave joined its own rows one part after another, and a
+// long prefix's 128 parts took 40 us.
 #pragma once
 
 #include "serve_common.h"

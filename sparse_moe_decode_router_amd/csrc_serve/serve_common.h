@@ -119,6 +119,7 @@ struct AttnArgs {
     const int32_t *members;
     float *shared_part;
     SharedTail *shared_tails;      // [batch][kv_heads * head_groups], of those with a prefix
+    int32_t prefix_units;
 };
 
 // Blocks of 2^L keys that a row at the last position of n sees: the first

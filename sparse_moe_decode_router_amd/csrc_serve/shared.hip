@@ -1,18 +1,18 @@
 // shared.hip - host side of decode over shared prefixes: the plan, argument checks, and
 // their part of the C ABI declared in include/moe_serve.h.
 //
-// Three launches.  The first multiplies the queries of all members of a group with the
-// keys of their prefix, as prompts do: the rows (member, query head) of a kv head are
-// taken 128 at a time, and the prefix in as many parts as fill the chip once.  The
-// second is decode over what each sequence has behind the prefix.  The third joins the
-// partial results of both.  Prefix keys are read once for 128 rows instead of once for
-// each member.
+// Two launches.  The first has two kinds of workgroups.  Some multiply the queries of all
+// members of a group with the keys of their prefix, as prompts do: the rows (member, query
+// head) of a kv head are taken 128 at a time, so that prefix keys are read once for 128
+// rows instead of once for each member.  The others decode what each sequence has behind
+// the prefix.  The second launch joins the partial results of both.
 //
-// Us for the prefix, the tails and the join: 64 sequences, 56 heads on 8, prefix 8192 and
-// tails up to 512: 29, 24, 9; four groups of 16, e4m3, prefixes up to 32768 and tails up to
-// 1000: 66, 24, 10; 32 sequences, 14 heads on 2, prefix 131072 and tails up to 300: 49, 8, 12.
-// The prefix is bound as prompts are (vector and matrix instructions), after some 8 us to
-// its first keys; tails by latencies.
+// Device time of the two launches, us: 64 sequences, 56 heads on 8, prefix 8192 and tails up to 512: 40
+// and 7; four groups of 16, e4m3, prefixes up to 32768 and tails up to 1000: 85 and 8; 32
+// sequences, 14 heads on 2, prefix 131072 and tails up to 300: 52 and 12.  Prefixes are bound
+// as prompts are (vector and matrix instructions), after some 7 us to their first keys;
+// tails by memory.  As launches of their own, each on the whole chip, they took 29 + 24,
+// 66 + 24 and 49 + 8.
 #include "serve_host.h"
 
 #include "attn_decode.h"
@@ -26,16 +26,21 @@ namespace {
 // The fewest tiles of 64 keys that a workgroup takes, and the most parts of a prefix: every
 // part is read again by the join.
 constexpr int kSharedTiles = 4, kSharedParts = 128;
-// Bytes of keys and values that reading prefixes apart has to spare: three launches instead of
-// one cost some 12 us, in which a prefix that is read again comes from the caches.  Decode of
-// each sequence by itself, and shared, us, 7 heads on each kv head: 59 MB (8 of 8192, 2 kv
-// heads) 16 and 25; 117 MB (8 of 16384, 2) 21 and 26; 126 MB (16 of 4096, 8, e4m3) 23 and
-// 24; 132 MB (64 of 512, 8) 17 and 25; 264 MB (64 of 1024, 8) 26 and 25; 235 MB (8 of 8192, 4
-// heads of 256 on 4 each) 39 and 35.
-constexpr int64_t kSharedLeast = 200000000;
+// Bytes of keys and values that reading prefixes apart has to spare: it takes some 16 us at
+// least, in which a prefix that is read again comes from the caches.  Decode of each
+// sequence by itself, and shared, us, 7 heads on each kv head: 7 MB (8 of 2000, 1 kv head)
+// 11 and 16; 29 MB (8 of 8192, 1; 8 of 4096, 2; 8 of 1024, 8) 18 and 18, 21 and 16, 13 and 16;
+// 34 MB (2 of 32768, 2) 20 and 24; 59 MB (8 of 8192, 2) 24 and 18; 66 MB (64 of 256, 8) 23
+// and 17; 126 MB (16 of 4096, 8, e4m3) 28 and 18; 264 MB (64 of 1024, 8) 35 and 18.
+constexpr int64_t kSharedLeast = 40000000;
 // Units behind the prefixes that a call aims at, for each compute unit: tails are short, and
-// a sequence's is best taken by one workgroup (64 tails of up to 512, 56 heads on 8: 1, 2
+// a sequence's is best taken by one workgroup (in a launch of their own, 64 tails of up to
+// 512, 56 heads on 8: 1, 2
 // and 4 a compute unit 63.0, 63.6 and 64.7 us; up to 1000 in e4m3: 100, 104, 107).
+
+// What the two kinds of work take on the whole chip, us: a first tile of either, 128 rows
+// times 64 keys for each dimension, a byte.
+constexpr double kStartUs = 7., kPrefixUs = 4.1e-5, kByteUs = 2e-7;
 
 size_t prefix_floats(const moe_attn_shared &p) {
     return (size_t)kPromptRows * (p.head_dim + 2) * p.slots * p.kv_heads;
@@ -97,7 +102,23 @@ moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *c, int3
             if (apart(g)) n += tiles_of(g) * parts_of(g, share);
         return n;
     };
-    const int64_t slots = std::max(1, prompt_slots(kv->head_dim) / kv->kv_heads);
+    // The workgroups that prefixes get: their share of the time that both kinds of work take,
+    // but half at least, since tails may be far shorter than those that are planned for.
+    int64_t work = 0, longest = 0, behind = 0;
+    for (int g = 0; g < groups; ++g)
+        if (apart(g)) {
+            work += tiles_of(g) * keys_of(g);
+            longest = std::max<int64_t>(longest, prefix[g]);
+            behind += cu[g + 1] - cu[g];
+        }
+    const double row_bytes = (double)plane_bytes(*kv) / kv->pages / kv->page * 2;
+    const double tails = (double)behind * std::max<int64_t>(0, c->longest - longest) +
+                         (double)(batch - behind) * c->longest;
+    const double t_prefix = kStartUs + kPrefixUs * work * kv->kv_heads * kv->head_dim;
+    const double t_tail = kStartUs + tails * row_bytes * kByteUs;
+    const double part = std::max(0.5, t_prefix / (t_prefix + t_tail));
+    const int64_t slots =
+        std::max<int64_t>(1, (int64_t)(prompt_slots(kv->head_dim) * part) / kv->kv_heads);
     const int64_t aim = units_with(1ll << 40) <= slots ? slots : 4 * slots;
     int64_t lo = kSharedTiles - 1, hi = 1ll << 26;      // (units_with falls)
     if (units_with(kSharedTiles) <= aim) hi = kSharedTiles;
@@ -204,8 +225,7 @@ moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config 
     AttnArgs a = attn_args(*kv, *c, layer);
     a.split = std::max(1, std::min(decode_split(*kv, *c, plan->tail), kPlanCus / (a.kv_heads * a.head_groups)));
     const int64_t grid = ((int64_t)a.split + plan->batch) * a.kv_heads * a.head_groups;
-    const int64_t first = plan->units;
-    if (grid > kMaxGrid256 || first > kMaxGrid256) return MOE_ERR_UNSUPPORTED;
+    if (grid + plan->units > kMaxGrid256) return MOE_ERR_UNSUPPORTED;
     int cus;
     if ((s = compute_units(&cus)) != MOE_OK) return s;
     a.q = q;
@@ -216,6 +236,7 @@ moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config 
     a.part = (float *)workspace;
     a.shared_part = (float *)((char *)workspace + round16(decode_bytes));
     a.counters = counters;
+    a.prefix_units = plan->units;
     a.batch = plan->batch;
     a.shared_tails = (SharedTail *)(a.shared_part + prefix_floats(*plan));
     a.shared_units = (const SharedUnit *)plan->data;
@@ -227,11 +248,10 @@ moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config 
             typedef decltype(t) T;
             constexpr bool kF8 = decltype(f8)::value;
             constexpr int D = decltype(d)::value;
-            k_attn_prompt<T, kF8, D, true><<<(int)first, kPromptThreads, 0, stream>>>(a);
-            moe_status r = launched();
+            k_attn_decode<T, kF8, D, true>
+                <<<(int)(plan->units + grid), kDecodeThreads, 0, stream>>>(a);
+            const moe_status r = launched();
             if (r != MOE_OK) return r;
-            k_attn_decode<T, kF8, D, true><<<(int)grid, kDecodeThreads, 0, stream>>>(a);
-            if ((r = launched()) != MOE_OK) return r;
             const int64_t join = (int64_t)plan->tiles * 4 * (D / 32) * kv->kv_heads;
             // Up to 32 parts are two rounds of loads; more are taken by four times the waves.
             if (plan->parts <= 32)

@@ -248,7 +248,7 @@ def test_members_grow_and_are_freed_under_one_plan():
 
 
 def test_little_to_spare_is_decoded_one_by_one():
-    """Below 200 MB the plan is decode() itself; with `least` the prefix is read apart."""
+    """Below 40 MB the plan is decode() itself; with `least` the prefix is read apart."""
     cache = gu.shared_cache([[0, 1, 2]], [160], [170, 161, 200], 2, 16, 64, BF, seed=13)
     att = attention.PagedAttention(cache.gpu(), 6, 3, 300)
     q = randn((3, 6, 64), BF, 14).cuda()
