@@ -554,6 +554,50 @@ def test_the_example_samples():
     layer.close()
 
 
+def test_calls_run_on_the_device_of_their_tensors(monkeypatch):
+    """Another device is current: every call switches to its own for the launch (seen by
+    what is asked for, since there may be one device)."""
+    now, entered = [7], []
+    real = torch.cuda.device
+
+    class Switch:
+        def __init__(self, device):
+            self.device = torch.device(device)
+
+        def __enter__(self):
+            entered.append(self.device)
+            self.inner, self.before = real(self.device), now[0]
+            now[0] = self.device.index
+            self.inner.__enter__()
+
+        def __exit__(self, *a):
+            now[0] = self.before
+            return self.inner.__exit__(*a)
+
+    cache = gu.shared_cache([[0, 1]], [32], [40, 50], 2, 16, 64, BF, seed=31)
+    kv = cache.gpu()
+    att = attention.PagedAttention(kv, 4, 2, 64)
+    plan = att.share([[0, 1]], [32], least=0)
+    turn = rotary.Rotary(rotary.frequencies(64))
+    sampler = sampling.Sampler(2, 100)
+    q, k = randn((2, 4, 64), BF, 32).cuda(), randn((2, 2, 64), BF, 33).cuda()
+    logits, u = randn((2, 100), F32, 34).cuda(), torch.tensor([0.3, 0.7]).cuda()
+    calls = [lambda: att.decode_shared(0, q, plan), lambda: sampler(logits, u, top_p=0.9),
+             lambda: kv.append_rotated(0, q, k, k, turn)]
+    want = [calls[0](), calls[1](), calls[2]()]
+    for module in (attention, sampling):
+        monkeypatch.setattr(module, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Switch)
+    got = [calls[2](), calls[0](), calls[1]()]
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert [d.index for d in entered] == [kv.device.index] * 3
+    assert torch.equal(got[0], want[2])
+    # (The keys at the last positions are the appended ones by now.)
+    assert bool(got[1][0].isfinite().all()) and got[1][0].shape == want[0][0].shape
+    assert torch.equal(got[2][0], want[1][0]) and torch.equal(got[2][1], want[1][1])
+
+
 def test_refusals_on_the_gpu():
     kv = su.HostCache([20, 30], 2, 16, 64, BF, seed=23).gpu()
     att = attention.PagedAttention(kv, 4, 2, 64)
