@@ -682,10 +682,11 @@ struct SampleLds {
     uint64_t list[kSampleList];
     uint32_t count_of[kSampleKeyBins];
     unsigned long long mass_of[kSampleKeyBins];
-    union {
-        double wave_d[kSampleWaves];
-        uint64_t wave_u[kSampleWaves];
-    };
+    // Places of their own: block_scan_d reads its array behind its last barrier, so that a
+    // wave may have gone on to write list_first and wave_u while another still reads wave_d.
+    // (Of one array, block_scan_d's first barrier keeps its uses apart.)
+    double wave_d[kSampleWaves];
+    uint64_t wave_u[kSampleWaves];
     int wave_i[kSampleWaves];
     double seg[kSampleSegments + 1];
     union {
@@ -695,7 +696,7 @@ struct SampleLds {
     int n, place[2 * kSampleWaves];
     uint32_t last;
     int count, before, bin;
-    uint64_t mass_before, border, list_end[kSampleWaves];
+    uint64_t mass_before, border, list_first[kSampleWaves], list_end[kSampleWaves];
 };
 // Of k_sample_plain.
 struct SamplePlainLds {
@@ -1041,15 +1042,15 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
                 last = max_u64(last, xor_u64(last, m));
             }
             if (lane == 0) {
-                s.wave_u[wave] = first;
+                s.list_first[wave] = first;
                 s.list_end[wave] = last;
             }
             __syncthreads();
-            lo = s.wave_u[0];
+            lo = s.list_first[0];
             border = s.list_end[0];
 #pragma unroll
             for (int w = 1; w < kSampleWaves; ++w) {
-                lo = min_u64(lo, s.wave_u[w]);
+                lo = min_u64(lo, s.list_first[w]);
                 border = max_u64(border, s.list_end[w]);
             }
         }
