@@ -248,9 +248,10 @@ moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config 
  * drawn, w_i over that sum.  T = 0 (below 2^-100, or NaN) takes the first largest logit,
  * logprob 0.  Logits of -inf and NaN are never drawn; a row of nothing else gives -1
  * and -inf.  With a logit of +inf only those have weight, 1 each.  u below 0 or NaN
- * counts as 0, from 1 on the last kept token is drawn.  Weights and their sums are in
- * 64 bits, and of tokens next to a border of top_p integers of 2^-44 of the largest of
- * them, whose sums have no order.
+ * counts as 0, which draws the first kept token, however small its weight; from 1 on the
+ * last one is drawn.  Weights and their sums are in 64 bits (a weight that is zero there is
+ * never drawn), and of tokens next to a border of top_p integers of 2^-44 of the largest
+ * of them, whose sums have no order.
  * Each filter is a device array by row, or NULL: the value for all rows beside it. */
 typedef struct {
     const float *temperature, *top_p, *min_p;

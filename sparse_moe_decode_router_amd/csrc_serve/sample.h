@@ -693,6 +693,7 @@ struct SampleLds {
         double upto[kSampleSegments];          // of a segment's kept ones at the border
         unsigned long long quanta[kSampleSegments];
     };
+    uint8_t some[kSampleSegments];             // whether the kept ones at the border have weight
     int n, place[2 * kSampleWaves];
     uint32_t last;
     int count, before, bin;
@@ -729,18 +730,19 @@ __device__ __forceinline__ int first_place(Lds &s, bool holds, bool some) {
 
 // The token of a row whose sums up to each segment are in s.seg: the segment, then the
 // place in it.  A thread takes a few chunks next to each other.  weight(x), and
-// is_kept(x, index).
+// is_kept(x, index).  some: whether segment `threadIdx.x` holds any weight.  (Not what the
+// sums up to it say: two that differ by nothing may be off by a rounding, and a weight
+// may be too small to show in them.)
 template <int Type, class Lds, class Weight, class Is>
 __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const SampleRow &f,
-                                           Lds &s, Weight weight, Is is_kept) {
+                                           Lds &s, bool some, Weight weight, Is is_kept) {
     typedef Logits<Type> L;
     const int own = threadIdx.x, segments = a.draws * kSampleWaves;
-    const double total = s.seg[segments], target = (double)f.u * total;
-    bool holds = false, some = false;
-    if (own < segments) {
-        some = s.seg[own + 1] > s.seg[own];
-        holds = some && s.seg[own + 1] > target;
-    }
+    const double total = s.seg[segments];
+    // From 1 on the target is beyond every sum, so that the last weight is taken; every
+    // weight is beyond a target of 0.
+    const double target = f.u < 1.f ? (double)f.u * total : __builtin_inf();
+    const bool holds = some && (target == 0.0 || s.seg[own + 1] > target);
     const int who = first_place(s, holds, some);
     const Segment<Type> seg(a, row, who, a.draw_chunks);
     const int per = (a.draw_chunks + kSampleThreads - 1) / kSampleThreads, first = own * per;
@@ -985,6 +987,7 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
     uint64_t border = 0;
     const int own = (int)threadIdx.x, per_segment = a.draw_chunks * L::kPer;
     double listed_kept = 0.0;       // of the listed ones those in segment `own`
+    bool listed_some = false;
     if (b.listed) {
         if (!wide && a.draws > 1) {
             // All slices' shares of the list: the n-th of all is in the share whose first is
@@ -1006,7 +1009,10 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
             }
         }
         if (!wide)
-            for (int i = own; i < segments; i += kSampleThreads) s.quanta[i] = 0;
+            for (int i = own; i < segments; i += kSampleThreads) {
+                s.quanta[i] = 0;
+                s.some[i] = 0;
+            }
         auto visit = [&](auto f) {
             if (wide) {
                 each_segment<Type>(a, row, [&](const Segment<Type> &seg, int) {
@@ -1077,17 +1083,20 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
             });
             __syncthreads();
             listed_kept = own < segments ? s.upto[own] : 0.0;
+            listed_some = listed_kept > 0.0;
         } else {
             const double per = 1.0 / unit;
             for (int j = own; j < n; j += kSampleThreads) {
                 const uint64_t v = s.list[j];
-                if (v > border) continue;
-                atomicAdd(&s.quanta[(sample_index(v) + seg.shift) / per_segment],
-                          (unsigned long long)__builtin_rint(
-                              kept_weight(sample_ordered<Type>(v)) * per));
+                const double w = v > border ? 0.0 : kept_weight(sample_ordered<Type>(v));
+                if (!(w > 0.0)) continue;
+                const int at = (sample_index(v) + seg.shift) / per_segment;
+                s.some[at] = 1;
+                atomicAdd(&s.quanta[at], (unsigned long long)__builtin_rint(w * per));
             }
             __syncthreads();
             listed_kept = own < segments ? (double)s.quanta[own] * unit : 0.0;
+            listed_some = own < segments && s.some[own];
         }
     }
     double all_listed = 0.0, listed_before = 0.0;
@@ -1095,7 +1104,7 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
     if (own <= segments)
         s.seg[own] = own < segments ? kept_before + listed_before : all_kept + all_listed;
     __syncthreads();
-    draw_token<Type>(a, row, f, s, kept_weight, [&](float x, int i) {
+    draw_token<Type>(a, row, f, s, kept > 0.0 || listed_some, kept_weight, [&](float x, int i) {
         return x >= b.top || sample_order<Type>(x, i) <= border;
     });
 }
@@ -1169,17 +1178,20 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_plain(const Sample
     }
     const SampleWeight weight_of(max, f.temperature);
     double before = 0.0;
+    bool some = false;
 #pragma unroll 1
     for (int j = 0; j < kEach && 64 * j < segments; ++j) {
         const int i = 64 * j + lane;
         const bool is = i < segments && its[j] > -__builtin_inff();
-        const double inc = before + wave_scan_d(is ? part[j] * weight_of(its[j]) : 0.0);
+        const double has = is ? part[j] * weight_of(its[j]) : 0.0;
+        const double inc = before + wave_scan_d(has);
+        if (wave == j) some = has > 0.0;
         if (wave == 0 && i < segments) s.seg[i + 1] = inc;
         before = lane_d(inc, 63);
     }
     if (own == 0) s.seg[0] = 0.0;
     __syncthreads();
-    draw_token<Type>(a, row, f, s, weight_of,
+    draw_token<Type>(a, row, f, s, some, weight_of,
                      [](float, int) { return true; });
 }
 

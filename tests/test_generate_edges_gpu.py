@@ -1,0 +1,69 @@
+"""Edges of the rotated append, decode over shared prefixes and sampling on the GPU."""
+import math
+
+import pytest
+import torch
+
+import generate_util as gu
+import serve_util as su
+from sparse_moe_decode_router_amd import sampling
+
+pytestmark = pytest.mark.gpu
+
+BF, FP, F32, E4 = torch.bfloat16, torch.float16, torch.float32, su.E4M3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+
+
+def call(x, u, **filters):
+    got = sampling.Sampler(*x.shape)(x.cuda(), u.cuda(), **filters)
+    torch.cuda.synchronize()
+    return got
+
+
+# ---- Sampling: numbers u at the ends ----------------------------------------
+
+@pytest.mark.parametrize("filters", [{}, dict(top_p=0.9), dict(top_k=5), dict(top_k=40, top_p=0.8),
+                                     dict(min_p=0.01)], ids=str)
+@pytest.mark.parametrize("rows,vocab,dtype,kept", [
+    (520, 4000, BF, 3000),       # 8 segments of a row, the last two empty
+    (64, 40000, F32, 35000),     # 64, the last eight
+    (256, 10000, FP, 9000),      # 16
+    (40, 300, F32, 10)], ids=str)
+def test_the_last_kept_token_is_drawn_from_one_on(rows, vocab, dtype, kept, filters):
+    """Behind the last kept token there is nothing but masked ones, whole segments of
+    them, whose sums up to each are no more than those before by definition, and may be by
+    rounding."""
+    g = torch.Generator().manual_seed(70)
+    x = torch.randn((rows, vocab), generator=g) * 3
+    x[:, kept:] = -math.inf
+    x = x.to(dtype)
+    u = torch.tensor([1.0, 2.0, math.inf])[torch.arange(rows) % 3]
+    gu.check_sample(call(x, u, **filters), x, u, **filters)
+
+
+def hardly(vocab):
+    """Rows of three tokens: one of all the weight in the middle, and two of which hardly
+    any is left at a temperature of 0.01, some of it below the smallest normal number of
+    64 bits."""
+    by = 6.9 + 0.02 * torch.arange(24)
+    x = torch.full((48, vocab), -math.inf)
+    x[:, vocab // 2] = 1.0
+    x[:, 1] = 1.0 - torch.cat([by, torch.full((24,), 7.3)])
+    x[:, vocab - 2] = 1.0 - torch.cat([torch.full((24,), 7.25), by])
+    return x
+
+
+@pytest.mark.parametrize("filters", [{}, dict(top_k=900), dict(top_k=3), dict(top_p=1.0, min_p=0.0)],
+                         ids=str)
+@pytest.mark.parametrize("vocab", [1000, 100003])
+def test_tokens_of_hardly_any_weight_are_first_and_last(vocab, filters):
+    x = hardly(vocab)
+    for u, at in ((0.0, 1), (1.0, vocab - 2), (0.5, vocab // 2)):
+        tokens, _ = call(x, torch.full((48,), u), temperature=0.01, **filters)
+        assert torch.all(tokens.cpu() == at)
