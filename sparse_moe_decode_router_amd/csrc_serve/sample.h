@@ -186,6 +186,10 @@ struct SampleWeight {
         max = inf ? 0x1p128 : (double)of_max;
         c = inf ? 0x1p900 : 1.44269504088896340736 / (double)temperature;
     }
+    // Of the power of 2 that is the weight.
+    __device__ __forceinline__ double exponent(float x) const {
+        return fmin(fmax(((double)x - max) * c, -1100.0), 0.0);
+    }
     __device__ __forceinline__ double operator()(float x) const {
         return exp2_64(((double)x - max) * c);
     }
@@ -729,13 +733,14 @@ __device__ __forceinline__ int first_place(Lds &s, bool holds, bool some) {
 }
 
 // The token of a row whose sums up to each segment are in s.seg: the segment, then the
-// place in it.  A thread takes a few chunks next to each other.  weight(x), and
-// is_kept(x, index).  some: whether segment `threadIdx.x` holds any weight.  (Not what the
+// place in it.  A thread takes a few chunks next to each other.  weight_of: of any of the
+// row's values, weight(x): as it is kept, and is_kept(x, index).  some: whether segment `threadIdx.x` holds any weight.  (Not what the
 // sums up to it say: two that differ by nothing may be off by a rounding, and a weight
 // may be too small to show in them.)
 template <int Type, class Lds, class Weight, class Is>
 __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const SampleRow &f,
-                                           Lds &s, bool some, Weight weight, Is is_kept) {
+                                           Lds &s, bool some, const SampleWeight &weight_of,
+                                           Weight weight, Is is_kept) {
     typedef Logits<Type> L;
     const int own = threadIdx.x, segments = a.draws * kSampleWaves;
     const double total = s.seg[segments];
@@ -759,7 +764,7 @@ __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const S
                     const int i = at + e + y;
                     const bool is = in < a.draw_chunks && (uint32_t)i < (uint32_t)a.vocab &&
                                     x > -__builtin_inff() && is_kept(x, i);
-                    take(i, is ? weight(x) : 0.0);
+                    take(i, x, is ? weight(x) : 0.0);
                 }
                 if constexpr (L::kPer == 8) c = (u32x4){c[2], c[3], 0u, 0u};
             }
@@ -770,22 +775,25 @@ __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const S
     int by = own;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
-        double at = before, of = 1.0;
+        double at = before;
+        float logit = 0.f;
         int token = 0;
         bool found = false;
         if (own == by)
-            each_kept([&](int i, double w) {
+            each_kept([&](int i, float x, double w) {
                 at += w;
                 if (!found && w > 0.0) {
                     token = i;
-                    of = w;
+                    logit = x;
                     found = at > target;
                 }
             });
         if (pass) {
             if (own == by) {
                 a.token[row] = token;
-                a.logprob[row] = (float)-log_64(total / of);
+                // (Not by its weight, which may be below the normal numbers.)
+                a.logprob[row] =
+                    (float)(weight_of.exponent(logit) * 0.69314718055994530942 - log_64(total));
             }
             return;
         }
@@ -1104,9 +1112,10 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_draw(const SampleA
     if (own <= segments)
         s.seg[own] = own < segments ? kept_before + listed_before : all_kept + all_listed;
     __syncthreads();
-    draw_token<Type>(a, row, f, s, kept > 0.0 || listed_some, kept_weight, [&](float x, int i) {
-        return x >= b.top || sample_order<Type>(x, i) <= border;
-    });
+    draw_token<Type>(a, row, f, s, kept > 0.0 || listed_some, weight_of, kept_weight,
+                     [&](float x, int i) {
+                         return x >= b.top || sample_order<Type>(x, i) <= border;
+                     });
 }
 
 // Rows without filters.
@@ -1191,7 +1200,7 @@ __global__ __launch_bounds__(kSampleThreads, 4) void k_sample_plain(const Sample
     }
     if (own == 0) s.seg[0] = 0.0;
     __syncthreads();
-    draw_token<Type>(a, row, f, s, some, weight_of,
+    draw_token<Type>(a, row, f, s, some, weight_of, weight_of,
                      [](float, int) { return true; });
 }
 

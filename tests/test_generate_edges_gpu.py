@@ -1,6 +1,7 @@
 """Edges of the rotated append, decode over shared prefixes and sampling on the GPU."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -67,3 +68,16 @@ def test_tokens_of_hardly_any_weight_are_first_and_last(vocab, filters):
     for u, at in ((0.0, 1), (1.0, vocab - 2), (0.5, vocab // 2)):
         tokens, _ = call(x, torch.full((48,), u), temperature=0.01, **filters)
         assert torch.all(tokens.cpu() == at)
+
+
+@pytest.mark.parametrize("filters", [{}, dict(top_k=900), dict(top_k=3), dict(top_p=1.0, min_p=0.0)],
+                         ids=str)
+@pytest.mark.parametrize("vocab", [1000, 100003])
+def test_probabilities_of_hardly_any_weight(vocab, filters):
+    """The logarithm is the exponent, whatever is left of its power in 64 bits."""
+    x, t = hardly(vocab), float(np.float32(0.01))
+    for u, at in ((0.0, 1), (1.0, vocab - 2)):
+        _, drawn = call(x, torch.full((48,), u), temperature=0.01, **filters)
+        # (all of the weight is the largest one's); one rounding to f32, 2^-40 before
+        want = (x[:, at].double() - 1.0) / t
+        assert float((drawn.cpu().double() / want - 1).abs().max()) <= 2.0 ** -24 + 2.0 ** -36
