@@ -205,8 +205,9 @@ moe_status moe_attn_prompt(const moe_kv_cache *kv, const moe_attn_config *cfg, i
  * may move, and a member may be freed (it then sees nothing), but not become another
  * sequence.
  * least: bytes of keys and values of one layer that reading prefixes once for each group has
- * to spare; with less, sequences are decoded one by one, which then takes no longer (below
- * 0: 40 MB, where that was measured to end; 0: prefixes are always read apart).
+ * to spare, counting of a prefix what a member sees at most (with a window its positions and
+ * the sinks); with less, sequences are decoded one by one (below 0: 40 MB, about where
+ * that was measured to take no longer; 0: prefixes are always read apart).
  * Host only: cu [groups + 1], members and prefix are host memory.  data NULL: only the
  * sizes; else it receives plan->ints integers, which the caller copies to the device and
  * puts the address of into plan->data. */

@@ -31,7 +31,14 @@ constexpr int kSharedTiles = 4, kSharedParts = 128;
 // sequence by itself, and shared, us, 7 heads on each kv head: 7 MB (8 of 2000, 1 kv head)
 // 11 and 16; 29 MB (8 of 8192, 1; 8 of 4096, 2; 8 of 1024, 8) 18 and 18, 21 and 16, 13 and 16;
 // 34 MB (2 of 32768, 2) 20 and 24; 59 MB (8 of 8192, 2) 24 and 18; 66 MB (64 of 256, 8) 23
-// and 17; 126 MB (16 of 4096, 8, e4m3) 28 and 18; 264 MB (64 of 1024, 8) 35 and 18.
+// and 17; 126 MB (16 of 4096, 8, e4m3) 28 and 18; 264 MB (64 of 1024, 8) 35 and 18.  Within
+// windows, counted as above (members by window, kv heads): 0.3 MB (2 by 64, 8) 11 and 16;
+// 32 MB (16 by 512, 8) 13 and 19; 34 MB (64 by 128, 8) 19 and 20; 59 MB (8 by 8192, 2) 24 and
+// 21; 66 MB (32 by 2048, 2) 17 and 23; 118 MB (8 by 4096, 8) 21 and 22; 133 MB (64 by 512, 8)
+// 27 and 20, behind longer tails, which leave less of the window to the prefix, 28 and 28; 261
+// MB (32 by 8192, 2) 34 and 23; 1058 MB (64 by 4096, 8) 85 and 35.  Bytes alone do not decide
+// it: a few microseconds are lost on either side of the border (one by one 29 MB of 8
+// sequences took 13 to 21, 60 MB 17 to 24, by how many parts their rows were cut into).
 constexpr int64_t kSharedLeast = 40000000;
 // Units behind the prefixes that a call aims at, for each compute unit: tails are short, and
 // a sequence's is best taken by one workgroup (in a launch of their own, 64 tails of up to
@@ -81,15 +88,25 @@ moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *c, int3
         return worth && cu[g + 1] - cu[g] > 1 && prefix[g] > 0 &&
                (c->window == 0 || c->sinks <= prefix[g]);
     };
+    // Most positions that a sequence sees of n: a window's, and the sinks.
+    auto seen_of = [&](int64_t n) {
+        return c->window > 0 ? std::min<int64_t>(n, (int64_t)c->window + c->sinks) : n;
+    };
+    const double row_bytes = (double)plane_bytes(*kv) / kv->pages / kv->page * 2;
     double spared = 0.0;
     for (int g = 0; g < groups; ++g)
         if (apart(g))
-            spared += (double)(cu[g + 1] - cu[g] - 1) * std::min<int64_t>(prefix[g], most) *
-                      (plane_bytes(*kv) / kv->pages / kv->page) * 2;
+            spared += (double)(cu[g + 1] - cu[g] - 1) *
+                      seen_of(std::min<int64_t>(prefix[g], most)) * row_bytes;
     worth = spared >= (double)(least < 0 ? kSharedLeast : least);
     auto tiles_of = [&](int g) { return ((cu[g + 1] - cu[g]) * group + kPromptRows - 1) / kPromptRows; };
+    // Tiles of keys that all members together see of a prefix: none begins its window before
+    // the shortest one does, which has the whole prefix as a rule, and a window begins
+    // within a tile.
+    auto tiles_in = [](int64_t n) { return (n + kPromptKeys - 1) / kPromptKeys; };
     auto keys_of = [&](int g) {
-        return (std::min<int64_t>(prefix[g], most) + kPromptKeys - 1) / kPromptKeys;
+        const int64_t all = tiles_in(std::min<int64_t>(prefix[g], most));
+        return c->window > 0 ? std::min(all, tiles_in(c->window) + 1 + tiles_in(c->sinks)) : all;
     };
     // The smallest share of tiles of keys with which all workgroups fit at once; if none
     // does, four rounds of them.
@@ -111,9 +128,8 @@ moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *c, int3
             longest = std::max<int64_t>(longest, prefix[g]);
             behind += cu[g + 1] - cu[g];
         }
-    const double row_bytes = (double)plane_bytes(*kv) / kv->pages / kv->page * 2;
-    const double tails = (double)behind * std::max<int64_t>(0, c->longest - longest) +
-                         (double)(batch - behind) * c->longest;
+    const double tails = (double)behind * seen_of(std::max<int64_t>(0, c->longest - longest)) +
+                         (double)(batch - behind) * seen_of(c->longest);
     const double t_prefix = kStartUs + kPrefixUs * work * kv->kv_heads * kv->head_dim;
     const double t_tail = kStartUs + tails * row_bytes * kByteUs;
     const double part = std::max(0.5, t_prefix / (t_prefix + t_tail));

@@ -6,6 +6,9 @@ import subprocess
 
 import pytest
 
+from test_generate_abi import config, plan
+from test_serve_abi import cache
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "sparse_moe_decode_router_amd", "csrc_serve")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -38,3 +41,47 @@ CHECKS(0); CHECKS(1); CHECKS(kSampleF32);
                                                                 "csrc"), "-I", CSRC, str(src)],
         capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-3000:]
+
+
+def shared_plan(window, sinks, prefix, members=16, groups=1, least=-1, longest=40000, heads=56,
+                kv_heads=8):
+    n = members * groups
+    c = cache(kv_heads=kv_heads, head_dim=128, seqs=n, cols=4096, page=64, pages=1 << 16)
+    cfg = config(q_heads=heads, batch=n, longest=longest, window=window, sinks=sinks)
+    lists = [list(range(g * members, (g + 1) * members)) for g in range(groups)]
+    s, p, data = plan(c, cfg, lists, [prefix] * groups, n, least)
+    assert s == 0
+    return p, data
+
+
+@pytest.mark.parametrize("members,prefix,window,sinks", [
+    (2, 131072, 64, 4), (16, 32768, 512, 4), (16, 32768, 128, 0), (64, 32768, 128, 1)])
+def test_little_to_spare_within_a_window(members, prefix, window, sinks):
+    """What reading a prefix apart spares is no more than members see of it: a window's
+    positions and the sinks (4 KB each here)."""
+    most = (members - 1) * (window + sinks) * 4096
+    assert most < 40000000
+    assert shared_plan(window, sinks, prefix, members)[0].units == 0
+    assert shared_plan(0, 0, prefix, members)[0].units > 0
+    assert shared_plan(window, sinks, prefix, members, least=most + 1)[0].units == 0
+    assert shared_plan(window, sinks, prefix, members, least=most)[0].units > 0
+
+
+@pytest.mark.parametrize("members,prefix,window,sinks", [
+    (2, 131072, 64, 4), (16, 32768, 512, 4), (64, 65536, 4096, 0), (8, 131072, 70, 64)])
+def test_parts_of_what_is_seen_of_a_prefix(members, prefix, window, sinks):
+    """No more parts than there are fours of the tiles of 64 keys that a window and its sinks
+    lie in, and as many workgroups as for a prefix of that length without a window."""
+    p, data = shared_plan(window, sinks, prefix, members, least=0)
+    tiles = -(-window // 64) + 1 + -(-sinks // 64)
+    assert 1 <= p.parts <= -(-tiles // 4)
+    assert p.units <= 512 or p.parts == 1
+    # (a prefix that a window sees all of is cut as it is without one)
+    a, b = shared_plan(prefix, 0, prefix, members, least=0), shared_plan(0, 0, prefix, members, least=0)
+    assert abs(a[0].parts - b[0].parts) <= 1
+
+
+def test_a_window_longer_than_the_prefix_changes_nothing():
+    a, x = shared_plan(50000, 16, 8192, 64, longest=8704)
+    b, y = shared_plan(0, 0, 8192, 64, longest=8704)
+    assert a.units == b.units > 0 and x.tolist() == y.tolist() and a.tail == b.tail
