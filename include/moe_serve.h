@@ -231,7 +231,8 @@ moe_status moe_attn_share(const moe_kv_cache *kv, const moe_attn_config *cfg, in
 moe_status moe_attn_shared_workspace(const moe_kv_cache *kv, const moe_attn_config *cfg,
                                      const moe_attn_shared *plan, size_t *workspace,
                                      size_t *counters);
-/* As moe_attn_decode, of plan->batch sequences. */
+/* As moe_attn_decode, of plan->batch sequences; kv and cfg are those the plan was made for
+ * (a cfg for shorter sequences, fewer of them or other heads or windows is refused). */
 moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config *cfg,
                                   const moe_attn_shared *plan, int32_t layer, const void *q,
                                   int32_t dtype, int64_t token_stride, int64_t head_stride,

@@ -211,7 +211,8 @@ moe_status moe_attn_shared_workspace(const moe_kv_cache *kv, const moe_attn_conf
     const moe_status s = moe_attn_workspace(kv, c, 0, workspace, counters);
     if (s != MOE_OK) return s;
     if (!plan || plan->q_heads != c->q_heads || plan->kv_heads != kv->kv_heads ||
-        plan->head_dim != kv->head_dim || plan->slots < 0 || plan->batch < 1)
+        plan->head_dim != kv->head_dim || plan->slots < 0 || plan->batch < 1 ||
+        plan->batch > c->batch || plan->tail > c->longest)
         return MOE_ERR_INVALID_ARG;
     *workspace = round16(*workspace) + sizeof(float) * prefix_floats(*plan) +
                  sizeof(SharedTail) * plan->batch * kv->kv_heads * head_groups(*kv, *c);
@@ -229,7 +230,9 @@ moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config 
     if (s != MOE_OK) return s;
     if (!plan->data || !aligned(plan->data, 16) || plan->q_heads != c->q_heads ||
         plan->kv_heads != kv->kv_heads || plan->head_dim != kv->head_dim ||
-        plan->window != c->window || plan->sinks != c->sinks || plan->units < 0 || plan->tiles < 0)
+        plan->window != c->window || plan->sinks != c->sinks || plan->units < 0 ||
+        plan->tiles < 0 || plan->slots < 0 ||
+        plan->tail > c->longest)    // (more parts than the workspace has room for)
         return MOE_ERR_INVALID_ARG;
     // Nothing is read apart: as any decode.
     if (plan->units == 0)

@@ -1,5 +1,6 @@
 """Host-side checks of edges of the rotated append, decode over shared prefixes and
 sampling that the tests of their refusals and plans leave out (no GPU needed)."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -7,7 +8,7 @@ import subprocess
 import pytest
 
 from test_generate_abi import config, plan
-from test_serve_abi import cache
+from test_serve_abi import cache, status
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "sparse_moe_decode_router_amd", "csrc_serve")
@@ -85,3 +86,22 @@ def test_a_window_longer_than_the_prefix_changes_nothing():
     a, x = shared_plan(50000, 16, 8192, 64, longest=8704)
     b, y = shared_plan(0, 0, 8192, 64, longest=8704)
     assert a.units == b.units > 0 and x.tolist() == y.tolist() and a.tail == b.tail
+
+
+def test_a_plan_for_longer_sequences_is_refused():
+    """The workspace is that of the configuration: a plan of more positions would cut its
+    sequences into more parts than there is room for."""
+    c, long, short = cache(), config(longest=40000), config(longest=500)
+    _, p, _ = plan(c, long, [[0, 1]], [16], 4)
+    assert p.units > 0 and p.tail > 500
+    p.data = 4096
+    kv, at = ctypes.addressof(c), ctypes.addressof(p)
+    sizes = [ctypes.byref(ctypes.c_size_t()) for _ in range(2)]
+    for cfg, want in ((long, 0), (short, -1), (config(longest=40000, batch=3), -1)):
+        assert status("moe_attn_shared_workspace", kv, ctypes.addressof(cfg), at, *sizes) == want
+    for cfg in (short, config(longest=40000, batch=3)):
+        assert status("moe_attn_decode_shared", kv, ctypes.addressof(cfg), at, 0, 4096, 0, 1792, 128,
+                      4096, 4096, 4096, 4096, None) == -1
+    p.slots = -1
+    assert status("moe_attn_decode_shared", kv, ctypes.addressof(long), at, 0, 4096, 0, 1792, 128,
+                  4096, 4096, 4096, 4096, None) == -1
