@@ -174,7 +174,8 @@ moe_status moe_attn_validate(const moe_kv_cache *kv, const moe_attn_config *cfg)
  * or of prompt calls with up to `tokens` new tokens (tokens = 0: decode).  Counters
  * are zero before the first call that uses them, and every call leaves them
  * zero; the workspace carries nothing from call to call.  Calls that may run
- * at the same time need their own of both. */
+ * at the same time need their own of both; a call may be of several launches, so
+ * threads that share them on one stream make their calls one after the other. */
 moe_status moe_attn_workspace(const moe_kv_cache *kv, const moe_attn_config *cfg, int32_t tokens,
                               size_t *workspace, size_t *counters);
 

@@ -348,10 +348,12 @@ class PagedAttention:
         out = torch.empty(q.shape, dtype=q.dtype, device=kv.device)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=kv.device)
         stream = raw_stream(self._index)
-        w, c, _ = shared._space.get(stream)
-        check(self._lib.moe_attn_decode_shared(kv._ref, self._cfg, shared._ref, layer, q.data_ptr(),
-                                               DTYPES[q.dtype], ts, hs, out.data_ptr(),
-                                               lse.data_ptr(), w, c, stream), "decode_shared")
+        space = shared._space
+        with space.lock:
+            w, c, _ = space.get(stream)
+            check(self._lib.moe_attn_decode_shared(
+                kv._ref, self._cfg, shared._ref, layer, q.data_ptr(), DTYPES[q.dtype], ts, hs,
+                out.data_ptr(), lse.data_ptr(), w, c, stream), "decode_shared")
         return out, lse
 
     def prompt(self, layer: int, q, cu, max_new: Optional[int] = None):

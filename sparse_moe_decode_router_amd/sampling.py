@@ -80,9 +80,10 @@ class Sampler:
         if rows == 0:
             return tokens, logprobs
         stream = raw_stream(self._index)
-        w, c, _ = self._space.get(stream)
         filters = SamplingStruct(t, p, m, k, t_all, p_all, m_all, k_all)
-        check(self._lib.moe_sample(logits.data_ptr(), LOGIT_DTYPES[logits.dtype], step, rows,
-                                   self.vocab, u.data_ptr(), ctypes.byref(filters),
-                                   tokens.data_ptr(), logprobs.data_ptr(), w, c, stream), "sample")
+        with self._space.lock:
+            w, c, _ = self._space.get(stream)
+            check(self._lib.moe_sample(
+                logits.data_ptr(), LOGIT_DTYPES[logits.dtype], step, rows, self.vocab, u.data_ptr(),
+                ctypes.byref(filters), tokens.data_ptr(), logprobs.data_ptr(), w, c, stream), "sample")
         return tokens, logprobs

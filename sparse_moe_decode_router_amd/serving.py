@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -155,11 +156,13 @@ class StreamSpace:
     are ordered, so they share; calls on different streams never do (those of a
     stream that is gone stay for the next one of its handle).  A call
     that is being captured into a graph gets its own, which the graph keeps
-    (its counters are cleared within the graph, by a fill kernel)."""
+    (its counters are cleared within the graph, by a fill kernel).  A call of
+    several launches holds the lock from the first to the last: threads that use
+    one stream take turns, so that no launch of another comes between."""
 
     def __init__(self, device, workspace: int, counters: int):
         self.device, self.sizes = device, (max(16, workspace), max(16, counters))
-        self._by_stream = {}
+        self._by_stream, self.lock = {}, threading.Lock()
 
     def _make(self):
         w, c = self.sizes

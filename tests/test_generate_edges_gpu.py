@@ -1,5 +1,7 @@
 """Edges of the rotated append, decode over shared prefixes and sampling on the GPU."""
 import math
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -7,7 +9,7 @@ import torch
 
 import generate_util as gu
 import serve_util as su
-from sparse_moe_decode_router_amd import sampling
+from sparse_moe_decode_router_amd import attention, sampling
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +83,75 @@ def test_probabilities_of_hardly_any_weight(vocab, filters):
         # (all of the weight is the largest one's); one rounding to f32, 2^-40 before
         want = (x[:, at].double() - 1.0) / t
         assert float((drawn.cpu().double() / want - 1).abs().max()) <= 2.0 ** -24 + 2.0 ** -36
+
+
+# ---- Calls from several threads ---------------------------------------------
+
+class OneAtATime:
+    """Stands for the library: every call takes a while, and notices another one."""
+
+    def __init__(self):
+        self.inside, self.most, self.calls = 0, 0, 0
+
+    def call(self, *args):
+        self.inside += 1
+        self.most, self.calls = max(self.most, self.inside), self.calls + 1
+        time.sleep(0.002)
+        self.inside -= 1
+        return 0
+
+    moe_sample = moe_attn_decode_shared = call
+
+
+def from_threads(f, n=4, times=5):
+    def work():
+        with torch.cuda.device(0):
+            for _ in range(times):
+                f()
+    threads = [threading.Thread(target=work) for _ in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+
+
+def test_threads_on_one_stream_take_turns():
+    """Calls of two launches share a workspace on a stream: the second launch of one has to
+    follow its first."""
+    cache = gu.shared_cache([[0, 1]], [32], [40, 50], 2, 16, 64, BF, seed=31)
+    att = attention.PagedAttention(cache.gpu(), 4, 2, 64)
+    plan = att.share([[0, 1]], [32], least=0)
+    sampler = sampling.Sampler(2, 100)
+    q = torch.zeros((2, 4, 64), dtype=BF, device="cuda")
+    x, u = torch.zeros((2, 100), device="cuda"), torch.zeros(2, device="cuda")
+    for owner, f in ((sampler, lambda: sampler(x, u, top_p=0.9)),
+                     (att, lambda: att.decode_shared(0, q, plan))):
+        owner._lib = OneAtATime()
+        from_threads(f)
+        assert owner._lib.calls == 20 and owner._lib.most == 1
+
+
+def test_threads_get_their_own_results():
+    g = torch.Generator().manual_seed(80)
+    cache = gu.shared_cache([[0, 1, 2]], [2000], [2010, 2001, 2100], 2, 16, 128, BF, seed=81)
+    att = attention.PagedAttention(cache.gpu(), 14, 3, 2200)
+    plan = att.share([[0, 1, 2]], [2000], least=0)
+    sampler = sampling.Sampler(3, 20000)
+    qs = [torch.randn((3, 14, 128), generator=g).to(BF).cuda() for _ in range(4)]
+    xs = [(3 * torch.randn((3, 20000), generator=g)).cuda() for _ in range(4)]
+    us = [torch.rand(3, generator=g).cuda() for _ in range(4)]
+    pair = lambda i: att.decode_shared(0, qs[i], plan) + sampler(xs[i], us[i], top_p=0.9)  # noqa: E731
+    want = [pair(i) for i in range(4)]
+    torch.cuda.synchronize()
+    got, turn = [[] for _ in range(4)], iter(range(4))
+
+    def work():
+        i = next(turn)
+        for _ in range(20):
+            got[i].append(pair(i))
+    from_threads(work, 4, 1)
+    torch.cuda.synchronize()
+    for a, each in zip(want, got):
+        assert len(each) == 20
+        for b in each:
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
