@@ -75,7 +75,7 @@ moe_status moe_kv_append_rotated(const moe_kv_cache *kv, int32_t layer, const mo
     if (layer < 0 || layer >= kv->layers || q_heads < 1 || tokens < 0 || batch < 0 ||
         batch > kv->seqs || tokens > kMaxRows)
         return MOE_ERR_INVALID_ARG;
-    if (q_heads > 1 << 20) return MOE_ERR_UNSUPPORTED;
+    if (q_heads > 1 << 20 || tokens > kMaxGrid256) return MOE_ERR_UNSUPPORTED;   // (a token each)
     if (!cu && tokens != batch) return MOE_ERR_INVALID_ARG;
     if (tokens == 0 || batch == 0) return MOE_OK;
     if (!q || !k || !v || !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||

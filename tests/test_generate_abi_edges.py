@@ -7,6 +7,7 @@ import subprocess
 
 import pytest
 
+from sparse_moe_decode_router_amd import serving
 from test_generate_abi import config, plan
 from test_serve_abi import cache, status
 
@@ -105,3 +106,12 @@ def test_a_plan_for_longer_sequences_is_refused():
     p.slots = -1
     assert status("moe_attn_decode_shared", kv, ctypes.addressof(long), at, 0, 4096, 0, 1792, 128,
                   4096, 4096, 4096, 4096, None) == -1
+
+
+def test_rotated_append_refuses_more_workgroups_than_a_grid_has():
+    """Tokens of many heads take a workgroup of 256 threads each."""
+    turn, c = serving.RotaryStruct(4096, 0, 128, 0, 1.0), cache()
+    for tokens, want in ((1 << 24, -2), ((1 << 24) + 1, -1)):
+        assert status("moe_kv_append_rotated", ctypes.addressof(c), 0, ctypes.addressof(turn), 4096,
+                      1 << 17, 128, 1024, 4096, 4096, 0, 2304, 128, tokens, 4096, 4, None, 4096,
+                      None) == want
