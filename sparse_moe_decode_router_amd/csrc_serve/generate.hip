@@ -40,15 +40,22 @@ int64_t most_slices(int rows, int vocab, int most) {
     return std::max<int64_t>((int64_t)rows * least_slices(vocab, MOE_F32),
                              std::min<int64_t>((int64_t)rows * most, (int64_t)kSampleGrid + rows));
 }
+// The same of rows that have several slices: histograms and lists of the others (32 KB each)
+// do not leave LDS.
+int64_t most_of_several(int rows, int vocab, int most) {
+    return most_slices(least_slices(vocab, MOE_F32) > 1 ? rows : std::min(rows, kSampleGrid - 1), vocab,
+                       most);
+}
 struct SampleSpace {
     size_t hist, sums, list, slices, borders, listed, all;
 };
-SampleSpace sample_space(int64_t slices, int64_t draws, int rows) {
+// hists, lists: of those slices and draws how many have a histogram and a list there.
+SampleSpace sample_space(int64_t slices, int64_t hists, int64_t draws, int64_t lists, int rows) {
     SampleSpace s;
     s.hist = 0;
-    s.sums = s.hist + sizeof(uint64_t) * kSampleBins * slices;
+    s.sums = s.hist + sizeof(uint64_t) * kSampleBins * hists;
     s.list = s.sums + sizeof(double) * kSampleWaves * kSampleSlots * draws;
-    s.slices = s.list + sizeof(uint64_t) * kSampleList * draws;
+    s.slices = s.list + sizeof(uint64_t) * kSampleList * lists;
     s.borders = s.slices + sizeof(SampleSlice) * slices;
     s.listed = s.borders + sizeof(SampleBorder) * rows;
     s.all = s.listed + sizeof(int32_t) * draws;
@@ -138,7 +145,9 @@ moe_status moe_sample_workspace(int32_t rows, int32_t vocab, size_t *workspace, 
     if (rows < 1 || vocab < 1 || !workspace || !counters) return MOE_ERR_INVALID_ARG;
     if (rows > kMaxRows / kSampleMaxDraws || vocab > kMaxVocab) return MOE_ERR_UNSUPPORTED;
     *workspace = sample_space(most_slices(rows, vocab, kSampleMaxSlices),
-                              most_slices(rows, vocab, kSampleMaxDraws), rows).all;
+                              most_of_several(rows, vocab, kSampleMaxSlices),
+                              most_slices(rows, vocab, kSampleMaxDraws),
+                              most_of_several(rows, vocab, kSampleMaxDraws), rows).all;
     *counters = sizeof(uint32_t) * (size_t)rows;
     return MOE_OK;
 }
@@ -164,8 +173,9 @@ moe_status moe_sample(const void *x, int32_t dtype, int64_t row_stride, int32_t 
     SampleArgs a = {};
     a.slices_n = sample_slices(rows, vocab, dtype, kSampleMaxSlices);
     a.draws = sample_slices(rows, vocab, dtype, kSampleMaxDraws);
-    const SampleSpace space =
-        sample_space((int64_t)a.slices_n * rows, (int64_t)a.draws * rows, rows);
+    const int64_t slices = (int64_t)a.slices_n * rows, draws = (int64_t)a.draws * rows;
+    const SampleSpace space = sample_space(slices, a.slices_n > 1 ? slices : 0, draws,
+                                           a.draws > 1 ? draws : 0, rows);
     char *ws = (char *)workspace;
     a.x = x;
     a.u = u;

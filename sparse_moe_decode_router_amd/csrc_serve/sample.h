@@ -78,10 +78,10 @@ struct SampleArgs {
     int32_t *token;
     float *logprob;
     SampleSlice *slices;      // [rows][slices]
-    uint64_t *hist;           // [rows][slices][kSampleBins]: count << 44 | weights
+    uint64_t *hist;           // [rows][slices][kSampleBins]: count << 44 | weights (of one: none)
     SampleBorder *borders;    // [rows]
     double *sums;             // [rows][draws][waves][kSampleSlots] (plain: the sum, the maximum)
-    uint64_t *list;           // [rows][draws][kSampleList]
+    uint64_t *list;           // [rows][draws][kSampleList] (of one: none)
     int32_t *listed;          // [rows][draws]
     uint32_t *counters;       // [rows]: arrivals
     int64_t stride;           // of rows, in elements

@@ -115,3 +115,15 @@ def test_rotated_append_refuses_more_workgroups_than_a_grid_has():
         assert status("moe_kv_append_rotated", ctypes.addressof(c), 0, ctypes.addressof(turn), 4096,
                       1 << 17, 128, 1024, 4096, 4096, 0, 2304, 128, tokens, 4096, 4, None, 4096,
                       None) == want
+
+
+@pytest.mark.parametrize("vocab", [1000, 32000, 65000])
+def test_sampling_workspace_of_many_rows(vocab):
+    """A row that one workgroup takes keeps its histogram and its list in LDS: beyond the 511
+    rows that may have several, a row adds its sums alone, below 1 KB."""
+    def size(rows):
+        w, n = ctypes.c_size_t(), ctypes.c_size_t()
+        assert status("moe_sample_workspace", rows, vocab, ctypes.byref(w), ctypes.byref(n)) == 0
+        return w.value
+    assert size(4096) - size(511) <= 1024 * (4096 - 511)
+    assert size(511) <= 2 * 32768 * 1023 + 1024 * 1023

@@ -155,3 +155,17 @@ def test_threads_get_their_own_results():
         assert len(each) == 20
         for b in each:
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("vocab", [1500, 20003])
+def test_fewer_rows_than_a_sampler_is_for(vocab):
+    """Calls of all sizes on one workspace: few rows are cut into slices, many are not."""
+    g = torch.Generator().manual_seed(90)
+    x = torch.randn((1100, vocab), generator=g) * 3
+    u = torch.rand(1100, generator=g)
+    sampler, xd, ud = sampling.Sampler(1100, vocab), x.cuda(), u.cuda()
+    for rows in (1100, 1, 511, 512, 60, 1100):
+        got = sampler(xd[:rows], ud[:rows], top_p=0.9)
+        torch.cuda.synchronize()
+        some = slice(max(0, rows - 40), rows)
+        gu.check_sample([t[some] for t in got], x[some], u[some], top_p=0.9)
