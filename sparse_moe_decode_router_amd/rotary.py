@@ -32,6 +32,9 @@ def frequencies(dim: int, base: float = 10000.0, factor: float = 1.0, original: 
     return f * (stay + (1 - stay) / factor)
 
 
+F32_MAX = torch.finfo(torch.float32).max
+
+
 class Rotary:
     """frequencies [rot / 2]: radians a position of each pair.  The dimensions
     first .. first + rot - 1 of a head are turned (both multiples of 16), pair j
@@ -47,7 +50,8 @@ class Rotary:
         require(bool(f.isfinite().all()), "frequencies: finite ones are needed")
         require(isinstance(first, int) and first >= 0 and first % 16 == 0,
                 f"first {first!r}: a multiple of 16 is needed")
-        require(math.isfinite(amplitude), f"amplitude {amplitude!r}")
+        require(math.isfinite(amplitude) and abs(amplitude) <= F32_MAX,
+                f"amplitude {amplitude!r}: a finite number of 32 bits is needed")
         self.turns = (f / (2 * math.pi)).to(device)
         self.device, self.first, self.rot = self.turns.device, first, 2 * f.numel()
         self.last = first + self.rot

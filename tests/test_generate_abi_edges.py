@@ -7,7 +7,8 @@ import subprocess
 
 import pytest
 
-from sparse_moe_decode_router_amd import serving
+from sparse_moe_decode_router_amd import rotary, serving
+from sparse_moe_decode_router_amd.binding import MoEError
 from test_generate_abi import config, plan
 from test_serve_abi import cache, status
 
@@ -127,3 +128,12 @@ def test_sampling_workspace_of_many_rows(vocab):
         return w.value
     assert size(4096) - size(511) <= 1024 * (4096 - 511)
     assert size(511) <= 2 * 32768 * 1023 + 1024 * 1023
+
+
+def test_amplitudes_are_held_in_32_bits():
+    """(A larger one used to become infinite.)"""
+    f = rotary.frequencies(64)
+    rotary.Rotary(f, amplitude=-3.4e38, device="cpu")
+    for bad in (3.5e38, -1e300):
+        with pytest.raises(MoEError):
+            rotary.Rotary(f, amplitude=bad, device="cpu")
