@@ -27,6 +27,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from .binding import MoEError
+from .rotary import Rotary
 from .serving import (DTYPES, AttnConfig, Cache, SharedPlan, StreamSpace, check, current_device,
                       lib, raw_stream, require, tensor)
 
@@ -198,6 +199,8 @@ class PagedKV:
                                f"{tuple(cu.shape)}")
         if not 0 <= layer < self.layers:
             raise MoEError(f"layer {layer} of {self.layers}")
+        if not isinstance(rotary, Rotary):
+            raise MoEError(f"rotary: a Rotary is needed, got {type(rotary).__name__}")
         if rotary.device != dev or rotary.last > dim:
             raise MoEError(f"rotary: on {rotary.device}, up to dimension {rotary.last}; heads are "
                            f"on {dev} and of {dim}")

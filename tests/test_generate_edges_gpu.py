@@ -9,7 +9,8 @@ import torch
 
 import generate_util as gu
 import serve_util as su
-from sparse_moe_decode_router_amd import attention, sampling
+from sparse_moe_decode_router_amd import attention, rotary, sampling
+from sparse_moe_decode_router_amd.binding import MoEError
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +170,18 @@ def test_fewer_rows_than_a_sampler_is_for(vocab):
         torch.cuda.synchronize()
         some = slice(max(0, rows - 40), rows)
         gu.check_sample([t[some] for t in got], x[some], u[some], top_p=0.9)
+
+
+# ---- Rotated append: refusals -----------------------------------------------
+
+def rotated_parts():
+    kv = su.HostCache([20, 30], 2, 16, 64, BF, seed=23).gpu()
+    y = torch.zeros((2, 8, 64), dtype=BF, device="cuda")
+    return kv, y[:, :4], y[:, 4:6], y[:, 6:], rotary.Rotary(rotary.frequencies(64))
+
+
+def test_what_is_no_rotary_is_refused():
+    kv, q, k, v, turn = rotated_parts()
+    for bad in (None, turn.turns, turn.struct, rotary.frequencies(64)):
+        with pytest.raises(MoEError):
+            kv.append_rotated(0, q, k, v, bad)
