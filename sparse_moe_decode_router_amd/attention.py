@@ -63,6 +63,15 @@ def _rows(t, name, heads, dim, dtypes, device) -> Tuple[int, int]:
                    "aligned, are needed")
 
 
+def _meet(a, b) -> bool:
+    """Whether the memory from the first to the last element of either meets."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    ends = [t.data_ptr() + t.element_size() *
+            (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) for t in (a, b)]
+    return a.data_ptr() < ends[1] and b.data_ptr() < ends[0]
+
+
 class PagedKV:
     """data [layers, 2, pages, kv_heads, page, head_dim] (bf16, fp16 or e4m3; keys
     at 0, values at 1), tables [seqs, cols] i32 (-1: no page), lengths [seqs]
@@ -167,7 +176,8 @@ class PagedKV:
                        out=None):
         """append() of keys turned by their positions, with the queries q [tokens,
         q_heads, head_dim] of the same tokens, which come back turned by the same
-        (in out, or a new tensor; out may be q where q is contiguous).  rotary: a
+        (in out, or a new tensor; out may be q where q is contiguous, and meets no
+        other memory of q, k or v).  rotary: a
         rotary.Rotary on the cache's device.  The queries of a sequence of length 0
         come back as they are; rows that cu leaves out are not written."""
         if current_device() != self._index:
@@ -209,6 +219,9 @@ class PagedKV:
         else:
             tensor(out, "out", dtype, q.shape, dev)
             require(out.data_ptr() % 16 == 0, "out: 16-byte alignment is needed")
+            own = out.data_ptr() == q.data_ptr() and q.is_contiguous()
+            for t, name in ((q, "q"), (k, "k"), (v, "v")):
+                require(not _meet(out, t) or (own and t is q), f"out: overlaps {name}")
         check(self._lib.moe_kv_append_rotated(
             self._ref, layer, rotary._ref, q.data_ptr(), qts, qhs, q_heads, k.data_ptr(), v_at,
             DTYPES[dtype], ts, hs, tokens, None if cu is None else cu.data_ptr(),

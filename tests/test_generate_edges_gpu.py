@@ -185,3 +185,27 @@ def test_what_is_no_rotary_is_refused():
     for bad in (None, turn.turns, turn.struct, rotary.frequencies(64)):
         with pytest.raises(MoEError):
             kv.append_rotated(0, q, k, v, bad)
+
+
+def test_results_over_other_operands_are_refused():
+    """Workgroups would read queries, keys and values that others have written over.  The
+    queries' own memory is theirs to write, and so is what is behind or before them all."""
+    kv, q, k, v, turn = rotated_parts()
+    flat = torch.zeros(4 * 4 * 64, dtype=BF, device="cuda")
+    at = lambda i: flat[64 * i:64 * (i + 8)].view(2, 4, 64)  # noqa: E731
+    small = at(0)[:, :2]
+    y = q.new_zeros((2, 12, 64))
+    for args, out in (((at(1), k, v), at(0)), ((q, at(4)[:, :2], v), at(0)),
+                      ((q, small, small), at(0)), ((q, k, small), at(0)),
+                      ((y[:, :4], y[:, 4:6], y[:, 6:8]), y.view(6, 4, 64)[1:3])):
+        with pytest.raises(MoEError):
+            kv.append_rotated(0, *args, turn, out=out)
+    assert kv.append_rotated(0, at(0), k, v, turn, out=at(0)).data_ptr() == at(0).data_ptr()
+    kv.append_rotated(0, at(0), k, v, turn, out=at(8))
+    kv.append_rotated(0, q, k, v, turn, out=at(0))
+    # one token: its keys and values are beside its queries
+    one = y[:1]
+    cu = torch.tensor([0, 1, 1], dtype=torch.int32, device="cuda")
+    kv.append_rotated(0, one[:, :4], one[:, 4:6], one[:, 6:8], turn, cu, out=one[:, 8:])
+    kv.append_rotated(0, one[:, :4], one[:, 4:6], one[:, 6:8], turn, cu, out=one[:, :4])
+    torch.cuda.synchronize()
