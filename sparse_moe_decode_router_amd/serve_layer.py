@@ -24,6 +24,7 @@ from . import binding, synth
 from .attention import PagedAttention, PagedKV
 from .rotary import Rotary, frequencies
 from .sampling import Sampler
+from .serving import require
 from .w4 import W4Linear
 
 
@@ -56,7 +57,7 @@ class ServeLayer:
         self.kv = PagedKV.empty(1, pages, kv_heads, page, head_dim, seqs, cols, cache,
                                 k_scale=scale, v_scale=scale)
         self.attention = PagedAttention(self.kv, q_heads, seqs, cols * page, window, sinks)
-        self.rotary = rotary
+        self.rotary, self.vocab = rotary, vocab
         if vocab:
             g = torch.Generator(device="cuda").manual_seed(seed + 2)
             self.embedding = torch.randn((vocab, hidden), generator=g, device="cuda",
@@ -146,8 +147,19 @@ def generate(steps=8, cache=torch.bfloat16, prompts=(300, 17, 120, 64), continua
     """Samples `continuations` continuations of each prompt (of random tokens): the
     prompts, a fork for each further continuation, then single tokens of all of
     them, whose prompts are read once where that pays (least: see
-    attention.share).  Returns the layer, tokens [prompts, continuations, steps],
-    the logarithms of their probabilities and microseconds per step."""
+    attention.share).  layer: a ServeLayer with positions and that vocabulary whose
+    cache holds nothing yet (None: one is made).  Returns the layer, tokens [prompts,
+    continuations, steps], the logarithms of their probabilities and microseconds
+    per step."""
+    for name, v in (("steps", steps), ("continuations", continuations), ("vocab", vocab),
+                    *(("prompts", p) for p in (*prompts, len(prompts)))):
+        require(isinstance(v, int) and v >= 1, f"{name}: integers from 1 on are needed, got {v!r}")
+    if layer is not None:
+        require(layer.rotary is not None and layer.vocab == vocab,
+                f"layer: positions and a vocabulary of {vocab} are needed")
+        require(len(prompts) * continuations <= layer.kv.seqs,
+                f"{len(prompts) * continuations} sequences, and the layer has {layer.kv.seqs}")
+        require(not bool(layer.kv.lengths.any()), "layer: its cache holds sequences")
     ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
     n, c = len(prompts), continuations
     if layer is None:

@@ -4,10 +4,12 @@ import ctypes
 import os
 import shutil
 import subprocess
+import types
 
 import pytest
+import torch
 
-from sparse_moe_decode_router_amd import rotary, serving
+from sparse_moe_decode_router_amd import rotary, serve_layer, serving
 from sparse_moe_decode_router_amd.binding import MoEError
 from test_generate_abi import config, plan
 from test_serve_abi import cache, status
@@ -137,3 +139,18 @@ def test_amplitudes_are_held_in_32_bits():
     for bad in (3.5e38, -1e300):
         with pytest.raises(MoEError):
             rotary.Rotary(f, amplitude=bad, device="cpu")
+
+
+@pytest.mark.parametrize("kw", [
+    dict(steps=0), dict(continuations=0), dict(prompts=()), dict(prompts=(5, 0)), dict(vocab=0),
+    dict(layer=dict(vocab=501)), dict(layer=dict(vocab=0)), dict(layer=dict(rotary=None)),
+    dict(layer=dict(seqs=5)), dict(layer=dict(lengths=[0, 0, 7, 0, 0, 0]))], ids=str)
+def test_generate_refuses(kw):
+    """(Tokens beyond a layer's embedding used to be looked up in it, and sequences that a cache
+    held already were taken for parts of the prompts.)"""
+    own = {**dict(vocab=500, rotary=1, seqs=6, lengths=[0] * 6), **kw.pop("layer", {})}
+    layer = types.SimpleNamespace(rotary=own["rotary"], vocab=own["vocab"], kv=types.SimpleNamespace(
+        seqs=own["seqs"], lengths=torch.tensor(own["lengths"])))
+    with pytest.raises(MoEError):
+        serve_layer.generate(**{**dict(steps=4, prompts=(70, 33), continuations=3, vocab=500,
+                                       layer=layer), **kw})
