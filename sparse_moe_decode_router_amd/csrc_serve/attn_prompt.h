@@ -666,7 +666,11 @@ __device__ __forceinline__ void attn_prompt(PromptLds<D> &s, int block) {
                     // Weights are rounded to 16 bits for the second product (their
                     // sum is not): the output's error grows from 0.0016 to 0.0022
                     // in bf16.  The pair that decode uses would double that
-                    // product, which with the first takes 45% of the time.
+                    // product, which with the first takes 45% of the time.  Of shared
+                    // prefixes, with pairs: 64 sequences over 8192 45.7 us instead of
+                    // 39.4 (error 0.0017, not 0.0022), four groups of 16 in e4m3 103.5
+                    // instead of 85.7 (0.0017, 0.0020), 32 over 131072 in fp16 71.7
+                    // instead of 58.5 (0.00021, 0.00025).
                     l += p0 + p1;
                     p[2 * u + (r >> 3)][(r & 7) >> 1] = T::pack(p0, p1);
                 }

@@ -52,7 +52,8 @@ __device__ __forceinline__ void cos_sin(double turns, float *c, float *s) {
     const float x = 6.2831853071795865f * (float)(turns - 0.25 * quarter);   // up to pi / 4
     const int k = (int)(quarter - 4.0 * __builtin_floor(0.25 * quarter));    // 0 .. 3
     const float y = x * x;
-    // Power series: what is left out is below 2^-28 of the result.
+    // Power series: what is left out is below 2^-28 of the sine and 2^-24.7 of the cosine
+    // (x^10 / 10! at pi / 4), as much as a rounding.
     const float sn = x + x * y * (-1.f / 6 + y * (1.f / 120 + y * (-1.f / 5040 + y * (1.f / 362880))));
     const float cs = 1.f + y * (-0.5f + y * (1.f / 24 + y * (-1.f / 720 + y * (1.f / 40320))));
     const float a = k & 1 ? sn : cs, b = k & 1 ? cs : sn;

@@ -545,9 +545,13 @@ __device__ __forceinline__ SampleBorder find_border(const SampleArgs &a, const S
         top = 0;
         above = 0;
     } else if (f.by_p) {
-        // What any sum of weights may be off by: each by 2^-23 for its power and for its 24
-        // bits, and for its place and the scale, rounded to 24 bits both (ln 2 / 64 a
-        // place; more, where they are off by many).
+        // What a border may be off by.  A weight is off by e < 2^-20.1: the exponent, formed
+        // near 24, is rounded to a multiple of 2^-19 (2^-20.5 of the weight), its power to 23
+        // bits, and that cut off to 24 bits.  Where the weights before a border are p of all
+        // and off by e one way, and the others the other way, they less p times the sum of
+        // all are off by 2 e p (1 - p) of that sum, at most 2^-21.1 (the sum errs with
+        // them); the margin is (1 + p) 2^-21.  Then for a value's place and the scale,
+        // rounded to 24 bits both (ln 2 / 64 a place; more, where they are off by many).
         const double off = all_mass * (0x1p-21 + fabs((double)place) * 0x1p-24 * 0.035) +
                            all_far * 0x1p-24 * 0.035;
         const double least = f.top_p * (lo - off) - off, most = f.top_p * (hi + off) + off;

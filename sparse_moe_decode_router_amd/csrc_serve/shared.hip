@@ -40,11 +40,6 @@ constexpr int kSharedTiles = 4, kSharedParts = 128;
 // it: a few microseconds are lost on either side of the border (one by one 29 MB of 8
 // sequences took 13 to 21, 60 MB 17 to 24, by how many parts their rows were cut into).
 constexpr int64_t kSharedLeast = 40000000;
-// Units behind the prefixes that a call aims at, for each compute unit: tails are short, and
-// a sequence's is best taken by one workgroup (in a launch of their own, 64 tails of up to
-// 512, 56 heads on 8: 1, 2
-// and 4 a compute unit 63.0, 63.6 and 64.7 us; up to 1000 in e4m3: 100, 104, 107).
-
 // What the two kinds of work take on the whole chip, us: a first tile of either, 128 rows
 // times 64 keys for each dimension, a byte.
 constexpr double kStartUs = 7., kPrefixUs = 4.1e-5, kByteUs = 2e-7;
@@ -242,7 +237,11 @@ moe_status moe_attn_decode_shared(const moe_kv_cache *kv, const moe_attn_config 
     if ((s = moe_attn_workspace(kv, c, 0, &decode_bytes, &counter_bytes)) != MOE_OK) return s;
     if (!workspace || !counters) return MOE_ERR_WORKSPACE;
     AttnArgs a = attn_args(*kv, *c, layer);
-    a.split = std::max(1, std::min(decode_split(*kv, *c, plan->tail), kPlanCus / (a.kv_heads * a.head_groups)));
+    // One unit behind the prefixes for each compute unit: tails are short, and prefixes are in the
+    // same launch (one a compute unit, half and twice as many, us: 64 tails of up to 512, 56
+    // heads on 8: 39.9, 39.4 and 40.9; 4 groups of 16 up to 1000, e4m3: 85.3, 85.5 and 85.4).
+    a.split = std::max(1, std::min(decode_split(*kv, *c, plan->tail),
+                                   kPlanCus / (a.kv_heads * a.head_groups)));
     const int64_t grid = ((int64_t)a.split + plan->batch) * a.kv_heads * a.head_groups;
     if (grid + plan->units > kMaxGrid256) return MOE_ERR_UNSUPPORTED;
     int cus;

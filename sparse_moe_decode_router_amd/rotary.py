@@ -1,7 +1,9 @@
 """Rotary positions: which dimensions of a head are turned, and how fast.
 
 ``frequencies`` gives the usual geometric ones, stretched for long contexts or
-not; ``Rotary`` keeps any on a device for ``PagedKV.append_rotated``.
+not; ``Rotary`` keeps any on a device for ``PagedKV.append_rotated``.  Models differ in
+how they stretch: one that does it in another way than ``frequencies`` says has its
+own frequencies given to ``Rotary``.
 """
 from __future__ import annotations
 
@@ -19,8 +21,11 @@ def frequencies(dim: int, base: float = 10000.0, factor: float = 1.0, original: 
     """[dim / 2] f64, in radians a position: base^(-2 j / dim).  factor: by how
     much a context longer than the `original` one stretches them.  Pairs that turn
     at least `fast` times within the original context stay, those that turn at most
-    `slow` times are divided by the factor, in between it is in proportion to the
-    turns; original 0: all are divided."""
+    `slow` times are divided by the factor, and in between the frequency is a mean of
+    the two in proportion to the turns (the pair's turns less `slow`, over `fast` less
+    `slow`).  Others go in proportion to the pair's index between the two ends, which
+    at slow 1 and fast 32 gives up to four times other frequencies: those are to be
+    computed by the caller.  original 0: all are divided."""
     require(isinstance(dim, int) and dim > 0 and dim % 2 == 0, f"dim {dim!r}: an even number is needed")
     require(base > 0 and factor > 0 and original >= 0 and slow < fast,
             "base and factor above 0, an original context, and slow < fast are needed")
