@@ -92,6 +92,10 @@ moe_status moe_kv_append_rotated(const moe_kv_cache *kv, int32_t layer, const mo
     if ((s = check_strides(q_token_stride, q_head_stride, q_heads, kv->head_dim)) != MOE_OK) return s;
     if ((s = check_strides(token_stride, head_stride, kv->kv_heads, kv->head_dim)) != MOE_OK)
         return s;
+    // In place only where every result has its own query's place.
+    if (q_out == q && ((tokens > 1 && q_token_stride != (int64_t)q_heads * kv->head_dim) ||
+                       (q_heads > 1 && q_head_stride != kv->head_dim)))
+        return MOE_ERR_INVALID_ARG;
     int cus;
     if ((s = compute_units(&cus)) != MOE_OK) return s;
     RotaryArgs a = {};

@@ -154,3 +154,18 @@ def test_generate_refuses(kw):
     with pytest.raises(MoEError):
         serve_layer.generate(**{**dict(steps=4, prompts=(70, 33), continuations=3, vocab=500,
                                        layer=layer), **kw})
+
+
+@pytest.mark.parametrize("kw,in_place", [
+    (dict(), False), (dict(qts=14 * 128), True), (dict(qts=14 * 128, qhs=256), False),
+    (dict(tokens=1, batch=1), True), (dict(tokens=1, batch=1, qts=0), True),
+    (dict(q_heads=1, qhs=0, qts=128), True), (dict(q_heads=1, qhs=0, qts=256), False)], ids=str)
+def test_rotated_append_in_place_needs_queries_without_gaps(kw, in_place):
+    """(Here there is no device: what is not refused for its arguments gets as far as that.)"""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    turn, c = serving.RotaryStruct(4096, 0, 128, 0, 1.0), cache()
+    args = dict(kv=ctypes.addressof(c), layer=0, rotary=ctypes.addressof(turn), q=4096, qts=2304,
+                qhs=128, q_heads=14, k=8192, v=8192, dtype=0, ts=2304, hs=128, tokens=2, cu=None,
+                batch=2, granted=None, out=4096, stream=None)
+    assert status("moe_kv_append_rotated", *{**args, **kw}.values()) == (-3 if in_place else -1)
