@@ -20,16 +20,18 @@
 //                   of a slice) that holds the drawn one; and that.
 // Bins are monotonic in the value and their counts exact, so that the list holds the
 // border whatever the weights' 20 bits missed (the margin of the search covers
-// that).  Where the list would be too long (thousands of equal logits at the border),
-// the passes go over the row instead.
+// that).  Where the list would be too long (thousands of equal logits at the border, or a
+// top_p within 2e-5 of 1, whose border is among nearly all tokens), the passes go over the
+// row instead, by one workgroup: for one row of 163840 282 us instead of 21.
 //   k_sample_plain  rows without filters: each segment's maximum and sum, and the last
 //                   slice draws.  One launch.
 //
 // What bounds it: few rows are a chain of latencies, each phase a barrier and a read of
 // what other slices left (one row of 163840, bf16: 19 us a launch, most of it after the
 // slices' passes of 2 and 4 us); many rows are bound by the vector unit, the 64-bit
-// exponentials above all (512 rows of 100003, top-p: 54 us to scan and 99 to draw, where
-// reading the logits takes 20).  Eight rows of 32003 without filters take 10 us.
+// exponentials above all (512 rows of 100003, top-p: 53 us to scan and 98 to draw, where
+// reading the logits takes 20).  Eight rows of 32003 without filters take 10 us, 64 of 163840
+// 25.  No registers are spilled but one, of the draw from f32.
 //   Histograms of 64-bit integers in LDS, because the order of additions must not change
 //   a sum, and because the borders then come from one pass instead of one a digit.
 //   More slices shorten the passes and lengthen what their last one reads: nine at most

@@ -7,9 +7,9 @@
 // rows instead of once for each member.  The others decode what each sequence has behind
 // the prefix.  The second launch joins the partial results of both.
 //
-// Device time of the two launches, us: 64 sequences, 56 heads on 8, prefix 8192 and tails up to 512: 40
-// and 7; four groups of 16, e4m3, prefixes up to 32768 and tails up to 1000: 85 and 8; 32
-// sequences, 14 heads on 2, prefix 131072 and tails up to 300: 52 and 12.  Prefixes are bound
+// Device time of the two launches, us: 64 sequences, 56 heads on 8, prefix 8192 and tails up
+// to 512: 38 and 7; four groups of 16, e4m3, prefixes up to 32768 and tails up to 1000: 83 and
+// 8; 32 sequences, 14 heads on 2, prefix 131072 and tails up to 300: 51 and 12.  Prefixes are bound
 // as prompts are (vector and matrix instructions), after some 7 us to their first keys;
 // tails by memory.  As launches of their own, each on the whole chip, they took 29 + 24,
 // 66 + 24 and 49 + 8.
