@@ -341,8 +341,9 @@ class PagedAttention:
         most; prefix: as many numbers of positions, from the first on, whose keys
         and values are the same in all of a group.  After fork that is what the
         parent had; its last page, if in part, may be counted in or not.  least:
-        bytes of keys and values of a layer that sharing has to spare, else
-        sequences are decoded one by one (None: what it takes to be faster)."""
+        bytes of keys and values of a layer that sharing has to spare (of a prefix
+        what a window and its sinks see at most), else sequences are decoded one by one
+        (None: about what it takes to be faster)."""
         return SharedPrefix(self, groups, prefix, self.batch if batch is None else batch, least)
 
     def decode_shared(self, layer: int, q, shared: "SharedPrefix"):

@@ -52,8 +52,9 @@ class Sampler:
 
     def __call__(self, logits, u, temperature=None, top_k=None, top_p=None, min_p=None):
         """logits [rows, vocab] (bf16, fp16 or f32; rows contiguous), u [rows] f32 in
-        [0, 1).  temperature, top_p, min_p: numbers, or f32 tensors [rows]; top_k:
-        an integer or an i32 tensor [rows]; None: 1, none, none, none.
+        [0, 1) (from 1 on: the last kept token).  temperature, top_p, min_p: numbers, or
+        f32 tensors [rows]; top_k: an integer or an i32 tensor [rows]; None: 1, none,
+        none, none.
         Temperature 0: the first largest logit.  Returns (tokens [rows] i32, the
         logarithms of the probabilities that they were drawn with [rows] f32); a
         row without anything above -inf gives -1 and -inf."""
