@@ -221,7 +221,7 @@ class PagedKV:
             require(out.data_ptr() % 16 == 0, "out: 16-byte alignment is needed")
             own = out.data_ptr() == q.data_ptr() and q.is_contiguous()
             for t, name in ((q, "q"), (k, "k"), (v, "v")):
-                require(not _meet(out, t) or (own and t is q), f"out: overlaps {name}")
+                require(not _meet(out, t) or (own and name == "q"), f"out: overlaps {name}")
         check(self._lib.moe_kv_append_rotated(
             self._ref, layer, rotary._ref, q.data_ptr(), qts, qhs, q_heads, k.data_ptr(), v_at,
             DTYPES[dtype], ts, hs, tokens, None if cu is None else cu.data_ptr(),

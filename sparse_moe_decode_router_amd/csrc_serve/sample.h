@@ -739,10 +739,10 @@ __device__ __forceinline__ int first_place(Lds &s, bool holds, bool some) {
 }
 
 // The token of a row whose sums up to each segment are in s.seg: the segment, then the
-// place in it.  A thread takes a few chunks next to each other.  weight_of: of any of the
-// row's values, weight(x): as it is kept, and is_kept(x, index).  some: whether segment `threadIdx.x` holds any weight.  (Not what the
-// sums up to it say: two that differ by nothing may be off by a rounding, and a weight
-// may be too small to show in them.)
+// place in it.  A thread takes a few chunks next to each other.  weight_of(x) of any of the
+// row's values, weight(x) as it is kept, and is_kept(x, index).  some: whether segment
+// `threadIdx.x` holds any weight.  (Not what the sums up to it say: two that differ by
+// nothing may be off by a rounding, and a weight may be too small to show in them.)
 template <int Type, class Lds, class Weight, class Is>
 __device__ __forceinline__ void draw_token(const SampleArgs &a, int row, const SampleRow &f,
                                            Lds &s, bool some, const SampleWeight &weight_of,

@@ -193,10 +193,11 @@ def test_results_over_other_operands_are_refused():
     kv, q, k, v, turn = rotated_parts()
     flat = torch.zeros(4 * 4 * 64, dtype=BF, device="cuda")
     at = lambda i: flat[64 * i:64 * (i + 8)].view(2, 4, 64)  # noqa: E731
-    small = at(0)[:, :2]
+    small, small2 = at(0)[:, :2], torch.zeros((2, 2, 64), dtype=BF, device="cuda")
     y = q.new_zeros((2, 12, 64))
     for args, out in (((at(1), k, v), at(0)), ((q, at(4)[:, :2], v), at(0)),
                       ((q, small, small), at(0)), ((q, k, small), at(0)),
+                      ((small2, small2, v), small2), ((small2, k, small2), small2),
                       ((y[:, :4], y[:, 4:6], y[:, 6:8]), y.view(6, 4, 64)[1:3])):
         with pytest.raises(MoEError):
             kv.append_rotated(0, *args, turn, out=out)
